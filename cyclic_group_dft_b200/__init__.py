@@ -15,6 +15,11 @@ Usage::
     dx = hb.backward_dx(dy)          # dy [N, Cout, G] -> dx [N, Cin, G]
     dw, dbias = hb.backward_dw(x, dy)  # fp32 [Cout, Cin, G], [Cout]
 
+    # around the layers, on the same [N, C, G] tensors (each with its gradient):
+    y, r = eq.eqlin_add_rmsnorm(x, residual, weight)          # y8, scale, r = eq.eqlin_add_rmsnorm_fp8(...)
+    q = eq.eqlin_rope(q, positions, heads=3, sections=(8, 8))
+    o, lse = eq.eqlin_attention_forward(q, k, v, heads=3, q_offsets=offsets, k_offsets=offsets)
+
 The functions with the C ABI's names (eqlin_prepare_weights, eqlin_forward,
 eqlin_destroy, ...) are the same calls with explicit arguments.
 
@@ -70,13 +75,28 @@ _EXPORTS = (
     "eqlin_mlp_query",
 )
 
-__all__ = list(_EXPORTS) + ["prepare", "workloads"]
+# the handle-free operators of a transformer block (norm, rotary positions, attention)
+_BLOCK_EXPORTS = (
+    "eqlin_add_rmsnorm",
+    "eqlin_add_rmsnorm_fp8",
+    "eqlin_rmsnorm_backward",
+    "eqlin_rmsnorm_backward_workspace_size",
+    "eqlin_rope",
+    "eqlin_attention_forward",
+    "eqlin_attention_backward",
+)
+
+__all__ = list(_EXPORTS) + list(_BLOCK_EXPORTS) + ["prepare", "workloads"]
 
 
 def __getattr__(name: str):
     if name in _EXPORTS or name == "prepare":
         capi = importlib.import_module("._capi", __name__)
         value = capi.eqlin_prepare_weights if name == "prepare" else getattr(capi, name)
+        globals()[name] = value
+        return value
+    if name in _BLOCK_EXPORTS:
+        value = getattr(importlib.import_module("._block", __name__), name)
         globals()[name] = value
         return value
     if name == "workloads":

@@ -8,6 +8,7 @@ one to run).
 """
 from __future__ import annotations
 
+import concurrent.futures
 import glob
 import os
 import subprocess
@@ -18,11 +19,12 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libeqlin.so")
+OBJ = os.path.join(PKG, "_build")   # one object file and one dependency list per source
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
     "-lineinfo", "-O3", "-std=c++17",
-    "-shared", "-Xcompiler", "-fPIC,-fvisibility=hidden",
+    "-Xcompiler", "-fPIC,-fvisibility=hidden",
     "--expt-relaxed-constexpr",
 ]
 
@@ -48,15 +50,42 @@ def nvcc() -> str:
     return cand if os.path.exists(cand) else "nvcc"
 
 
+def _object_stale(obj: str, dep: str) -> bool:
+    """Is the object older than its source, one of the headers it included, or this file?"""
+    if not (os.path.exists(obj) and os.path.exists(dep)):
+        return True
+    t = os.path.getmtime(obj)
+    with open(dep) as f:
+        names = f.read().split(":", 1)[-1].replace("\\\n", " ").split()
+    own = [n for n in names if os.path.abspath(n).startswith(ROOT)] + [os.path.abspath(__file__)]
+    return any(not os.path.exists(n) or os.path.getmtime(n) > t for n in own)
+
+
+def _compile(src: str, force: bool, verbose: bool, extra: list[str]) -> str:
+    stem = os.path.join(OBJ, os.path.splitext(os.path.basename(src))[0])
+    obj, dep = stem + ".o", stem + ".d"
+    if force or extra or _object_stale(obj, dep):
+        tmp = f"{stem}.tmp{os.getpid()}"
+        cmd = [nvcc(), *NVCC_FLAGS, *extra, "-I", INCLUDE, "-I", CSRC, "-MD", "-MF", tmp + ".d",
+               "-c", "-o", tmp + ".o", src]
+        if verbose:
+            print(" ".join(cmd), file=sys.stderr)
+        subprocess.run(cmd, check=True)
+        os.replace(tmp + ".d", dep)
+        os.replace(tmp + ".o", obj)
+    return obj
+
+
 def build(force: bool = False, verbose: bool = False, extra: list[str] | None = None) -> str:
-    """Compile libeqlin.so unless it is newer than every source."""
+    """Compile libeqlin.so unless it is newer than every source (sources in parallel, each
+    only when it or a header that it includes changed)."""
     if not force and up_to_date():
         return LIB
+    os.makedirs(OBJ, exist_ok=True)
+    with concurrent.futures.ThreadPoolExecutor(os.cpu_count() or 1) as pool:
+        objs = list(pool.map(lambda src: _compile(src, force, verbose, extra or []), sources()))
     tmp = LIB + f".tmp{os.getpid()}"
-    cmd = [nvcc(), *NVCC_FLAGS, *(extra or []), "-I", INCLUDE, "-I", CSRC, "-o", tmp, *sources()]
-    if verbose:
-        print(" ".join(cmd), file=sys.stderr)
-    subprocess.run(cmd, check=True)
+    subprocess.run([nvcc(), *NVCC_FLAGS, "-shared", "-o", tmp, *objs], check=True)
     os.replace(tmp, LIB)
     return LIB
 

@@ -24,6 +24,7 @@
 #include "eqlin_layout.h"
 #include "eqlin_mlp.cuh"
 #include "eqlin_prep.cuh"
+#include "eqlin_report.h"
 
 using eqlin::TcParams;
 using eqlin::TmParams;
@@ -31,6 +32,25 @@ using eqlin::TmParams;
 #include "eqlin_host_plan.h"
 #include "eqlin_host_launch.h"
 #include "eqlin_host_mlp.h"
+
+namespace eqlin {
+
+int report(int code, const char* msg) noexcept {
+    try {
+        g_last_error = msg;
+    } catch (...) {   // no memory for the message: the code alone tells
+        g_last_error.clear();
+    }
+    return code;
+}
+
+int report_cuda(cudaError_t e, const char* what) noexcept {
+    char text[256];
+    std::snprintf(text, sizeof(text), "%s: %s", what, cudaGetErrorString(e));
+    return report(EQLIN_ERR_CUDA, text);
+}
+
+}  // namespace eqlin
 
 struct eqlin_handle {
     int device = 0;

@@ -1,0 +1,205 @@
+// eqlin_attn.cu -- host side of attention over packed sequences (include/eqlin.h): argument
+// checks, the choice of kernels and their launches.
+#include <algorithm>
+#include <cmath>
+
+#include "eqlin_attn.cuh"
+#include "eqlin_attn_f32.cuh"
+#include "eqlin_host_util.h"
+
+namespace {
+
+using namespace eqlin::host;
+using eqlin::report;
+namespace attn = eqlin::attn;
+
+constexpr int64_t kMaxRows = int64_t(1) << 31;
+constexpr int64_t kMaxStride = int64_t(1) << 40;
+
+int check_shape(const eqlin_attention_shape* a) {
+    if (!a) return report(EQLIN_ERR_INVALID_ARG, "shape is NULL");
+    if (a->q_rows < 0 || a->k_rows < 0 || a->heads < 1 || a->kv_heads < 1 || a->head_dim < 1 || a->sequences < 1)
+        return report(EQLIN_ERR_INVALID_ARG, "row counts must be >= 0; heads, kv_heads, head_dim, sequences >= 1");
+    if (!known_dtype(a->io_dtype)) return report(EQLIN_ERR_INVALID_ARG, "unknown dtype");
+    if (a->heads % a->kv_heads) return report(EQLIN_ERR_INVALID_ARG, "heads must be a multiple of kv_heads");
+    if (!(a->scale > 0.f) || !std::isfinite(a->scale))
+        return report(EQLIN_ERR_INVALID_ARG, "scale must be finite and positive");
+    if (a->causal != 0 && a->causal != 1) return report(EQLIN_ERR_INVALID_ARG, "causal must be 0 or 1");
+    if (!a->q_offsets != !a->k_offsets)
+        return report(EQLIN_ERR_INVALID_ARG, "q_offsets and k_offsets go together");
+    if (!a->q_offsets && a->sequences != 1)
+        return report(EQLIN_ERR_INVALID_ARG, "several sequences need q_offsets and k_offsets");
+    if (a->head_dim % 8 || a->head_dim > 128)
+        return report(EQLIN_ERR_UNSUPPORTED, "head_dim must be a multiple of 8 and at most 128");
+    if (a->heads > 65535 || a->q_rows >= kMaxRows || a->k_rows >= kMaxRows || a->sequences >= (int64_t(1) << 24))
+        return report(EQLIN_ERR_UNSUPPORTED, "fewer than 65536 heads, 2^31 rows and 2^24 sequences are supported");
+    if (!aligned(a->q_offsets, 4) || !aligned(a->k_offsets, 4))
+        return report(EQLIN_ERR_MISALIGNED, "the offsets must be 4-byte aligned");
+    return EQLIN_OK;
+}
+
+// One tensor of `rows` rows of `width` features: stride and address.
+int check_tensor(const void* t, int64_t rows, int64_t width, int64_t stride, int io, const char* what) {
+    if (rows == 0) return EQLIN_OK;
+    if (!t) return report(EQLIN_ERR_INVALID_ARG, what);
+    const int vec = 16 / elem_bytes(io);
+    if (stride < width || stride > kMaxStride) return report(EQLIN_ERR_INVALID_ARG, "a row stride is smaller than its row, or too large");
+    if (stride % vec || !aligned(t, 16))
+        return report(EQLIN_ERR_MISALIGNED, "rows must be 16-byte aligned (address and stride)");
+    return EQLIN_OK;
+}
+
+unsigned slots(int64_t rows, int64_t sequences, int m) { return static_cast<unsigned>(rows / m + sequences); }
+
+void fill(const eqlin_attention_shape* a, attn::Params& p) {
+    p.q_offsets = a->q_offsets;
+    p.k_offsets = a->k_offsets;
+    p.q_stride = a->q_stride;
+    p.k_stride = a->k_stride;
+    p.v_stride = a->v_stride;
+    p.o_stride = a->o_stride;
+    p.q_rows = static_cast<int>(a->q_rows);
+    p.k_rows = static_cast<int>(a->k_rows);
+    p.sequences = static_cast<int>(a->sequences);
+    p.heads = static_cast<int>(a->heads);
+    p.kv_heads = static_cast<int>(a->kv_heads);
+    p.D = static_cast<int>(a->head_dim);
+    p.causal = a->causal;
+    p.scale = a->scale;
+}
+
+template <class T, int DP>
+int forward_f32(const attn::Params& p, cudaStream_t st) {
+    using namespace attn::f32;
+    return launch(eqlin_attn_fwd_f32_kernel<T, DP>, dim3(slots(p.q_rows, p.sequences, kM), p.heads), dim3(kThreads),
+                  Shape<DP>::FWD_BYTES, st, "attention launch", p);
+}
+template <class T>
+int forward_t(const attn::Params& p, cudaStream_t st) {
+    return p.D <= 64 ? forward_f32<T, 64>(p, st) : forward_f32<T, 128>(p, st);
+}
+
+template <class T>
+int launch_delta(const attn::Params& p, cudaStream_t st) {
+    constexpr int VEC = 16 / sizeof(T);
+    int lanes = 1;
+    while (lanes * VEC < p.D) lanes *= 2;
+    const long long units = static_cast<long long>(p.q_rows) * p.heads;
+    const long long blocks = (units + 256 / lanes - 1) / (256 / lanes);
+    return launch(attn::eqlin_attn_delta_kernel<T, VEC>, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, st,
+                  "attention gradient launch", p, lanes);
+}
+
+template <class T, int DP>
+int backward_f32(const attn::Params& p, cudaStream_t st) {
+    using namespace attn::f32;
+    int s = EQLIN_OK;
+    if (p.q_rows > 0) s = launch_delta<T>(p, st);
+    if (s == EQLIN_OK && p.k_rows > 0)
+        s = launch(eqlin_attn_dkv_f32_kernel<T, DP>, dim3(slots(p.k_rows, p.sequences, kM), p.kv_heads),
+                   dim3(kThreads), Shape<DP>::DKV_BYTES, st, "attention gradient launch", p);
+    if (s == EQLIN_OK && p.q_rows > 0)
+        s = launch(eqlin_attn_dq_f32_kernel<T, DP>, dim3(slots(p.q_rows, p.sequences, kM), p.heads), dim3(kThreads),
+                   Shape<DP>::DQ_BYTES, st, "attention gradient launch", p);
+    return s;
+}
+template <class T>
+int backward_t(const attn::Params& p, cudaStream_t st) {
+    return p.D <= 64 ? backward_f32<T, 64>(p, st) : backward_f32<T, 128>(p, st);
+}
+
+}  // namespace
+
+extern "C" {
+
+int eqlin_attention_workspace_size(const eqlin_attention_shape* shape, int backward, size_t* bytes) {
+    if (!bytes) return report(EQLIN_ERR_INVALID_ARG, "NULL argument");
+    const int s = check_shape(shape);
+    if (s != EQLIN_OK) return s;
+    *bytes = backward ? size_t(shape->q_rows) * size_t(shape->heads) * sizeof(float) : 0;
+    return EQLIN_OK;
+}
+
+int eqlin_attention_forward(const eqlin_attention_shape* shape, const void* q, const void* k, const void* v, void* o,
+                            float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+    int s = check_shape(shape);
+    if (s != EQLIN_OK) return s;
+    const eqlin_attention_shape& a = *shape;
+    const int64_t wq = a.heads * a.head_dim, wk = a.kv_heads * a.head_dim;
+    if ((s = check_tensor(q, a.q_rows, wq, a.q_stride, a.io_dtype, "q is NULL")) != EQLIN_OK ||
+        (s = check_tensor(k, a.k_rows, wk, a.k_stride, a.io_dtype, "k is NULL")) != EQLIN_OK ||
+        (s = check_tensor(v, a.k_rows, wk, a.v_stride, a.io_dtype, "v is NULL")) != EQLIN_OK ||
+        (s = check_tensor(o, a.q_rows, wq, a.o_stride, a.io_dtype, "o is NULL")) != EQLIN_OK)
+        return s;
+    if (!aligned(lse, 4)) return report(EQLIN_ERR_MISALIGNED, "lse must be 4-byte aligned");
+    size_t need = 0;
+    if ((s = eqlin_attention_workspace_size(shape, 0, &need)) != EQLIN_OK) return s;
+    if (need && (!workspace || workspace_bytes < need))
+        return report(EQLIN_ERR_INVALID_ARG, "workspace missing or smaller than eqlin_attention_workspace_size");
+    if (!aligned(workspace, 16)) return report(EQLIN_ERR_MISALIGNED, "workspace must be 16-byte aligned");
+    if (a.q_rows == 0) return EQLIN_OK;
+    int sms = 0;
+    if ((s = current_device(nullptr, &sms)) != EQLIN_OK) return s;
+    attn::Params p = {};
+    fill(shape, p);
+    p.q = q;
+    p.k = k;
+    p.v = v;
+    p.out = o;
+    p.lse = lse;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (a.io_dtype == EQLIN_F32) return forward_t<float>(p, st);
+    return a.io_dtype == EQLIN_F16 ? forward_t<__half>(p, st) : forward_t<__nv_bfloat16>(p, st);
+}
+
+int eqlin_attention_backward(const eqlin_attention_shape* shape, const eqlin_attention_grad_strides* strides,
+                             const void* dout, const void* q, const void* k, const void* v, const void* o,
+                             const float* lse, void* dq, void* dk, void* dv, void* workspace, size_t workspace_bytes,
+                             void* stream) {
+    int s = check_shape(shape);
+    if (s != EQLIN_OK) return s;
+    if (!strides) return report(EQLIN_ERR_INVALID_ARG, "strides is NULL");
+    const eqlin_attention_shape& a = *shape;
+    const int64_t wq = a.heads * a.head_dim, wk = a.kv_heads * a.head_dim;
+    const int io = a.io_dtype;
+    if ((s = check_tensor(q, a.q_rows, wq, a.q_stride, io, "q is NULL")) != EQLIN_OK ||
+        (s = check_tensor(k, a.k_rows, wk, a.k_stride, io, "k is NULL")) != EQLIN_OK ||
+        (s = check_tensor(v, a.k_rows, wk, a.v_stride, io, "v is NULL")) != EQLIN_OK ||
+        (s = check_tensor(o, a.q_rows, wq, a.o_stride, io, "o is NULL")) != EQLIN_OK ||
+        (s = check_tensor(dout, a.q_rows, wq, strides->dout, io, "dout is NULL")) != EQLIN_OK ||
+        (s = check_tensor(dq, a.q_rows, wq, strides->dq, io, "dq is NULL")) != EQLIN_OK ||
+        (s = check_tensor(dk, a.k_rows, wk, strides->dk, io, "dk is NULL")) != EQLIN_OK ||
+        (s = check_tensor(dv, a.k_rows, wk, strides->dv, io, "dv is NULL")) != EQLIN_OK)
+        return s;
+    if (a.q_rows > 0 && !lse) return report(EQLIN_ERR_INVALID_ARG, "lse is NULL");
+    if (!aligned(lse, 4)) return report(EQLIN_ERR_MISALIGNED, "lse must be 4-byte aligned");
+    size_t need = 0;
+    if ((s = eqlin_attention_workspace_size(shape, 1, &need)) != EQLIN_OK) return s;
+    if (need && (!workspace || workspace_bytes < need))
+        return report(EQLIN_ERR_INVALID_ARG, "workspace missing or smaller than eqlin_attention_workspace_size");
+    if (!aligned(workspace, 16)) return report(EQLIN_ERR_MISALIGNED, "workspace must be 16-byte aligned");
+    if (a.q_rows == 0 && a.k_rows == 0) return EQLIN_OK;
+    int sms = 0;
+    if ((s = current_device(nullptr, &sms)) != EQLIN_OK) return s;
+    attn::Params p = {};
+    fill(shape, p);
+    p.q = q;
+    p.k = k;
+    p.v = v;
+    p.o = o;
+    p.dout = dout;
+    p.lse = const_cast<float*>(lse);
+    p.delta = static_cast<float*>(workspace);
+    p.dq = dq;
+    p.dk = dk;
+    p.dv = dv;
+    p.do_stride = strides->dout;
+    p.dq_stride = strides->dq;
+    p.dk_stride = strides->dk;
+    p.dv_stride = strides->dv;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (io == EQLIN_F32) return backward_t<float>(p, st);
+    return io == EQLIN_F16 ? backward_t<__half>(p, st) : backward_t<__nv_bfloat16>(p, st);
+}
+
+}  // extern "C"

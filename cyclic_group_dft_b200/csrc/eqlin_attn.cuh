@@ -1,0 +1,127 @@
+// eqlin_attn.cuh -- what the attention kernels share: parameters, packed sequences and the
+// kernel that prepares the gradients.
+//
+// For query row i and key row j of one sequence and one head (D features: channels times group
+// elements, so a cyclic shift of the group axis of q and k leaves every product unchanged and
+// a shift of v shifts the output):
+//     s_ij = scale * q_i . k_j,   p_ij = exp(s_ij - lse_i) over the visible j,   o_i = sum_j p_ij v_j
+// Causal: query i of Lq sees key j of Lk when j <= i + Lk - Lq (the last query sees every key).
+// A row that sees no key has o = 0, lse = -infinity and zero gradients.
+//     dv_j = sum_i p_ij do_i,  ds_ij = p_ij (do_i . v_j - delta_i),  delta_i = do_i . o_i
+//     dq_i = scale * sum_j ds_ij k_j,   dk_j = scale * sum_i ds_ij q_i
+// Query head h reads key/value head h / (heads / kv_heads); dk and dv of a shared head sum over
+// its query heads inside one block, so no atomics are used and results do not vary.
+#pragma once
+
+#include <cstdint>
+
+#include "eqlin_vec.cuh"
+#include "sm100_ptx.cuh"
+
+namespace eqlin {
+namespace attn {
+
+struct Params {
+    const void *q, *k, *v, *o, *dout;
+    void *out, *dq, *dk, *dv;      // out: the forward's o
+    float* lse;                    // [heads][q_rows], or NULL
+    float* delta;                  // [heads][q_rows] (gradients)
+    const int32_t *q_offsets, *k_offsets;   // [sequences + 1], or NULL: one sequence of all rows
+    long long q_stride, k_stride, v_stride, o_stride, do_stride, dq_stride, dk_stride, dv_stride;
+    int q_rows, k_rows, sequences, heads, kv_heads, D;
+    int causal;
+    float scale;
+    int* status;                   // device status word (bounded waits)
+    unsigned long long timeout_ns;
+};
+
+// Rows [start, start + len) of sequence b.  Offsets live in device memory, where the host cannot
+// check them: they are clamped to the tensor's rows and to one another, so that bad ones give
+// wrong sequences but no access outside the tensors.
+struct Rows {
+    int start, len;
+};
+__device__ __forceinline__ Rows sequence_rows(const int32_t* offsets, int b, int rows) {
+    if (!offsets) return {0, rows};
+    const int s = min(max(offsets[b], 0), rows);
+    const int e = min(max(offsets[b + 1], s), rows);
+    return {s, e - s};
+}
+
+// Blocks are given tiles of M consecutive rows of one sequence without knowing the lengths on the
+// host.  Sequence b owns the slots [off[b] / M + b, off[b+1] / M + b + 1): at least as many as it has
+// tiles, in order, and rows / M + sequences in all.  A slot past its sequence's last tile has none.
+// The slot's sequence is the last b whose first slot is not past it: a search in log2(sequences)
+// reads; with 32 lanes probing at once, in log32 rounds.  Every lane of the warp must call it.
+struct Tile {
+    int b;       // sequence
+    int tile;    // tile within the sequence, or -1: none
+    Rows own;    // the sequence's rows on this side
+};
+template <int M>
+__device__ __forceinline__ Tile find_tile(const int32_t* offsets, int sequences, int rows, int slot) {
+    int b = 0;
+    if (offsets) {
+        int lo = 0, n = sequences;   // the answer lies in [lo, lo + n)
+        const int lane = threadIdx.x & 31;
+        while (n > 1) {
+            const int step = (n + 31) / 32;
+            const int probe = lo + lane * step;
+            const bool ok = lane * step < n && min(max(offsets[probe], 0), rows) / M + probe <= slot;
+            const unsigned m = __ballot_sync(0xFFFFFFFFu, ok);
+            const int last = m ? 31 - __clz(m) : 0;
+            const int rest = n - last * step;
+            lo += last * step;
+            n = rest < step ? rest : step;
+        }
+        b = lo;
+    }
+    Tile t;
+    t.b = b;
+    t.own = sequence_rows(offsets, b, rows);
+    const int first = offsets ? min(max(offsets[b], 0), rows) / M + b : 0;
+    t.tile = slot - first;
+    if (t.tile < 0 || static_cast<long long>(t.tile) * M >= t.own.len) t.tile = -1;
+    return t;
+}
+
+// Keys [0, n) that query rows up to `last` (within the sequence) may see.
+__device__ __forceinline__ int keys_seen(int last, int q_len, int k_len, int causal) {
+    if (!causal) return k_len;
+    const long long n = static_cast<long long>(last) + 1 + k_len - q_len;
+    return static_cast<int>(n < 0 ? 0 : (n < k_len ? n : k_len));
+}
+// First query row (within the sequence) that sees key `first`.
+__device__ __forceinline__ int first_query(int first, int q_len, int k_len, int causal) {
+    if (!causal) return 0;
+    const long long i = static_cast<long long>(first) + q_len - k_len;
+    return static_cast<int>(i < 0 ? 0 : i);
+}
+
+// delta[h][i] = do_i . o_i in fp32: one warp per (row, 32 / lanes heads), reading both tensors
+// once.  A head takes `lanes` = the power of two >= D / VEC lanes.
+template <class T, int VEC>
+__global__ void __launch_bounds__(256) eqlin_attn_delta_kernel(const Params p, int lanes) {
+    using V = Vec<T, VEC>;
+    ptx::grid_launch_dependents();
+    ptx::grid_dependency_wait();
+    const int per_block = 256 / lanes;
+    const long long unit = static_cast<long long>(blockIdx.x) * per_block + threadIdx.x / lanes;
+    const int lane = threadIdx.x & (lanes - 1);
+    const bool live = unit < static_cast<long long>(p.q_rows) * p.heads;
+    const int row = live ? static_cast<int>(unit / p.heads) : 0;
+    const int h = live ? static_cast<int>(unit - static_cast<long long>(row) * p.heads) : 0;
+    float s = 0.f;
+    if (live && lane * VEC < p.D) {
+        float a[VEC], b[VEC];
+        V::unpack(V::load(static_cast<const T*>(p.dout) + row * p.do_stride + static_cast<long long>(h) * p.D + lane * VEC), a);
+        V::unpack(V::load(static_cast<const T*>(p.o) + row * p.o_stride + static_cast<long long>(h) * p.D + lane * VEC), b);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) s = fmaf(a[e], b[e], s);
+    }
+    for (int o = lanes >> 1; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+    if (live && lane == 0) p.delta[static_cast<long long>(h) * p.q_rows + row] = s;
+}
+
+}  // namespace attn
+}  // namespace eqlin

@@ -406,6 +406,136 @@ EQLIN_API int eqlin_mlp_destroy(eqlin_mlp* m);
 EQLIN_API int eqlin_mlp_query(int64_t Cin, int64_t H, int64_t Cout, int64_t G, int io_dtype, int64_t* stages,
                               int64_t* smem_bytes);
 
+/*
+ * The rest of an equivariant transformer block (page "Flash EQ-Linear: ...", section "A Nivel
+ * de Red": networks built of EQ-Linear layers): attention between tokens, the norm with the
+ * residual's addition and rotary positions, on the layers' layout [N, C, G].  Each commutes
+ * with cyclic shifts of the group axis.  These calls keep no state: every pointer, the
+ * workspace included, is the caller's, nothing is allocated and nothing is synchronised.
+ * They accept G = 1 as well (features without a group axis).
+ *
+ * eqlin_add_rmsnorm -- r = x + residual;  y[n,c,g] = r[n,c,g] * w[c] / sqrt(mean_{c,g} r[n]^2 + eps)
+ *
+ *   x, residual  device, [N, C, G] of io_dtype; residual may be NULL (r = x).
+ *   weight       device, [C] of w_dtype, or NULL (ones).
+ *   y            device, [N, C, G] of io_dtype.
+ *   sum_out      device, [N, C, G] of io_dtype: receives r (the new residual stream); or NULL.
+ *                y and sum_out may be x or residual themselves (the same address), but not one
+ *                another; any other overlap is undefined.
+ *   eps          finite, >= 0.
+ * Statistics and y are computed in fp32 from the unrounded sum; y and r are rounded once.
+ * N == 0 is a no-op.  Supported: G in {1, 2, 4, 8, 16}, N < 2^31; for 16-bit I/O C*G a multiple
+ * of 8 and at most 16384, for fp32 at most 8192 (2048 when C*G is not a multiple of 4).
+ *
+ * eqlin_add_rmsnorm_fp8 -- the same with y in 8 bits: per row scale[n] = max |y[n]| / 448 (1 for
+ * a row of zeros), y8 = e4m3(y / scale[n]), round to nearest even.  y8: device, [N, C, G] bytes,
+ * 16-byte aligned, overlapping nothing; scale: device, [N] fp32.
+ *
+ * eqlin_rmsnorm_backward -- the gradients, from the stored sum r:
+ *   dx = dsum + rstd * (w dy - u * mean(w dy u)),  u = r * rstd,   of x and of residual alike;
+ *   dweight[c] = sum_{n,g} dy u   (fp32, written, not accumulated; NULL: not computed).
+ *   dsum is the gradient that reaches r through the residual stream, or NULL (zero).  dx may be
+ *   dy, sum or dsum itself (the same address).
+ *   workspace    device, at least eqlin_rmsnorm_backward_workspace_size bytes (host only; 0
+ *                for N == 0), 16-byte aligned; needed only with dweight.  Calls whose work
+ *                overlaps on the GPU must not share it.
+ * One launch, and a second, fixed-order reduction for dweight: repeated calls give the same bits.
+ * N == 0 writes zeros to dweight.
+ *
+ * Errors of the three: INVALID_ARG (sizes, eps, dtype, NULL pointers, workspace), UNSUPPORTED,
+ * MISALIGNED (tensors not 16-byte aligned), CUDA.
+ */
+EQLIN_API int eqlin_add_rmsnorm(const void* x, const void* residual, const void* weight, void* y, void* sum_out,
+                                int64_t N, int64_t C, int64_t G, float eps, int w_dtype, int io_dtype, void* stream);
+EQLIN_API int eqlin_add_rmsnorm_fp8(const void* x, const void* residual, const void* weight, void* y8, float* scale,
+                                    void* sum_out, int64_t N, int64_t C, int64_t G, float eps, int w_dtype,
+                                    int io_dtype, void* stream);
+EQLIN_API int eqlin_rmsnorm_backward_workspace_size(int64_t N, int64_t C, int64_t G, int io_dtype, size_t* bytes);
+EQLIN_API int eqlin_rmsnorm_backward(const void* dy, const void* sum, const void* weight, const void* dsum, void* dx,
+                                     float* dweight, int64_t N, int64_t C, int64_t G, float eps, int w_dtype,
+                                     int io_dtype, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * eqlin_rope -- rotary positions with 1 to 4 axes (row, column, time, ...) on `heads` heads of
+ * head_channels channels each.  Channels c and c + head_channels/2 of a head are pair c; the pairs
+ * are divided among the axes in order, sections[a] of them for axis a, and pair j of axis a is
+ * turned by positions[n, a] * base^(-j / sections[a]) radians, for every group element alike:
+ *     y[c] = x[c] cos - x[c'] sin,   y[c'] = x[c'] cos + x[c] sin,   c' = c + head_channels/2
+ *
+ *   x, y         device, N rows of heads * head_channels * G features of io_dtype, x_stride and
+ *                y_stride features apart (slices of wider rows, such as the queries and keys of
+ *                a joint projection).  y may be x (same address and stride); any other overlap
+ *                is undefined.  Aligned to the element size; 16-byte aligned rows are fastest.
+ *   positions    device, [N, axes] int32, any values.
+ *   sections     host, `axes` counts >= 0 that add up to head_channels / 2.
+ *   base         finite, >= 1.
+ *   inverse      non-zero: turn back (this is also the gradient: dx = inverse rotation of dy).
+ * Angles are exact to 2^-32 turns for every position.  N == 0 is a no-op.
+ * Errors: INVALID_ARG, UNSUPPORTED (G not in {1, 2, 4, 8, 16}; head_channels odd or above 256),
+ * MISALIGNED, CUDA.
+ */
+EQLIN_API int eqlin_rope(const void* x, const int32_t* positions, void* y, int64_t N, int64_t heads,
+                         int64_t head_channels, int64_t G, const int32_t* sections, int axes, double base,
+                         int64_t x_stride, int64_t y_stride, int inverse, int io_dtype, void* stream);
+
+/*
+ * Attention over packed sequences.  Rows of q, k, v and o are tokens; a row holds its heads one
+ * after the other, head_dim = channels of a head * G features each.  Sequences follow one another
+ * in the rows: sequence b has the query rows [q_offsets[b], q_offsets[b+1]) and the key rows
+ * [k_offsets[b], k_offsets[b+1]).  Within a sequence, for query head h with key head
+ * h / (heads / kv_heads):
+ *     s_ij = scale * q_i . k_j,   lse_i = log sum_j exp(s_ij),   o_i = sum_j exp(s_ij - lse_i) v_j
+ * over the keys j that row i sees: all, or with `causal` those with j <= i + (keys - queries), so
+ * that the last query sees every key.  A row that sees no key gets o = 0, lse = -infinity and
+ * adds nothing to any gradient.
+ */
+typedef struct {
+    int64_t q_rows, k_rows;     /* rows of q and o; rows of k and v (< 2^31) */
+    int64_t sequences;          /* >= 1 */
+    int64_t heads, kv_heads;    /* heads a multiple of kv_heads */
+    int64_t head_dim;           /* features of a head: a multiple of 8, at most 128 */
+    const int32_t* q_offsets;   /* device, [sequences + 1], non-decreasing from 0 up; or both NULL: */
+    const int32_t* k_offsets;   /*   one sequence of all rows.  They may be the same array. */
+    int64_t q_stride, k_stride, v_stride, o_stride; /* features from one row to the next */
+    int io_dtype;               /* eqlin_dtype of q, k, v, o and their gradients */
+    int causal;                 /* 0 or 1 */
+    float scale;                /* finite, > 0 (usually 1 / sqrt(head_dim)) */
+} eqlin_attention_shape;
+
+typedef struct {
+    int64_t dout, dq, dk, dv;   /* features from one row to the next */
+} eqlin_attention_grad_strides;
+
+/*
+ * eqlin_attention_workspace_size -- bytes of workspace that the forward (backward == 0) or the
+ * backward needs.  Host only.
+ *
+ * eqlin_attention_forward -- o and lse.
+ *   q, k, v, o   device, rows 16-byte aligned (address and stride).  o may not overlap the others.
+ *   lse          device, [heads, q_rows] fp32 (natural logarithm); or NULL.
+ * eqlin_attention_backward -- dq, dk, dv from dout = dL/do and the forward's inputs, o and lse.
+ *   Written, not accumulated; they overlap none of the inputs.  dk and dv of a key head shared by
+ *   several query heads are the sums over them.
+ *
+ * 16-bit I/O multiplies on the tensor cores with fp32 accumulation; the weights exp(s - lse) and
+ * ds are rounded to the I/O type before their products.  fp32 I/O: fp32 arithmetic.  Statistics
+ * are fp32.  No atomics: repeated calls give the same bits.
+ * Rows that no sequence covers (behind the last one) are not read and not written.  A row holding
+ * infinities or NaN affects its own sequence only.  Offsets are device data the host cannot
+ * check: decreasing or out-of-range ones are clamped (wrong sequences, no access out of bounds).
+ *   workspace    device, 16-byte aligned, at least eqlin_attention_workspace_size bytes; calls
+ *                whose work overlaps on the GPU must not share it.  May be NULL when 0 are needed.
+ *   stream       asynchronous on this stream; allocates nothing.
+ * Errors: INVALID_ARG, UNSUPPORTED (head_dim), MISALIGNED, CUDA.
+ */
+EQLIN_API int eqlin_attention_workspace_size(const eqlin_attention_shape* shape, int backward, size_t* bytes);
+EQLIN_API int eqlin_attention_forward(const eqlin_attention_shape* shape, const void* q, const void* k, const void* v,
+                                      void* o, float* lse, void* workspace, size_t workspace_bytes, void* stream);
+EQLIN_API int eqlin_attention_backward(const eqlin_attention_shape* shape, const eqlin_attention_grad_strides* strides,
+                                       const void* dout, const void* q, const void* k, const void* v, const void* o,
+                                       const float* lse, void* dq, void* dk, void* dv, void* workspace,
+                                       size_t workspace_bytes, void* stream);
+
 /* Static description of a status code ("ok", "invalid argument", ...). */
 EQLIN_API const char* eqlin_status_string(int status);
 

@@ -1,0 +1,464 @@
+"""Attention over packed sequences, residual RMS norm and rotary positions on the GPU, against
+their float64 definitions (block_reference.py) with bounds derived there."""
+from __future__ import annotations
+
+import math
+
+import pytest
+import torch
+
+import cyclic_group_dft_b200 as eq
+import block_reference as ref
+from block_reference import within
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda:0"
+TYPES = [torch.bfloat16, torch.float16, torch.float32]
+
+
+def _randn(*shape, seed, dtype, std=1.0):
+    return (torch.randn(*shape, generator=torch.Generator().manual_seed(seed)) * std).to(dtype)
+
+
+# ------------------------------------------------------------------------------------ norm
+NORM_SHAPES = [(1, 8, 1), (3, 1, 8), (5, 96, 4), (257, 96, 4), (7, 64, 8), (33, 32, 16), (2, 100, 2), (4, 192, 4),
+               (19, 136, 4), (3, 512, 8), (2, 1024, 16), (70, 4, 2)]
+NORM_F32_ONLY = [(3, 3, 1), (9, 5, 2), (2, 2047, 1), (5, 2, 1)]
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("N,C,G", NORM_SHAPES + NORM_F32_ONLY)
+def test_norm(N, C, G, dtype):
+    if dtype != torch.float32 and (N, C, G) in NORM_F32_ONLY:
+        pytest.skip("16-byte rows only")
+    if dtype == torch.float32 and C * G > 8192:
+        pytest.skip("fp32 rows of at most 8192 features")
+    eps, u = 1e-6, ref.unit(dtype)
+    x, res = _randn(N, C, G, seed=N, dtype=dtype), _randn(N, C, G, seed=C, dtype=dtype, std=3.0)
+    w = _randn(C, seed=G, dtype=torch.float32)
+    for residual, weight in ((res, w), (None, None), (res, w.to(dtype))):
+        y64, r64, _ = ref.add_rmsnorm(x, residual, weight, eps)
+        y, r = eq.eqlin_add_rmsnorm(x.to(DEV), None if residual is None else residual.to(DEV),
+                                    None if weight is None else weight.to(DEV), eps=eps)
+        within(y, y64, (u + ref.E) * y64.abs() + ref.tiny(dtype), "y")
+        within(r, r64, (u + 2.0 ** -23) * r64.abs() + ref.tiny(dtype), "r")
+    y8, scale, r = eq.eqlin_add_rmsnorm_fp8(x.to(DEV), res.to(DEV), w.to(DEV), eps=eps)
+    y64, r64, _ = ref.add_rmsnorm(x, res, w, eps)
+    top = y64.abs().amax((1, 2))
+    within(scale, torch.where(top > 0, top / 448, torch.ones_like(top)), ref.E * (top / 448 + 1), "scale")
+    # e4m3: half a step is 2^-4 of the value, at least 2^-10 (half the smallest subnormal), in scale units
+    s = (top / 448)[:, None, None]
+    within(y8.float().cpu().double() * scale.cpu().double()[:, None, None], y64,
+           (2.0 ** -4 + 4 * ref.E) * y64.abs() + (2.0 ** -10 + ref.E) * s, "y8 * scale")
+    within(r, r64, (u + 2.0 ** -23) * r64.abs() + ref.tiny(dtype), "r")
+    dy, dsum = _randn(N, C, G, seed=5, dtype=dtype), _randn(N, C, G, seed=6, dtype=dtype)
+    for weight, ds in ((w, dsum), (None, None), (w.to(dtype), dsum)):
+        dx64, dw64, dx_b, dw_b = ref.rmsnorm_backward(dy, r.cpu(), weight, ds, eps)
+        dx, dw = eq.eqlin_rmsnorm_backward(dy.to(DEV), r, None if weight is None else weight.to(DEV),
+                                           None if ds is None else ds.to(DEV), eps=eps)
+        within(dx, dx64, dx_b, "dx")
+        within(dw, dw64, dw_b, "dweight")
+
+
+def test_norm_zero_rows_and_empty_batches():
+    x = torch.zeros(3, 16, 4, dtype=torch.bfloat16, device=DEV)
+    y8, scale, r = eq.eqlin_add_rmsnorm_fp8(x, x)
+    assert (scale == 1).all() and (y8.float() == 0).all() and (r == 0).all()
+    e = x[:0]
+    y, r = eq.eqlin_add_rmsnorm(e, e)
+    assert y.shape == e.shape and r.shape == e.shape
+    dx, dw = eq.eqlin_rmsnorm_backward(e, e)
+    assert dx.shape == e.shape and (dw == 0).all()
+    # infinities and NaN stay in their rows
+    x = torch.ones(4, 16, 4, device=DEV)
+    x[1, 3, 2], x[2, 0, 0] = float("nan"), float("inf")
+    y, _ = eq.eqlin_add_rmsnorm(x, None)
+    assert y[1].isnan().all() and y[2].isnan().any() and torch.isfinite(y[[0, 3]]).all()
+
+
+def test_norm_in_place_and_large_values():
+    x, res = _randn(50, 96, 4, seed=1, dtype=torch.bfloat16).to(DEV), _randn(50, 96, 4, seed=2, dtype=torch.bfloat16).to(DEV)
+    y, r = eq.eqlin_add_rmsnorm(x, res)
+    x2, res2 = x.clone(), res.clone()
+    y2, r2 = eq.eqlin_add_rmsnorm(x2, res2, y=x2, sum_out=res2)      # y over x, the sum over the residual
+    assert torch.equal(y, y2) and torch.equal(r, r2) and y2.data_ptr() == x2.data_ptr()
+    dy = _randn(50, 96, 4, seed=3, dtype=torch.bfloat16).to(DEV)
+    dx, dw = eq.eqlin_rmsnorm_backward(dy, r, dsum=dy)
+    dx2, dw2 = eq.eqlin_rmsnorm_backward(dy, r, dsum=dy, dx=dy)
+    assert torch.equal(dx, dx2) and torch.equal(dw, dw2)
+    with pytest.raises(ValueError):
+        eq.eqlin_add_rmsnorm(x, res, y=x, sum_out=x)
+    big = torch.full((2, 16, 4), 3e4, dtype=torch.float16, device=DEV)   # squares overflow fp16, not fp32
+    y, _ = eq.eqlin_add_rmsnorm(big, None)
+    assert (y.float() - 1).abs().max() <= 2.0 ** -11
+
+
+def test_norm_gradient_against_differences():
+    N, C, G, eps = 5, 24, 4, 1e-3
+    x = _randn(N, C, G, seed=1, dtype=torch.float64)
+    w, dy = _randn(C, seed=2, dtype=torch.float64), _randn(N, C, G, seed=3, dtype=torch.float64)
+    f = lambda x, w: float((ref.add_rmsnorm(x, None, w, eps)[0] * dy).sum())   # noqa: E731
+    r = x.float()
+    dx, dw = eq.eqlin_rmsnorm_backward(dy.float().to(DEV), r.to(DEV), w.float().to(DEV), eps=eps)
+    h = 1e-5   # central differences of a smooth function in float64: truncation and rounding below 1e-8
+    for (n, c, g) in ((0, 0, 0), (4, 23, 3), (2, 11, 1)):
+        d = torch.zeros_like(x)
+        d[n, c, g] = h
+        assert abs((f(x + d, w) - f(x - d, w)) / (2 * h) - dx[n, c, g].item()) < 2e-5
+    for c in (0, 7, 23):
+        d = torch.zeros_like(w)
+        d[c] = h
+        assert abs((f(x, w + d) - f(x, w - d)) / (2 * h) - dw[c].item()) < 2e-4
+
+
+# ------------------------------------------------------------------------------------ rope
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("N,heads,Dh,G,sections,base,far", [
+    (1, 1, 2, 1, (1,), 100.0, 10), (5, 3, 8, 4, (2, 2), 100.0, 56), (300, 6, 32, 4, (8, 8), 10000.0, 1000),
+    (17, 4, 8, 16, (2, 1, 1), 100.0, 14), (33, 2, 6, 2, (0, 3), 10.0, 1 << 20), (9, 5, 10, 1, (5,), 10000.0, 1 << 30),
+    (2, 1, 256, 2, (100, 20, 7, 1), 500.0, 100000), (40, 12, 8, 8, (4,), 1.0, 7), (3, 2, 12, 2, (6,), 100.0, 50),
+])
+def test_rope(N, heads, Dh, G, sections, base, far, dtype):
+    x = _randn(N, heads * Dh, G, seed=N, dtype=dtype)
+    pos = torch.randint(-far, far, (N, len(sections)), generator=torch.Generator().manual_seed(1), dtype=torch.int32)
+    y64, bound = ref.rope(x, pos, heads, sections, base)
+    y = eq.eqlin_rope(x.to(DEV), pos.to(DEV), heads=heads, sections=sections, base=base)
+    # beside the bound of the arithmetic: the reference's own angle, position * frequency rounded to
+    # float64, is off by up to 2^-52 of up to `far` radians
+    slack = far * 2.0 ** -51 * x.double().abs().max()
+    within(y, y64, bound + slack, "y")
+    back64, bound = ref.rope(y.cpu(), pos, heads, sections, base, inverse=True)
+    back = eq.eqlin_rope(y, pos.to(DEV), heads=heads, sections=sections, base=base, inverse=True)
+    within(back, back64, bound + 2 * slack, "inverse")
+
+
+@pytest.mark.parametrize("offset,width", [(0, 96), (8, 104), (4, 100), (1, 97), (2, 98)])
+def test_rope_slices_and_in_place(offset, width):
+    """Channel slices of a wider tensor at every alignment, and y over x."""
+    G, heads, Dh = 2, 3, 8
+    joint = _randn(21, width, G, seed=3, dtype=torch.bfloat16).to(DEV)
+    before = joint.clone()
+    pos = torch.randint(0, 99, (21, 2), dtype=torch.int32).to(DEV)
+    x = joint[:, offset:offset + heads * Dh]
+    want = eq.eqlin_rope(x.contiguous(), pos, heads=heads, sections=(2, 2))
+    assert torch.equal(eq.eqlin_rope(x, pos, heads=heads, sections=(2, 2)), want)
+    eq.eqlin_rope(x, pos, heads=heads, sections=(2, 2), out=x)
+    assert torch.equal(x, want)
+    before[:, offset:offset + heads * Dh] = want
+    assert torch.equal(joint, before)                       # nothing beside the slice changed
+    with pytest.raises(ValueError):
+        eq.eqlin_rope(joint.transpose(1, 2), pos, heads=1, sections=(1,))
+    assert eq.eqlin_rope(x[:0], pos[:0], heads=heads, sections=(2, 2)).shape == (0, heads * Dh, G)
+
+
+def test_rope_gradient_is_the_inverse():
+    x, dy = _randn(7, 16, 4, seed=1, dtype=torch.float32).to(DEV), _randn(7, 16, 4, seed=2, dtype=torch.float32).to(DEV)
+    pos = torch.randint(0, 50, (7, 2), dtype=torch.int32).to(DEV)
+    kw = dict(heads=2, sections=(2, 2), base=100.0)
+    left = (eq.eqlin_rope(x, pos, **kw).double() * dy.double()).sum()
+    right = (x.double() * eq.eqlin_rope(dy, pos, inverse=True, **kw).double()).sum()
+    assert abs(left - right) <= ref.E * (x.double().abs().sum() + dy.double().abs().sum())
+
+
+# ------------------------------------------------------------------------------- attention
+SELF = [
+    ([1], 1, 1, 8, False), ([1], 2, 1, 64, True), ([49] * 5, 3, 3, 128, False), ([64], 2, 2, 64, True),
+    ([63, 65, 1, 0, 128, 129, 200], 2, 1, 64, True), ([63, 65, 1, 0, 128, 129, 200], 2, 2, 128, False),
+    ([5, 0, 0, 3], 6, 2, 40, True), ([256, 255, 257], 3, 1, 72, True), ([700], 2, 2, 96, False),
+    ([130, 12], 4, 1, 16, False), ([31] * 9, 2, 1, 24, True), ([0, 0, 17], 1, 1, 32, False),
+    ([385, 2, 640], 2, 1, 120, True), ([2] * 70, 1, 1, 56, True), ([1] * 40 + [300], 2, 1, 128, True),
+]
+CROSS = [
+    ([1, 1, 1], [300, 0, 7], 4, 2, 64, False), ([10, 0, 130, 3], [0, 20, 50, 400], 2, 1, 128, True),
+    ([1], [2000], 8, 2, 64, False), ([200], [70], 2, 2, 48, True), ([5, 129], [513, 128], 3, 1, 80, False),
+    ([0, 0], [5, 9], 2, 1, 64, True), ([5, 9], [0, 0], 2, 1, 64, True), ([2], [1500], 2, 1, 128, True),
+]
+
+
+def _attention(q_lens, k_lens, H, Hk, D, causal, dtype, G=4, seed=0, tail=0, std=1.0):
+    """Runs forward and backward; returns the GPU's outputs and the reference's with their bounds."""
+    G = math.gcd(G, D)
+    Nq, Nk, Dh = sum(q_lens), sum(k_lens), D // G
+    q = _randn(Nq + tail, H * Dh, G, seed=seed, dtype=dtype, std=std)
+    k, v = (_randn(Nk + tail, Hk * Dh, G, seed=seed + i, dtype=dtype, std=s) for i, s in ((1, std), (2, 1.0)))
+    do = _randn(Nq + tail, H * Dh, G, seed=seed + 3, dtype=dtype)
+    want, bound = ref.attention(q, k, v, do, q_lens, k_lens, H, Hk, causal)
+    kw = dict(heads=H, kv_heads=Hk, causal=causal, q_offsets=ref.offsets(q_lens, DEV),
+              k_offsets=ref.offsets(k_lens, DEV))
+    qd, kd, vd, dod = (t.to(DEV) for t in (q, k, v, do))
+    o, lse = eq.eqlin_attention_forward(qd, kd, vd, **kw)
+    # the gradients get the definition's o and lse, so that their bounds need not count the forward's
+    o_ref = want["o"].to(dtype).to(DEV)
+    lse_ref = want["lse"].float().to(DEV)
+    dq, dk, dv = eq.eqlin_attention_backward(dod, qd, kd, vd, o_ref, lse_ref, **kw)
+    torch.cuda.synchronize()
+    return {"o": o, "lse": lse, "dq": dq, "dk": dk, "dv": dv}, want, bound
+
+
+def _check_attention(got, want, bound):
+    for name in ("o", "lse", "dq", "dk", "dv"):
+        within(got[name], want[name], bound[name], name)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("lens,H,Hk,D,causal", SELF)
+def test_self_attention(lens, H, Hk, D, causal, dtype):
+    _check_attention(*_attention(lens, lens, H, Hk, D, causal, dtype, seed=len(lens) * 7 + D))
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("q_lens,k_lens,H,Hk,D,causal", CROSS)
+def test_cross_attention(q_lens, k_lens, H, Hk, D, causal, dtype):
+    _check_attention(*_attention(q_lens, k_lens, H, Hk, D, causal, dtype, seed=len(q_lens) + D))
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_attention_with_one_weight_far_above_the_others(dtype):
+    """Scores of several hundred: the running maximum moves far, most weights vanish."""
+    got, want, bound = _attention([150, 260], [150, 260], 2, 2, 64, False, dtype, seed=3, std=6.0)
+    _check_attention(got, want, bound)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("lens", [[49, 3, 20], [130, 5, 260]])
+@pytest.mark.parametrize("causal", [False, True])
+def test_not_a_number_stays_in_its_sequence(lens, causal, dtype):
+    """The middle sequence holds NaN and infinities everywhere; so do the rows behind the last one."""
+    H, D, G = 2, 64, 4
+    n, tail = sum(lens), 9
+    q, k, v, do = (_randn(n + tail, H * D // G, G, seed=i, dtype=dtype) for i in range(4))
+    a, b = lens[0], lens[0] + lens[1]
+    keep = torch.cat([torch.arange(a), torch.arange(b, n)])
+    want, bound = ref.attention(q[keep], k[keep], v[keep], do[keep], [lens[0], lens[2]], [lens[0], lens[2]], H, H, causal)
+    for t in (q, k, v, do):
+        t[a:b] = float("nan")
+        t[n:] = float("inf")
+    off = ref.offsets(lens, DEV)
+    kw = dict(heads=H, causal=causal, q_offsets=off, k_offsets=off)
+    q, k, v, do = (t.to(DEV) for t in (q, k, v, do))
+    mark = [torch.full_like(q, 7.0) for _ in range(4)]
+    lse = torch.full((H, n + tail), 7.0, device=DEV)
+    eq.eqlin_attention_forward(q, k, v, o=mark[0], lse=lse, **kw)
+    o = mark[0].clone()
+    eq.eqlin_attention_backward(do, q, k, v, o, lse, grads=tuple(mark[1:]), **kw)
+    for t in mark:
+        assert (t[n:] == 7).all()                              # rows behind the last sequence: as they were
+        assert t[a:b].isnan().any()
+    assert (lse[:, n:] == 7).all()
+    within(mark[0][keep.to(DEV)], want["o"], bound["o"], "o")
+    within(lse[:, keep.to(DEV)], want["lse"], bound["lse"], "lse")
+    for t, name in zip(mark[1:], ("dq", "dk", "dv")):
+        # the gradients used the GPU's own o and lse: twice the bound covers their distance
+        within(t[keep.to(DEV)], want[name], 3 * bound[name], name)
+
+
+def test_joint_projection_slices():
+    """q, k, v as channel slices of one tensor and gradients into slices of another."""
+    H, Hk, Dh, G = 3, 1, 16, 4
+    lens = [100, 29, 150]
+    n, C = sum(lens), (H + 2 * Hk) * Dh
+    joint = _randn(n, C, G, seed=1, dtype=torch.bfloat16).to(DEV)
+    q, k, v = joint[:, :H * Dh], joint[:, H * Dh:(H + Hk) * Dh], joint[:, (H + Hk) * Dh:]
+    off = ref.offsets(lens, DEV)
+    kw = dict(heads=H, kv_heads=Hk, q_offsets=off, k_offsets=off, causal=True)
+    o, lse = eq.eqlin_attention_forward(q, k, v, **kw)
+    o2, lse2 = eq.eqlin_attention_forward(q.contiguous(), k.contiguous(), v.contiguous(), **kw)
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    wide = torch.zeros(n, H * Dh + 8, G, dtype=torch.bfloat16, device=DEV)
+    eq.eqlin_attention_forward(q, k, v, o=wide[:, 4:4 + H * Dh], **kw)
+    assert torch.equal(wide[:, 4:4 + H * Dh], o) and (wide[:, :4] == 0).all() and (wide[:, 4 + H * Dh:] == 0).all()
+    do = _randn(n, H * Dh, G, seed=2, dtype=torch.bfloat16).to(DEV)
+    dj = torch.zeros_like(joint)
+    grads = (dj[:, :H * Dh], dj[:, H * Dh:(H + Hk) * Dh], dj[:, (H + Hk) * Dh:])
+    eq.eqlin_attention_backward(do, q, k, v, o, lse, grads=grads, **kw)
+    plain = eq.eqlin_attention_backward(do, q.contiguous(), k.contiguous(), v.contiguous(), o, lse, **kw)
+    assert torch.equal(dj, torch.cat(plain, 1))
+    # a single sequence: no offsets
+    one = eq.eqlin_attention_forward(q[:100], k[:100], v[:100], heads=H, kv_heads=Hk, causal=True)[0]
+    within(one, o[:100].double(), 2.0 ** -7 * o[:100].double().abs() + 2.0 ** -9, "one sequence")
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_attention_is_deterministic_and_equivariant(dtype):
+    H, Dh, G = 2, 16, 4
+    lens = [200, 33, 129]
+    n = sum(lens)
+    q, k, v, do = (_randn(n, H * Dh, G, seed=i, dtype=dtype).to(DEV) for i in range(4))
+    off = ref.offsets(lens, DEV)
+    kw = dict(heads=H, q_offsets=off, k_offsets=off)
+    o, lse = eq.eqlin_attention_forward(q, k, v, **kw)
+    g = eq.eqlin_attention_backward(do, q, k, v, o, lse, **kw)
+    for _ in range(3):
+        o2, lse2 = eq.eqlin_attention_forward(q, k, v, **kw)
+        g2 = eq.eqlin_attention_backward(do, q, k, v, o, lse, **kw)
+        assert torch.equal(o, o2) and torch.equal(lse, lse2) and all(torch.equal(a, b) for a, b in zip(g, g2))
+    want, bound = ref.attention(q.cpu(), k.cpu(), v.cpu(), do.cpu(), lens, lens, H, H, False)
+    turned = [t.roll(1, dims=2).contiguous() for t in (q, k, v)]
+    o2, _ = eq.eqlin_attention_forward(*turned, **kw)
+    within(o2, o.roll(1, dims=2).double(), 2 * bound["o"].roll(1, dims=2), "shifted o")
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("bad", [[0, 50, 20, 130], [-5, 40, 90, 130], [10, 60, 200, 300], [130, 0, 130, 0],
+                                 [2 ** 31 - 1, -2 ** 31, 0, 130]])
+def test_bad_offsets_stay_inside_the_tensors(bad, dtype):
+    """Offsets that decrease or point outside are clamped: the call returns, guard rows stay."""
+    n, H, G = 130, 2, 4
+    q, k, v, do = (_randn(n + 8, H * 16, G, seed=i, dtype=dtype).to(DEV) for i in range(4))
+    off = torch.tensor(bad, dtype=torch.int32, device=DEV)
+    kw = dict(heads=H, q_offsets=off, k_offsets=off, causal=True)
+    outs = [torch.full_like(q, 7.0) for _ in range(4)]
+    lse = torch.zeros(H, n, device=DEV)
+    eq.eqlin_attention_forward(q[:n], k[:n], v[:n], o=outs[0][:n], lse=lse, **kw)
+    eq.eqlin_attention_backward(do[:n], q[:n], k[:n], v[:n], outs[0][:n], lse, grads=tuple(t[:n] for t in outs[1:]), **kw)
+    torch.cuda.synchronize()
+    assert all((t[n:] == 7).all() for t in outs)
+
+
+def test_attention_gradient_against_differences():
+    lens, H, Dh, G, D = [7, 5], 2, 4, 2, 8
+    n = sum(lens)
+    ts = [_randn(n, H * Dh, G, seed=i, dtype=torch.float64) for i in range(4)]
+    do = ts[3]
+
+    def f(q, k, v):
+        return float((ref.attention(q, k, v, do, lens, lens, H, H, True)[0]["o"] * do).sum())
+
+    off = ref.offsets(lens, DEV)
+    kw = dict(heads=H, q_offsets=off, k_offsets=off, causal=True)
+    dev = [t.float().to(DEV) for t in ts]
+    o, lse = eq.eqlin_attention_forward(*dev[:3], **kw)
+    grads = eq.eqlin_attention_backward(dev[3], *dev[:3], o, lse, **kw)
+    for which in range(3):
+        for at in ((0, 0, 0), (6, 3, 1), (11, 7, 0), (8, 5, 1)):
+            d = [torch.zeros_like(t) for t in ts[:3]]
+            d[which][at] = 1e-5
+            up, down = f(*(t + e for t, e in zip(ts, d))), f(*(t - e for t, e in zip(ts, d)))
+            # the inputs' rounding to fp32 moves the gradient by about 1e-6, the differences by 1e-9
+            assert abs((up - down) / 2e-5 - grads[which][at].item()) < 2e-5
+
+
+def test_streams_graphs_and_two_calls_at_once():
+    """A captured call replayed on new inputs, and two calls in flight on two streams."""
+    H, Dh, G = 4, 16, 4
+    lens = [150, 49, 128, 1]
+    n = sum(lens)
+    off = ref.offsets(lens, DEV)
+    kw = dict(heads=H, q_offsets=off, k_offsets=off, causal=True)
+    make = lambda s: [_randn(n, H * Dh, G, seed=s + i, dtype=torch.bfloat16).to(DEV) for i in range(4)]   # noqa: E731
+    w = _randn(H * Dh, seed=1, dtype=torch.float32).to(DEV)
+    pos = torch.randint(0, 20, (n, 2), dtype=torch.int32).to(DEV)
+
+    def step(q, k, v, do):
+        q2 = eq.eqlin_rope(q, pos, heads=H, sections=(4, 4))
+        o, lse = eq.eqlin_attention_forward(q2, k, v, **kw)
+        y, r = eq.eqlin_add_rmsnorm(o, q, w)
+        dr, dw = eq.eqlin_rmsnorm_backward(do, r, w)
+        return (o, y, dr, dw) + eq.eqlin_attention_backward(dr, q2, k, v, o, lse, **kw)
+
+    a, b = make(10), make(20)
+    want_a, want_b = [t.clone() for t in step(*a)], [t.clone() for t in step(*b)]
+    static = [t.clone() for t in a]
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = step(*static)
+    for x, want in ((a, want_a), (b, want_b), (a, want_a)):
+        for s, t in zip(static, x):
+            s.copy_(t)
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(u, v) for u, v in zip(out, want))
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(5):
+        with torch.cuda.stream(s1):
+            o1 = step(*a)
+        with torch.cuda.stream(s2):
+            o2 = step(*b)
+        torch.cuda.synchronize()
+        assert all(torch.equal(u, v) for u, v in zip(o1, want_a))
+        assert all(torch.equal(u, v) for u, v in zip(o2, want_b))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_transformer_block(dtype):
+    """norm -> joint projection -> rotary positions -> attention -> projection -> add and norm, forward
+    and gradients, through the layers and the operators together, against float64."""
+    import oracle
+    C, G, H, lens = 32, 4, 4, [49, 30, 130]
+    n, Dh, eps = sum(lens), C // H, 1e-6
+    x = _randn(n, C, G, seed=1, dtype=dtype)
+    w1, w2 = _randn(C, seed=2, dtype=dtype, std=0.2) + 1, _randn(C, seed=3, dtype=dtype, std=0.2) + 1
+    wqkv = _randn(3 * C, C, G, seed=4, dtype=dtype, std=(C * G) ** -0.5)
+    wo = _randn(C, C, G, seed=5, dtype=dtype, std=(C * G) ** -0.5)
+    dz = _randn(n, C, G, seed=6, dtype=dtype)
+    side = 7
+    pos = torch.stack([torch.arange(n) // side, torch.arange(n) % side], 1).to(torch.int32)
+    off = ref.offsets(lens, DEV)
+    qkv_layer = eq.prepare(wqkv.to(DEV), None, io_dtype=dtype, backward=True)
+    out_layer = eq.prepare(wo.to(DEV), None, io_dtype=dtype, backward=True)
+    d = lambda t: t.to(DEV)   # noqa: E731
+    rope = dict(heads=2 * H, sections=(Dh // 4, Dh // 4), base=100.0)
+    att = dict(heads=H, q_offsets=off, k_offsets=off)
+    # forward
+    y, r = eq.eqlin_add_rmsnorm(d(x), None, d(w1), eps=eps)
+    joint = qkv_layer.forward(y)
+    qk, v = joint[:, :2 * C], joint[:, 2 * C:]
+    eq.eqlin_rope(qk, d(pos), out=qk, **rope)
+    o, lse = eq.eqlin_attention_forward(qk[:, :C], qk[:, C:], v, **att)
+    a = out_layer.forward(o)
+    z, r2 = eq.eqlin_add_rmsnorm(a, r, d(w2), eps=eps)
+    # gradients
+    dr2, dw2 = eq.eqlin_rmsnorm_backward(d(dz), r2, d(w2), eps=eps)
+    do = out_layer.backward_dx(dr2)
+    dwo, _ = out_layer.backward_dw(o, dr2, with_bias=False)
+    dj = torch.empty_like(joint)
+    eq.eqlin_attention_backward(do, qk[:, :C], qk[:, C:], v, o, lse, grads=(dj[:, :C], dj[:, C:2 * C], dj[:, 2 * C:]), **att)
+    eq.eqlin_rope(dj[:, :2 * C], d(pos), out=dj[:, :2 * C], inverse=True, **rope)
+    dy = qkv_layer.backward_dx(dj)
+    dwqkv, _ = qkv_layer.backward_dw(y, dj, with_bias=False)
+    dx, dw1 = eq.eqlin_rmsnorm_backward(dy, r, d(w1), dsum=dr2, eps=eps)
+    torch.cuda.synchronize()
+    # the same in float64, with autograd's gradients
+    X, W1, W2, Q, O = (t.double().requires_grad_() for t in (x, w1, w2, wqkv, wo))
+    shift = torch.tensor([[(g - h) % G for h in range(G)] for g in range(G)])
+
+    def layer(t, w):
+        return torch.einsum("oigh,nih->nog", w[:, :, shift], t)
+
+    def norm(t, w):
+        return t / torch.sqrt((t * t).mean((1, 2), keepdim=True) + eps) * w[None, :, None]
+
+    angle = torch.cat([pos[:, i:i + 1].double() * torch.tensor([100.0 ** (-j / (Dh // 4)) for j in range(Dh // 4)],
+                                                               dtype=torch.float64) for i in range(2)], 1)
+    cos, sin = angle.cos()[:, None, :, None], angle.sin()[:, None, :, None]
+
+    def turn(t):
+        t = t.reshape(n, H, 2, Dh // 2, G)
+        p, q = t[:, :, 0], t[:, :, 1]
+        return torch.stack([p * cos - q * sin, q * cos + p * sin], 2).reshape(n, H, Dh * G)
+
+    J = layer(norm(X, W1), Q)
+    qq, kk, vv = turn(J[:, :C]), turn(J[:, C:2 * C]), J[:, 2 * C:].reshape(n, H, Dh * G)
+    parts, at = [], 0
+    for L in lens:
+        s = torch.einsum("ihd,jhd->hij", qq[at:at + L], kk[at:at + L]) / math.sqrt(Dh * G)
+        parts.append(torch.einsum("hij,jhd->ihd", s.softmax(-1), vv[at:at + L]))
+        at += L
+    R2 = layer(torch.cat(parts).reshape(n, C, G), O) + X
+    Z = norm(R2, W2)
+    (Z * dz.double()).sum().backward()
+    assert abs(float(torch.from_numpy(oracle.forward(x, wo, None)).sub(layer(x.double(), wo.double())).abs().max())) < 1e-9
+    # normwise: each stage rounds its output (u) and its 16-bit operands (2 u); the longest way back
+    # passes 12 stages, whose errors add at most linearly: 12 * 3 u = 0.14 in the worst case for
+    # bf16; independent roundings add by root sum of squares, 6 u * sqrt(12) = 0.08 at three
+    # times their expected size; fp32 stages: 1e-6 each
+    tol = 6 * ref.unit(dtype) * math.sqrt(12) if dtype != torch.float32 else 12 * 2e-6
+    for name, got, want in (("z", z, Z), ("dx", dx, X.grad), ("dw1", dw1, W1.grad), ("dw2", dw2, W2.grad),
+                            ("dwqkv", dwqkv, Q.grad), ("dwo", dwo, O.grad)):
+        err = float((got.double().cpu() - want.detach()).norm() / want.detach().norm())
+        assert err <= tol, (name, err, tol)
+    qkv_layer.close()
+    out_layer.close()
