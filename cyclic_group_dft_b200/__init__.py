@@ -84,6 +84,7 @@ _BLOCK_EXPORTS = (
     "eqlin_rope",
     "eqlin_attention_forward",
     "eqlin_attention_backward",
+    "eqlin_attention_device_status",
 )
 
 __all__ = list(_EXPORTS) + list(_BLOCK_EXPORTS) + ["prepare", "workloads"]

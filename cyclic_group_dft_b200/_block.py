@@ -35,7 +35,8 @@ _lib.eqlin_attention_workspace_size.argtypes = [ctypes.POINTER(_AttentionShape),
 _lib.eqlin_attention_forward.argtypes = [ctypes.POINTER(_AttentionShape)] + [_vp] * 6 + [_sz, _vp]
 _lib.eqlin_attention_backward.argtypes = ([ctypes.POINTER(_AttentionShape), ctypes.POINTER(_GradStrides)]
                                           + [_vp] * 10 + [_sz, _vp])
-for _f in ("eqlin_add_rmsnorm", "eqlin_add_rmsnorm_fp8", "eqlin_rmsnorm_backward_workspace_size",
+_lib.eqlin_attention_device_status.argtypes = [ctypes.POINTER(_int)]
+for _f in ("eqlin_attention_device_status", "eqlin_add_rmsnorm", "eqlin_add_rmsnorm_fp8", "eqlin_rmsnorm_backward_workspace_size",
            "eqlin_rmsnorm_backward", "eqlin_rope", "eqlin_attention_workspace_size", "eqlin_attention_forward",
            "eqlin_attention_backward"):
     getattr(_lib, _f).restype = _int
@@ -314,3 +315,12 @@ def eqlin_attention_backward(do: torch.Tensor, q: torch.Tensor, k: torch.Tensor,
                                              0 if workspace is None else workspace.numel(), _stream_ptr(stream)),
                "eqlin_attention_backward")
     return dq, dk, dv
+
+
+def eqlin_attention_device_status(device=None) -> int:
+    """Synchronises the device (default: the current one), then reads and clears its word for errors of
+    the attention kernels: EQLIN_OK, or EQLIN_ERR_TIMEOUT when a wait inside one ran out."""
+    v = _int()
+    with torch.cuda.device(torch.cuda.current_device() if device is None else device):
+        _check(_lib.eqlin_attention_device_status(ctypes.byref(v)), "eqlin_attention_device_status")
+    return int(v.value)

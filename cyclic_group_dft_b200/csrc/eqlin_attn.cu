@@ -3,8 +3,13 @@
 #include <algorithm>
 #include <cmath>
 
+#include <cudaTypedefs.h>
+
+#include <mutex>
+
 #include "eqlin_attn.cuh"
 #include "eqlin_attn_f32.cuh"
+#include "eqlin_attn_tc.cuh"
 #include "eqlin_host_util.h"
 
 namespace {
@@ -66,6 +71,80 @@ void fill(const eqlin_attention_shape* a, attn::Params& p) {
     p.D = static_cast<int>(a->head_dim);
     p.causal = a->causal;
     p.scale = a->scale;
+}
+
+// ---------------------------------------------------------------- tensor cores (16-bit I/O)
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        void* f = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) ==
+                cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+    });
+    return fn;
+}
+
+// Tensor [rows][heads][D], rows `stride` features apart, read in boxes of 64 features of one head and
+// 128 rows with 128-byte swizzle.  Coordinates are (0 or 64, head, row): every copy starts on a
+// 16-byte boundary.  What lies outside the tensor, features past D among it, reads as zero.
+int encode_map(const void* t, int64_t rows, int64_t heads, int64_t D, int64_t stride, int io, CUtensorMap* map) {
+    auto encode = tensor_map_encoder();
+    if (!encode) return report(EQLIN_ERR_CUDA, "cuTensorMapEncodeTiled is unavailable");
+    cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(heads), static_cast<cuuint64_t>(rows)};
+    cuuint64_t strides[2] = {static_cast<cuuint64_t>(D * 2), static_cast<cuuint64_t>(stride * 2)};
+    cuuint32_t box[3] = {64, 1, static_cast<cuuint32_t>(attn::tc::kTile)};
+    cuuint32_t estr[3] = {1, 1, 1};
+    const CUresult r = encode(map, io == EQLIN_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+                              const_cast<void*>(t), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? EQLIN_OK : report(EQLIN_ERR_CUDA, "cuTensorMapEncodeTiled failed");
+}
+
+// Grid of `heads` blocks for each slot, or an error where that is more than a launch takes.
+int tc_grid(int64_t rows, int64_t sequences, int m, int64_t heads, unsigned* grid) {
+    const int64_t n = (rows / m + sequences) * heads;
+    if (n >= (int64_t(1) << 31)) return report(EQLIN_ERR_UNSUPPORTED, "too many rows, sequences and heads for one call");
+    *grid = static_cast<unsigned>(n);
+    return EQLIN_OK;
+}
+
+// Limits of the bounded waits; EQLIN_WAIT_TIMEOUT_MS and the test hook EQLIN_TEST_STOP_AFTER (the load
+// warp stops after that many tiles, so that the waits run out) are read on each call.
+unsigned long long wait_timeout_ns() {
+    const char* t = std::getenv("EQLIN_WAIT_TIMEOUT_MS");
+    const long long ms = t ? std::atoll(t) : 0;
+    return ms > 0 ? static_cast<unsigned long long>(ms) * 1000000ull : 2000000000ull;
+}
+long long stop_after() {
+    const char* t = std::getenv("EQLIN_TEST_STOP_AFTER");
+    return t ? std::atoll(t) : -1;
+}
+
+template <class T, int DP, int NQ>
+int forward_tc(attn::tc::FwdParams fp, int io, cudaStream_t st) {
+    using F = attn::tc::Fwd<DP, NQ>;
+    attn::Params& p = fp.p;
+    CUtensorMap mq, mk, mv;
+    unsigned grid = 0;
+    int s = tc_grid(p.q_rows, p.sequences, NQ * attn::tc::kTile, p.heads, &grid);
+    if (s == EQLIN_OK) s = encode_map(p.q, p.q_rows, p.heads, p.D, p.q_stride, io, &mq);
+    mk = mv = mq;   // without keys neither is read
+    if (s == EQLIN_OK && p.k_rows > 0) s = encode_map(p.k, p.k_rows, p.kv_heads, p.D, p.k_stride, io, &mk);
+    if (s == EQLIN_OK && p.k_rows > 0) s = encode_map(p.v, p.k_rows, p.kv_heads, p.D, p.v_stride, io, &mv);
+    if (s != EQLIN_OK) return s;
+    return launch(attn::tc::eqlin_attn_fwd_tc_kernel<T, DP, NQ>, dim3(grid), dim3(F::THREADS), F::SMEM, st,
+                  "attention launch", mq, mk, mv, fp);
+}
+template <class T>
+int forward_16(attn::Params& p, int io, cudaStream_t st) {
+    p.timeout_ns = wait_timeout_ns();
+    attn::tc::FwdParams fp = {p, stop_after()};
+    return p.D <= 64 ? forward_tc<T, 64, 1>(fp, io, st) : forward_tc<T, 128, 2>(fp, io, st);
 }
 
 template <class T, int DP>
@@ -149,7 +228,20 @@ int eqlin_attention_forward(const eqlin_attention_shape* shape, const void* q, c
     p.lse = lse;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (a.io_dtype == EQLIN_F32) return forward_t<float>(p, st);
-    return a.io_dtype == EQLIN_F16 ? forward_t<__half>(p, st) : forward_t<__nv_bfloat16>(p, st);
+    return a.io_dtype == EQLIN_F16 ? forward_16<__half>(p, a.io_dtype, st) : forward_16<__nv_bfloat16>(p, a.io_dtype, st);
+}
+
+int eqlin_attention_device_status(int* status_out) {
+    if (!status_out) return report(EQLIN_ERR_INVALID_ARG, "NULL argument");
+    cudaError_t e = cudaDeviceSynchronize();
+    if (e != cudaSuccess) return eqlin::report_cuda(e, "cudaDeviceSynchronize");
+    int v = 0;
+    const int zero = 0;
+    if ((e = cudaMemcpyFromSymbol(&v, attn::g_status, sizeof(v))) != cudaSuccess ||
+        (e = cudaMemcpyToSymbol(attn::g_status, &zero, sizeof(zero))) != cudaSuccess)
+        return eqlin::report_cuda(e, "status read");
+    *status_out = v;
+    return EQLIN_OK;
 }
 
 int eqlin_attention_backward(const eqlin_attention_shape* shape, const eqlin_attention_grad_strides* strides,

@@ -31,7 +31,6 @@ struct Params {
     int q_rows, k_rows, sequences, heads, kv_heads, D;
     int causal;
     float scale;
-    int* status;                   // device status word (bounded waits)
     unsigned long long timeout_ns;
 };
 

@@ -1,0 +1,454 @@
+// eqlin_attn_tc.cuh -- 16-bit attention on the tcgen05 tensor cores: what the forward and the
+// gradient kernels share, and the forward.
+//
+// Operands in shared memory are tiles of 128 token rows, one box of 64 features (128 bytes) after the
+// other, as a TMA load with 128-byte swizzle leaves them.  The same tile serves a product over
+// features (K-major: rows are the M or N index) and a product over tokens (MN-major: rows are the K
+// index).  Features past the head's end arrive as zeros.
+#pragma once
+
+#include <cuda.h>
+
+#include "eqlin_attn.cuh"
+
+namespace eqlin {
+namespace attn {
+
+// Error word of this library's attention kernels on a device (bounded waits that ran out).
+__device__ int g_status;
+
+namespace tc {
+
+constexpr int kTile = 128;                       // token rows of an operand tile
+constexpr int kBoxBytes = kTile * 128;           // one box: 128 rows of 64 features
+constexpr int kErrTimeout = -6;                  // EQLIN_ERR_TIMEOUT
+constexpr uint32_t kWaitSleepNs = 20000;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+struct Ctl {
+    volatile int abort;
+    uint32_t tmem_base;
+};
+
+// Bounded mbarrier wait.  Returns false (after flagging) on timeout or abort.
+__device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, Ctl* ctl, unsigned long long timeout_ns) {
+    if (ptx::mbar_try_wait(bar, parity)) return true;
+    const uint64_t t0 = ptx::globaltimer_ns();
+    for (uint32_t spin = 1;; ++spin) {
+        if (ptx::mbar_try_wait_sleep(bar, parity, kWaitSleepNs)) return true;
+        if ((spin & 7u) == 0) {
+            if (ctl->abort) return false;
+            if (ptx::globaltimer_ns() - t0 > timeout_ns) {
+                ctl->abort = 1;
+                atomicCAS(&g_status, 0, kErrTimeout);
+                return false;
+            }
+        }
+    }
+}
+// The same for a whole warp: one answer for all lanes, which are together again afterwards.
+__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, Ctl* ctl, unsigned long long timeout_ns) {
+    return __all_sync(0xFFFFFFFFu, wait_bounded(bar, parity, ctl, timeout_ns));
+}
+// Bounded wait that ignores the abort flag, for copies or MMAs in flight before exit.
+__device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity, unsigned long long timeout_ns) {
+    const uint64_t t0 = ptx::globaltimer_ns();
+    while (!ptx::mbar_try_wait(bar, parity)) {
+        if (ptx::globaltimer_ns() - t0 > timeout_ns) {
+            atomicCAS(&g_status, 0, kErrTimeout);
+            return;
+        }
+    }
+}
+
+// 3-D tiled TMA load of a box (feature, head, row).
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* m, int32_t c0, int32_t c1, int32_t c2,
+                                            uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(m)), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
+        : "memory");
+}
+// D[tmem] (+)= A[tmem] * B[smem], kind::f16; A: lane = row, two K elements per 32-bit column.
+__device__ __forceinline__ void umma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                            uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+        "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+        "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+        "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Descriptors of a tile, split in halves (the low half carries the start address >> 4).
+//   K-major SWIZZLE_128B: 8-row groups 1 KB apart; 16 features further: + 32 bytes; box: + 16 KB.
+//   MN-major SWIZZLE_128B: K groups of 8 rows 1 KB apart, the next 64 features one box (16 KB) on;
+//   16 rows further: + 2 KB.
+__device__ __forceinline__ uint64_t desc_k(uint32_t start) {
+    constexpr uint32_t hi = (1024u >> 4) | (1u << 14) | (2u << 29);
+    return (static_cast<uint64_t>(hi) << 32) | (1u << 16) | (start >> 4);
+}
+__device__ __forceinline__ uint64_t desc_mn(uint32_t start) {
+    constexpr uint32_t hi = (1024u >> 4) | (1u << 14) | (2u << 29);
+    return (static_cast<uint64_t>(hi) << 32) | ((static_cast<uint32_t>(kBoxBytes) >> 4) << 16) | (start >> 4);
+}
+// D[128 x 128] = A B^T over `steps` * 16 features, both tiles K-major.
+__device__ __forceinline__ void mma_features(uint32_t d, uint32_t a, uint32_t b, int steps, uint32_t idesc) {
+    for (int s = 0; s < steps; ++s) {
+        const uint32_t off = static_cast<uint32_t>(s >> 2) * kBoxBytes + static_cast<uint32_t>(s & 3) * 32;
+        ptx::umma_f16(d, desc_k(a + off), desc_k(b + off), idesc, s > 0);
+    }
+}
+// D[128 x N] (+)= A[tmem, 128 x 128] B over the 128 rows of tile b.
+__device__ __forceinline__ void mma_rows(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool add, int s0 = 0,
+                                         int s1 = 8) {
+    for (int s = s0; s < s1; ++s)
+        umma_f16_ts(d, a + s * 8, desc_mn(b + s * 2048), idesc, add || s > 0);
+}
+constexpr uint32_t kBMnMajor = 1u << 16;         // instruction descriptor: B is MN-major
+
+// Rows [valid, 128) of a tile as zeros (all lanes of one warp): a row of another sequence would turn a
+// weight of zero into NaN if it holds an infinity or NaN.
+__device__ __forceinline__ void zero_tail(uint8_t* tile, int boxes, int valid, int lane) {
+    for (int b = 0; b < boxes; ++b)
+        for (int i = valid * 8 + lane; i < kTile * 8; i += 32)
+            *reinterpret_cast<uint4*>(tile + b * kBoxBytes + i * 16) = make_uint4(0, 0, 0, 0);
+    ptx::fence_proxy_async_smem();
+    __syncwarp();
+}
+
+// ------------------------------------------------------------------------------------- forward
+//
+// A block takes NQ tiles of 128 query rows of one head and walks their keys in tiles of 128.  Warps:
+// NQ warpgroups of softmax (thread = query row = TMEM lane), one warp of loads, one of MMAs.
+//   S_i = Q_i K^T                      (SS product, fp32 in TMEM)
+//   m, l running maximum and sum; P = exp2(c (S - m)) rounded to the I/O type, over S in TMEM
+//   O_i += P V                         (A from TMEM)
+// The maximum that P refers to moves only when the true one has grown by more than 2^8: until then
+// P stays below 2^8, and the rescaling of O (a round trip through registers) is rarely needed.
+// With two query tiles the tensor cores work on one while the other's softmax runs.
+template <int DP, int NQ>
+struct Fwd {
+    static constexpr int BOXES = DP / 64;
+    static constexpr int TILE_BYTES = BOXES * kBoxBytes;
+    // D <= 64: two blocks per SM, each with half of the TMEM and at most 113 KB of shared memory
+    static constexpr int STAGES = NQ == 2 ? (227 * 1024 - 2048) / TILE_BYTES - NQ : 4;
+    static constexpr int THREADS = NQ * 128 + 64;
+    static constexpr int WARP_LOAD = NQ * 4, WARP_MMA = NQ * 4 + 1;
+    static constexpr int TMEM_COLS = NQ * (128 + DP) <= 256 ? 256 : 512;
+    static constexpr size_t SMEM = 1024 + 512 + static_cast<size_t>(STAGES + NQ) * TILE_BYTES;
+};
+
+struct FwdParams {
+    Params p;
+    long long stop_after;    // test hook: the load warp stops after this many tiles; -1 off
+};
+
+template <class T, int DP, int NQ>
+__global__ void __launch_bounds__(Fwd<DP, NQ>::THREADS, NQ == 2 ? 1 : 2)
+    eqlin_attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
+                             const __grid_constant__ CUtensorMap mv, const __grid_constant__ FwdParams fp) {
+    using F = Fwd<DP, NQ>;
+    constexpr int ST = F::STAGES;
+    const Params& p = fp.p;
+    extern __shared__ uint8_t raw[];
+    uint8_t* base = ptx::smem_align_1k(raw);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(base + (F::STAGES + NQ) * F::TILE_BYTES);
+    Ctl* ctl = reinterpret_cast<Ctl*>(bars + 48);
+    auto bar = [&](int i) { return ptx::smem_u32(bars + i); };
+    // barriers: [0, ST) full, [ST, 2 ST) empty, then per query tile: q, s, p, o
+    auto full = [&](int s) { return bar(s); };
+    auto empty = [&](int s) { return bar(ST + s); };
+    auto q_full = [&](int i) { return bar(2 * ST + i); };
+    auto s_full = [&](int i) { return bar(2 * ST + NQ + i); };
+    auto p_full = [&](int i) { return bar(2 * ST + 2 * NQ + i); };
+    auto o_full = [&](int i) { return bar(2 * ST + 3 * NQ + i); };
+    const uint32_t drained = bar(2 * ST + 4 * NQ);
+    uint8_t* q_tile = base;
+    uint8_t* ring = base + NQ * F::TILE_BYTES;
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        ctl->abort = 0;
+        for (int s = 0; s < ST; ++s) {
+            ptx::mbar_init(full(s), 1);
+            ptx::mbar_init(empty(s), 1);
+        }
+        for (int i = 0; i < NQ; ++i) {
+            ptx::mbar_init(q_full(i), 1);
+            ptx::mbar_init(s_full(i), 1);
+            ptx::mbar_init(p_full(i), 128);
+            ptx::mbar_init(o_full(i), 1);
+        }
+        ptx::mbar_init(drained, 1);
+        ptx::fence_mbar_init();
+    }
+    if (warp == F::WARP_MMA) {
+        ptx::tmem_alloc(ptx::smem_u32(&ctl->tmem_base), F::TMEM_COLS);
+        ptx::tmem_relinquish();
+    }
+    ptx::grid_dependency_wait();
+
+    // Heads vary fastest; the slots of a causal call run backwards, so that the tiles with the most
+    // keys start first.
+    const int h = blockIdx.x % p.heads, hk = h / (p.heads / p.kv_heads);
+    const int n_slots = gridDim.x / p.heads;
+    const int slot = p.causal ? n_slots - 1 - blockIdx.x / p.heads : blockIdx.x / p.heads;
+    const Tile t = find_tile<NQ * kTile>(p.q_offsets, p.sequences, p.q_rows, slot);
+    const Rows kr = sequence_rows(p.k_offsets, t.b, p.k_rows);
+    const int r0 = t.tile * NQ * kTile;
+    int count[NQ], n = 0;     // key tiles of each query tile
+#pragma unroll
+    for (int i = 0; i < NQ; ++i) {
+        const int rows = t.tile < 0 ? 0 : min(kTile, t.own.len - r0 - i * kTile);
+        count[i] = rows <= 0 ? 0
+                             : (keys_seen(r0 + i * kTile + rows - 1, t.own.len, kr.len, p.causal) + kTile - 1) / kTile;
+        n = max(n, count[i]);
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    // only now: a dependent block that took this SM's TMEM first would wait for this grid, and this
+    // block for the TMEM
+    ptx::grid_launch_dependents();
+    const uint32_t tmem = ctl->tmem_base;
+    auto t_s = [&](int i) { return tmem + i * 128; };
+    auto t_o = [&](int i) { return tmem + NQ * 128 + i * DP; };
+
+    if (warp == F::WARP_LOAD) {
+        if (lane == 0 && n > 0) {
+            long long issued = 0;
+            bool ok = true;
+            auto load = [&](const CUtensorMap* m, uint8_t* dst, int head, int row, uint32_t b) {
+                ptx::mbar_arrive_expect_tx(b, F::TILE_BYTES);
+                for (int x = 0; x < F::BOXES; ++x)
+                    tma_load_3d(ptx::smem_u32(dst) + x * kBoxBytes, m, x * 64, head, row, b);
+            };
+            for (int i = 0; i < NQ; ++i)
+                if (count[i] > 0) load(&mq, q_tile + i * F::TILE_BYTES, h, t.own.start + r0 + i * kTile, q_full(i));
+            for (int u = 0; ok && u < 2 * n; ++u) {      // K_0, V_0, K_1, V_1, ...
+                const int s = u % ST;
+                if (u >= ST && !wait_bounded(empty(s), ((u / ST) & 1) ^ 1, ctl, p.timeout_ns)) break;
+                if (issued == fp.stop_after) break;
+                load(u & 1 ? &mv : &mk, ring + s * F::TILE_BYTES, hk, kr.start + (u >> 1) * kTile, full(s));
+                ++issued;
+            }
+            // every copy must land before the block's shared memory is given up
+            for (int i = 0; i < NQ; ++i)
+                if (count[i] > 0) drain_wait(q_full(i), 0, p.timeout_ns);
+            for (int s = 0; s < ST; ++s) {
+                const long long times = issued > s ? (issued - s + ST - 1) / ST : 0;
+                if (times > 0) drain_wait(full(s), static_cast<uint32_t>((times - 1) & 1), p.timeout_ns);
+            }
+        }
+    } else if (warp == F::WARP_MMA) {
+        if (n > 0) {
+            const uint32_t id_s = idesc_f16kind_f32(128, 128, Io16<T>::kUmmaFormat, false);
+            const uint32_t id_o = idesc_f16kind_f32(128, (p.D + 15) / 16 * 16, Io16<T>::kUmmaFormat, false) | kBMnMajor;
+            const int steps = (p.D + 15) / 16;
+            bool ok = true;
+            auto stage = [&](int u) { return ring + (u % ST) * F::TILE_BYTES; };
+            auto wait_stage = [&](int u) { return wait_warp(full(u % ST), (u / ST) & 1, ctl, p.timeout_ns); };
+            auto scores = [&](int i, int u) {
+                if (lane == 0) {
+                    mma_features(t_s(i), ptx::smem_u32(q_tile + i * F::TILE_BYTES), ptx::smem_u32(stage(u)), steps, id_s);
+                    ptx::umma_commit(s_full(i));
+                }
+                __syncwarp();
+            };
+            ok = wait_stage(0);
+#pragma unroll
+            for (int i = 0; i < NQ; ++i)
+                if (ok && count[i] > 0) {
+                    ok = wait_warp(q_full(i), 0, ctl, p.timeout_ns);
+                    ptx::tc_fence_after();
+                    if (ok) scores(i, 0);
+                }
+            if (ok && lane == 0) ptx::umma_commit(empty(0));
+            for (int j = 0; ok && j < n; ++j) {
+                bool have_v = false, have_k = false;
+#pragma unroll
+                for (int i = 0; i < NQ; ++i) {
+                    if (!ok || j >= count[i]) continue;
+                    if (!have_v) {
+                        have_v = true;
+                        if (!(ok = wait_stage(2 * j + 1))) break;
+                        const int valid = kr.len - j * kTile;
+                        if (valid < kTile) zero_tail(stage(2 * j + 1), F::BOXES, valid, lane);
+                    }
+                    if (!(ok = wait_warp(p_full(i), j & 1, ctl, p.timeout_ns))) break;
+                    ptx::tc_fence_after();
+                    if (lane == 0) {
+                        mma_rows(t_o(i), t_s(i), ptx::smem_u32(stage(2 * j + 1)), id_o, j > 0);
+                        ptx::umma_commit(o_full(i));
+                    }
+                    __syncwarp();
+                    if (j + 1 < count[i]) {
+                        // S_i is written after the product above has read P_i out of it: MMAs of one
+                        // thread run in order
+                        if (!have_k) {
+                            have_k = true;
+                            if (!(ok = wait_stage(2 * j + 2))) break;
+                            ptx::tc_fence_after();
+                        }
+                        scores(i, 2 * j + 2);
+                    }
+                }
+                if (ok && lane == 0) {
+                    ptx::umma_commit(empty((2 * j + 1) % ST));
+                    if (j + 1 < n) ptx::umma_commit(empty((2 * j + 2) % ST));
+                }
+            }
+            // every MMA, and every arrival that one owes a barrier, before shared memory and TMEM go
+            if (lane == 0) {
+                ptx::umma_commit(drained);
+                drain_wait(drained, 0, p.timeout_ns);
+            }
+            __syncwarp();
+        }
+    } else {
+        const int i = NQ == 1 ? 0 : warp >> 2;
+        const int cnt = NQ == 1 ? count[0] : (i == 0 ? count[0] : count[NQ - 1]);
+        const int row = r0 + i * kTile + (threadIdx.x & 127);      // row of the sequence
+        const bool live = t.tile >= 0 && row < t.own.len;
+        const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+        const uint32_t ts = t_s(i) + lanes, to = t_o(i) + lanes;
+        // keys this row sees
+        const int seen = live ? keys_seen(row, t.own.len, kr.len, p.causal) : 0;
+        // keys that every row of the tile sees: tiles below need no mask
+        const int seen_all = p.causal ? keys_seen(r0 + i * kTile, t.own.len, kr.len, 1) : kr.len;
+        const float c2 = p.scale * kLog2e;
+        float top = -INFINITY, sum = 0.f;
+        bool ok = true;
+        for (int j = 0; j < cnt; ++j) {
+            if (!(ok = wait_warp(s_full(i), j & 1, ctl, p.timeout_ns))) break;
+            ptx::tc_fence_after();
+            uint32_t s[4][32];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) ptx::tmem_ld_32x32b<32>(ts + c * 32, s[c]);
+            ptx::tmem_wait_ld();
+#pragma unroll
+            for (int c = 0; c < 4; ++c) ptx::tmem_regs_ready(s[c]);
+            if ((j + 1) * kTile > seen_all) {
+                const int n_seen = seen - j * kTile;
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        if (c * 32 + e >= n_seen) s[c][e] = 0xFF800000u;
+            }
+            float m0 = -INFINITY, m1 = -INFINITY, m2 = -INFINITY, m3 = -INFINITY;
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+                m0 = fmaxf(m0, __uint_as_float(s[0][e]));
+                m1 = fmaxf(m1, __uint_as_float(s[1][e]));
+                m2 = fmaxf(m2, __uint_as_float(s[2][e]));
+                m3 = fmaxf(m3, __uint_as_float(s[3][e]));
+            }
+            const float m = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3));
+            bool move = (m - top) * c2 > 8.f;                       // also the first finite maximum
+            if (j == 0) {
+                top = m;
+            } else if (__any_sync(0xFFFFFFFFu, move)) {
+                // O must be at rest: the product of the tile before is done
+                if (!(ok = wait_warp(o_full(i), (j - 1) & 1, ctl, p.timeout_ns))) break;
+                ptx::tc_fence_after();
+                const float fade = move ? ex2((top - m) * c2) : 1.f;   // 0 while top is -infinity
+                if (move) top = m;
+                sum *= fade;
+                for (int c = 0; c < p.D; c += 16) {
+                    uint32_t o[16];
+                    ptx::tmem_ld_32x32b<16>(to + c, o);
+                    ptx::tmem_wait_ld();
+                    ptx::tmem_regs_ready(o);
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * fade);
+                    tmem_st16(to + c, o);
+                }
+            }
+            const float off = top == -INFINITY ? 0.f : -top * c2;
+            float part[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                uint32_t w[16];
+#pragma unroll
+                for (int e = 0; e < 32; e += 2) {
+                    const float a = ex2(fmaf(__uint_as_float(s[c][e]), c2, off));
+                    const float b = ex2(fmaf(__uint_as_float(s[c][e + 1]), c2, off));
+                    part[(e >> 1) & 3] += a + b;
+                    w[e >> 1] = Io16<T>::pack(a, b);
+                }
+                tmem_st16(ts + c * 16, w);
+            }
+            sum += (part[0] + part[1]) + (part[2] + part[3]);
+            tmem_wait_st();
+            ptx::tc_fence_before();
+            ptx::mbar_arrive(p_full(i));
+        }
+        if (ok && cnt > 0) ok = wait_warp(o_full(i), (cnt - 1) & 1, ctl, p.timeout_ns);
+        if (ok && t.tile >= 0) {
+            ptx::tc_fence_after();
+            const float inv = sum == 0.f ? 0.f : 1.f / sum;        // a row that sees no key
+            const long long at = static_cast<long long>(t.own.start) + row;
+            if (live && p.lse)
+                p.lse[static_cast<long long>(h) * p.q_rows + at] =
+                    sum == 0.f ? -INFINITY : fmaf(top * p.scale, 1.f, logf(sum));
+            T* out = static_cast<T*>(p.out) + at * p.o_stride + static_cast<long long>(h) * p.D;
+            for (int c = 0; c < p.D; c += 16) {
+                uint32_t o[16] = {};
+                if (cnt > 0) {
+                    ptx::tmem_ld_32x32b<16>(to + c, o);
+                    ptx::tmem_wait_ld();
+                    ptx::tmem_regs_ready(o);
+                }
+                if (!live) continue;
+#pragma unroll
+                for (int e = 0; e < 16; e += 8) {
+                    if (c + e >= p.D) break;
+                    uint32_t w[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        w[k] = Io16<T>::pack(__uint_as_float(o[e + 2 * k]) * inv, __uint_as_float(o[e + 2 * k + 1]) * inv);
+                    *reinterpret_cast<uint4*>(out + c + e) = make_uint4(w[0], w[1], w[2], w[3]);
+                }
+            }
+        }
+        ptx::tc_fence_before();
+    }
+    __syncthreads();
+    if (warp == F::WARP_MMA) {
+        ptx::tc_fence_after();
+        ptx::tmem_dealloc(tmem, F::TMEM_COLS);
+    }
+}
+
+}  // namespace tc
+}  // namespace attn
+}  // namespace eqlin

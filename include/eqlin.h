@@ -535,6 +535,12 @@ EQLIN_API int eqlin_attention_backward(const eqlin_attention_shape* shape, const
                                        const void* dout, const void* q, const void* k, const void* v, const void* o,
                                        const float* lse, void* dq, void* dk, void* dv, void* workspace,
                                        size_t workspace_bytes, void* stream);
+/*
+ * eqlin_attention_device_status -- synchronise the current device, then read and clear its word for
+ * errors of the attention kernels: EQLIN_OK, or EQLIN_ERR_TIMEOUT when a bounded wait inside one ran
+ * out since the last call (its outputs are then undefined).  Errors: INVALID_ARG, CUDA.
+ */
+EQLIN_API int eqlin_attention_device_status(int* status_out);
 
 /* Static description of a status code ("ok", "invalid argument", ...). */
 EQLIN_API const char* eqlin_status_string(int status);

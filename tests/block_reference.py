@@ -48,9 +48,12 @@ def offsets(lens, device=None) -> torch.Tensor:
     return t.to(torch.int32).to(device) if device else t.to(torch.int32)
 
 
-def attention(q, k, v, do, q_lens, k_lens, heads, kv_heads, causal, scale=None):
+def attention(q, k, v, do, q_lens, k_lens, heads, kv_heads, causal, scale=None, chained=False):
     """{"o", "lse", "dq", "dk", "dv"} in float64 and {name: bound} for kernels of q's dtype, for
-    q [Nq, H Dh, G], k and v [Nk, Hk Dh, G]; the gradients are those for o rounded to q's dtype."""
+    q [Nq, H Dh, G], k and v [Nk, Hk Dh, G]; the gradients are those for o rounded to q's dtype.
+    chained: the gradients were given the kernel's own o and lse.  Then o is off by up to its bound, which
+    moves delta_i = do_i . o_i by up to sum_d |do_id| bound(o_id), and lse by up to its bound, which
+    moves every weight by that much relative to itself."""
     T, u, t0 = q.dtype, unit(q.dtype), tiny(q.dtype)
     if T == torch.float32:
         p_round, ds_round = 0.0, 0.0          # fp32 keeps them unrounded
@@ -90,6 +93,10 @@ def attention(q, k, v, do, q_lens, k_lens, heads, kv_heads, causal, scale=None):
             delta_err = E * (w.abs() * ot.abs()).sum(1)
             ds = p * (dp - delta[:, None])
             p32 = p_err - p * p_round - t0 * (p > 0)             # ds is formed from unrounded weights
+            if chained:
+                delta_err = delta_err + (w.abs() * bound["o"][rows, h]).sum(1)
+                off = p * torch.where(lse == -math.inf, torch.zeros_like(lse), lse_err)[:, None]
+                p32, p_err = p32 + off, p_err + off
             ds_err = p32 * (dp - delta[:, None]).abs() + p * (dp_err + delta_err[:, None]) \
                 + E * p * (dp.abs() + delta.abs()[:, None])
             ds_err = ds_err + ds_round * (ds.abs() + ds_err) + t0 * (p > 0)
