@@ -9,6 +9,7 @@
 
 #include "eqlin_attn.cuh"
 #include "eqlin_attn_f32.cuh"
+#include "eqlin_attn_bwd_tc.cuh"
 #include "eqlin_attn_tc.cuh"
 #include "eqlin_host_util.h"
 
@@ -182,6 +183,42 @@ int backward_f32(const attn::Params& p, cudaStream_t st) {
                    Shape<DP>::DQ_BYTES, st, "attention gradient launch", p);
     return s;
 }
+template <class T, int DP>
+int backward_tc(const attn::tc::BwdParams& bp, int io, cudaStream_t st) {
+    namespace tc = attn::tc;
+    using B = tc::Bwd<DP>;
+    const attn::Params& p = bp.p;
+    unsigned grid_k = 0, grid_q = 0;
+    int s = tc_grid(p.k_rows, p.sequences, tc::kTile, p.kv_heads, &grid_k);
+    if (s == EQLIN_OK) s = tc_grid(p.q_rows, p.sequences, tc::kTile, p.heads, &grid_q);
+    CUtensorMap mq, mk, mv, mdo;
+    if (s == EQLIN_OK && p.q_rows > 0) {
+        s = encode_map(p.q, p.q_rows, p.heads, p.D, p.q_stride, io, &mq);
+        if (s == EQLIN_OK) s = encode_map(p.dout, p.q_rows, p.heads, p.D, p.do_stride, io, &mdo);
+    }
+    if (s == EQLIN_OK && p.k_rows > 0) {
+        s = encode_map(p.k, p.k_rows, p.kv_heads, p.D, p.k_stride, io, &mk);
+        if (s == EQLIN_OK) s = encode_map(p.v, p.k_rows, p.kv_heads, p.D, p.v_stride, io, &mv);
+    }
+    if (s != EQLIN_OK) return s;
+    if (p.q_rows == 0) mq = mdo = mk;   // the side without rows is never read
+    if (p.k_rows == 0) mk = mv = mq;
+    if (p.q_rows > 0) s = launch_delta<T>(p, st);
+    if (s == EQLIN_OK && p.k_rows > 0)
+        s = launch(tc::eqlin_attn_dkv_tc_kernel<T, DP>, dim3(grid_k), dim3(B::THREADS), B::SMEM, st,
+                   "attention gradient launch", mq, mk, mv, mdo, bp);
+    if (s == EQLIN_OK && p.q_rows > 0)
+        s = launch(tc::eqlin_attn_dq_tc_kernel<T, DP>, dim3(grid_q), dim3(B::THREADS), B::SMEM, st,
+                   "attention gradient launch", mq, mk, mv, mdo, bp);
+    return s;
+}
+template <class T>
+int backward_16(attn::Params& p, int io, cudaStream_t st) {
+    p.timeout_ns = wait_timeout_ns();
+    const attn::tc::BwdParams bp = {p, stop_after()};
+    return p.D <= 64 ? backward_tc<T, 64>(bp, io, st) : backward_tc<T, 128>(bp, io, st);
+}
+
 template <class T>
 int backward_t(const attn::Params& p, cudaStream_t st) {
     return p.D <= 64 ? backward_f32<T, 64>(p, st) : backward_f32<T, 128>(p, st);
@@ -291,7 +328,7 @@ int eqlin_attention_backward(const eqlin_attention_shape* shape, const eqlin_att
     p.dv_stride = strides->dv;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (io == EQLIN_F32) return backward_t<float>(p, st);
-    return io == EQLIN_F16 ? backward_t<__half>(p, st) : backward_t<__nv_bfloat16>(p, st);
+    return io == EQLIN_F16 ? backward_16<__half>(p, io, st) : backward_16<__nv_bfloat16>(p, io, st);
 }
 
 }  // extern "C"

@@ -1,0 +1,509 @@
+// eqlin_attn_bwd_tc.cuh -- gradients of 16-bit attention on the tcgen05 tensor cores.
+//
+// Two kernels, each with its sums in TMEM and without atomics, so that results do not vary:
+//   dk, dv: a block holds 128 keys of one key head and walks the queries of its group's heads:
+//       S^T = K Q^T,  dP^T = V dO^T,  P^T = exp2(c S^T - lse),  dS^T = P^T (dP^T - delta)
+//       dV += P^T dO,  dK += dS^T Q           (A = P^T, dS^T from TMEM)
+//   dq: a block holds 128 queries of one head and walks their keys:
+//       S = Q K^T,  dP = dO V^T,  dS = P (dP - delta),  dQ += dS K
+// Computing S and dP twice costs two more products than one kernel would (7 for 5), and saves the
+// atomics or the fp32 copy of dq that one kernel needs.
+// Warps: two warpgroups of 128 threads for the elementwise work (thread = TMEM lane; each warpgroup
+// takes 64 of the 128 columns), one warp of loads, one of MMAs.
+#pragma once
+
+#include "eqlin_attn_tc.cuh"
+
+namespace eqlin {
+namespace attn {
+namespace tc {
+
+template <int DP>
+struct Bwd {
+    static constexpr int BOXES = DP / 64;
+    static constexpr int TILE_BYTES = BOXES * kBoxBytes;
+    static constexpr int FIXED = 2;                      // tiles that stay: K, V or Q, dO
+    static constexpr int STAGES = DP == 64 ? 8 : 4;      // ring
+    static constexpr int THREADS = 256 + 64;
+    static constexpr int WARP_LOAD = 8, WARP_MMA = 9;
+    static constexpr size_t SMEM = 1024 + 512 + 4 * kTile * sizeof(float2) / 2 +
+                                   static_cast<size_t>(STAGES + FIXED) * TILE_BYTES;
+};
+
+struct BwdParams {
+    Params p;
+    long long stop_after;    // test hook, as in FwdParams
+};
+
+// the A operand in TMEM whose K index runs over 64 columns of each warpgroup: words [0, 32) and [64, 96)
+__device__ __forceinline__ void mma_rows_halves(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool add) {
+    for (int s = 0; s < 8; ++s)
+        umma_f16_ts(d, a + (s >> 2) * 64 + (s & 3) * 8, desc_mn(b + s * 2048), idesc, add || s > 0);
+}
+
+// 128 rows x D features of an fp32 accumulator in TMEM, times `mul`, to the rows of an output.
+template <class T>
+__device__ __forceinline__ void store_accumulator(uint32_t taddr, bool filled, bool live, T* out, int D, float mul) {
+    for (int c = 0; c < D; c += 16) {
+        uint32_t o[16] = {};
+        if (filled) {
+            ptx::tmem_ld_32x32b<16>(taddr + c, o);
+            ptx::tmem_wait_ld();
+            ptx::tmem_regs_ready(o);
+        }
+        if (!live) continue;
+#pragma unroll
+        for (int e = 0; e < 16; e += 8) {
+            if (c + e >= D) break;
+            uint32_t w[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                w[k] = Io16<T>::pack(__uint_as_float(o[e + 2 * k]) * mul, __uint_as_float(o[e + 2 * k + 1]) * mul);
+            *reinterpret_cast<uint4*>(out + c + e) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+    }
+}
+
+// ------------------------------------------------------------------------------- dk and dv
+template <class T, int DP>
+__global__ void __launch_bounds__(Bwd<DP>::THREADS, 1)
+    eqlin_attn_dkv_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
+                             const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mdo,
+                             const __grid_constant__ BwdParams bp) {
+    using B = Bwd<DP>;
+    constexpr int ST = B::STAGES;
+    const Params& p = bp.p;
+    extern __shared__ uint8_t raw[];
+    uint8_t* base = ptx::smem_align_1k(raw);
+    float2* rows = reinterpret_cast<float2*>(base + (ST + B::FIXED) * B::TILE_BYTES);   // [2][128]: lse, delta
+    uint64_t* bars = reinterpret_cast<uint64_t*>(rows + 2 * kTile);
+    Ctl* ctl = reinterpret_cast<Ctl*>(bars + 48);
+    auto bar = [&](int i) { return ptx::smem_u32(bars + i); };
+    auto full = [&](int s) { return bar(s); };
+    auto empty = [&](int s) { return bar(ST + s); };
+    const uint32_t fixed_full = bar(2 * ST), s_full = bar(2 * ST + 1), dp_full = bar(2 * ST + 2),
+                   p_full = bar(2 * ST + 3), ds_full = bar(2 * ST + 4), done = bar(2 * ST + 5),
+                   rows_full = bar(2 * ST + 6);
+    uint8_t *k_tile = base, *v_tile = base + B::TILE_BYTES, *ring = base + 2 * B::TILE_BYTES;
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        ctl->abort = 0;
+        for (int s = 0; s < ST; ++s) {
+            ptx::mbar_init(full(s), 1);
+            ptx::mbar_init(empty(s), 1);
+        }
+        ptx::mbar_init(fixed_full, 1);
+        ptx::mbar_init(s_full, 1);
+        ptx::mbar_init(dp_full, 1);
+        ptx::mbar_init(p_full, 256);
+        ptx::mbar_init(rows_full, 256);
+        ptx::mbar_init(ds_full, 256);
+        ptx::mbar_init(done, 1);
+        ptx::fence_mbar_init();
+    }
+    if (warp == B::WARP_MMA) {
+        ptx::tmem_alloc(ptx::smem_u32(&ctl->tmem_base), 512);
+        ptx::tmem_relinquish();
+    }
+    ptx::grid_dependency_wait();
+    const int hk = blockIdx.x % p.kv_heads, slot = blockIdx.x / p.kv_heads, group = p.heads / p.kv_heads;
+    const Tile t = find_tile<kTile>(p.k_offsets, p.sequences, p.k_rows, slot);
+    const Rows qr = sequence_rows(p.q_offsets, t.b, p.q_rows);
+    const int r0 = t.tile * kTile;
+    // query tiles: from the first that sees the first key of this tile
+    const int begin = t.tile < 0 ? 0 : first_query(r0, qr.len, t.own.len, p.causal) / kTile;
+    const int per_head = t.tile < 0 ? 0 : max(0, (qr.len + kTile - 1) / kTile - begin);
+    const int n = per_head * group;
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    ptx::grid_launch_dependents();   // after the allocation, as in the forward
+    const uint32_t tmem = ctl->tmem_base;
+    const uint32_t t_s = tmem, t_dp = tmem + 128, t_dv = tmem + 256, t_dk = tmem + 256 + DP;
+
+    if (warp == B::WARP_LOAD) {
+        if (lane == 0 && n > 0) {
+            long long issued = 0;
+            auto load = [&](const CUtensorMap* m, uint8_t* dst, int head, int row, uint32_t b) {
+                for (int x = 0; x < B::BOXES; ++x)
+                    tma_load_3d(ptx::smem_u32(dst) + x * kBoxBytes, m, x * 64, head, row, b);
+            };
+            ptx::mbar_arrive_expect_tx(fixed_full, 2 * B::TILE_BYTES);
+            load(&mk, k_tile, hk, t.own.start + r0, fixed_full);
+            load(&mv, v_tile, hk, t.own.start + r0, fixed_full);
+            for (int u = 0; u < 2 * n; ++u) {      // Q_0, dO_0, Q_1, dO_1, ...
+                const int s = u % ST, it = u >> 1;
+                if (u >= ST && !wait_bounded(empty(s), ((u / ST) & 1) ^ 1, ctl, p.timeout_ns)) break;
+                if (issued == bp.stop_after) break;
+                ptx::mbar_arrive_expect_tx(full(s), B::TILE_BYTES);
+                load(u & 1 ? &mdo : &mq, ring + s * B::TILE_BYTES, hk * group + it / per_head,
+                     qr.start + (begin + it % per_head) * kTile, full(s));
+                ++issued;
+            }
+            drain_wait(fixed_full, 0, p.timeout_ns);
+            for (int s = 0; s < ST; ++s) {
+                const long long times = issued > s ? (issued - s + ST - 1) / ST : 0;
+                if (times > 0) drain_wait(full(s), static_cast<uint32_t>((times - 1) & 1), p.timeout_ns);
+            }
+        }
+    } else if (warp == B::WARP_MMA) {
+        if (n > 0) {
+            const uint32_t id_s = idesc_f16kind_f32(128, 128, Io16<T>::kUmmaFormat, false);
+            const uint32_t id_o = idesc_f16kind_f32(128, (p.D + 15) / 16 * 16, Io16<T>::kUmmaFormat, false) | kBMnMajor;
+            const int steps = (p.D + 15) / 16;
+            auto stage = [&](int u) { return ring + (u % ST) * B::TILE_BYTES; };
+            // a ring tile, with zeros for the rows past the sequence's end
+            auto take = [&](int u) {
+                if (!wait_warp(full(u % ST), (u / ST) & 1, ctl, p.timeout_ns)) return false;
+                const int valid = qr.len - (begin + (u >> 1) % per_head) * kTile;
+                if (valid < kTile) zero_tail(stage(u), B::BOXES, valid, lane);
+                return true;
+            };
+            auto product = [&](uint32_t d, uint8_t* fixed, int u, uint32_t b) {
+                if (lane == 0) {
+                    mma_features(d, ptx::smem_u32(fixed), ptx::smem_u32(stage(u)), steps, id_s);
+                    ptx::umma_commit(b);
+                }
+                __syncwarp();
+            };
+            bool ok = wait_warp(fixed_full, 0, ctl, p.timeout_ns) && take(0);
+            if (ok) product(t_s, k_tile, 0, s_full);
+            ok = ok && take(1);
+            if (ok) product(t_dp, v_tile, 1, dp_full);
+            for (int j = 0; ok && j < n; ++j) {
+                if (!(ok = wait_warp(p_full, j & 1, ctl, p.timeout_ns))) break;
+                ptx::tc_fence_after();
+                if (lane == 0) mma_rows_halves(t_dv, t_s, ptx::smem_u32(stage(2 * j + 1)), id_o, j > 0);
+                __syncwarp();
+                // MMAs of one thread run in order: S^T is written after P^T has been read out of it
+                if (j + 1 < n) {
+                    if (!(ok = take(2 * j + 2))) break;
+                    product(t_s, k_tile, 2 * j + 2, s_full);
+                }
+                if (!(ok = wait_warp(ds_full, j & 1, ctl, p.timeout_ns))) break;
+                ptx::tc_fence_after();
+                if (lane == 0) {
+                    mma_rows_halves(t_dk, t_dp, ptx::smem_u32(stage(2 * j)), id_o, j > 0);
+                    ptx::umma_commit(empty((2 * j) % ST));
+                    ptx::umma_commit(empty((2 * j + 1) % ST));
+                }
+                __syncwarp();
+                if (j + 1 < n) {
+                    if (!(ok = take(2 * j + 3))) break;
+                    product(t_dp, v_tile, 2 * j + 3, dp_full);
+                }
+            }
+            if (lane == 0) {
+                ptx::umma_commit(done);
+                drain_wait(done, 0, p.timeout_ns);
+            }
+            __syncwarp();
+        }
+    } else {
+        const int half = warp >> 2, tid = threadIdx.x;
+        const int row = r0 + (tid & 127);                          // key of the sequence
+        const bool live = t.tile >= 0 && row < t.own.len;
+        const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+        const uint32_t ts = t_s + lanes + half * 64, tdp = t_dp + lanes + half * 64;
+        const float c2 = p.scale * kLog2e;
+        bool ok = true;
+        // lse (threads of the first warpgroup) or delta (second) of query tid & 127 of tile j; a row
+        // that sees no key, or is past the end, gets lse = +infinity: weights of zero
+        auto fetch = [&](int j) {
+            const int q = (begin + j % per_head) * kTile + (tid & 127);
+            if (q >= qr.len) return half ? 0.f : INFINITY;
+            const long long at = static_cast<long long>(hk * group + j / per_head) * p.q_rows + qr.start + q;
+            if (half) return p.delta[at];
+            const float l = p.lse[at];
+            return l == -INFINITY ? INFINITY : l * kLog2e;
+        };
+        float next = n > 0 ? fetch(0) : 0.f;
+        for (int j = 0; j < n; ++j) {
+            float2* rj = rows + (j & 1) * kTile;
+            // tile j - 2, which had this buffer, is read: dP of tile j - 1 was issued after all threads' dS of it
+            reinterpret_cast<float*>(rj + (tid & 127))[half] = next;
+            ptx::mbar_arrive(rows_full);
+            if (j + 1 < n) next = fetch(j + 1);
+            if (!(ok = wait_warp(rows_full, j & 1, ctl, p.timeout_ns))) break;
+            if (!(ok = wait_warp(s_full, j & 1, ctl, p.timeout_ns))) break;
+            ptx::tc_fence_after();
+            uint32_t s[2][32];
+            ptx::tmem_ld_32x32b<32>(ts, s[0]);
+            ptx::tmem_ld_32x32b<32>(ts + 32, s[1]);
+            ptx::tmem_wait_ld();
+            ptx::tmem_regs_ready(s[0]);
+            ptx::tmem_regs_ready(s[1]);
+            const int q0 = (begin + j % per_head) * kTile;
+            if (p.causal && static_cast<long long>(r0) + kTile - 1 > static_cast<long long>(q0) + t.own.len - qr.len) {
+                // key `row` is seen by queries from row - (keys - queries) on
+                const long long first = static_cast<long long>(row) - (t.own.len - qr.len) - q0 - half * 64;
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        if (c * 32 + e < first) s[c][e] = 0xFF800000u;
+            }
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                uint32_t w[16];
+#pragma unroll
+                for (int e = 0; e < 32; e += 2) {
+                    const float4 ld = *reinterpret_cast<const float4*>(rj + half * 64 + c * 32 + e);   // lse, delta, lse, delta
+                    const float a = ex2(fmaf(__uint_as_float(s[c][e]), c2, -ld.x));
+                    const float b = ex2(fmaf(__uint_as_float(s[c][e + 1]), c2, -ld.z));
+                    s[c][e] = __float_as_uint(a);
+                    s[c][e + 1] = __float_as_uint(b);
+                    w[e >> 1] = Io16<T>::pack(a, b);
+                }
+                tmem_st16(ts + c * 16, w);
+            }
+            tmem_wait_st();
+            ptx::tc_fence_before();
+            ptx::mbar_arrive(p_full);
+            if (!(ok = wait_warp(dp_full, j & 1, ctl, p.timeout_ns))) break;
+            ptx::tc_fence_after();
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                uint32_t d[32], w[16];
+                ptx::tmem_ld_32x32b<32>(tdp + c * 32, d);
+                ptx::tmem_wait_ld();
+                ptx::tmem_regs_ready(d);
+#pragma unroll
+                for (int e = 0; e < 32; e += 2) {
+                    const float4 ld = *reinterpret_cast<const float4*>(rj + half * 64 + c * 32 + e);
+                    const float a = __uint_as_float(s[c][e]) * (__uint_as_float(d[e]) - ld.y);
+                    const float b = __uint_as_float(s[c][e + 1]) * (__uint_as_float(d[e + 1]) - ld.w);
+                    w[e >> 1] = Io16<T>::pack(a, b);
+                }
+                // words [0, 32) of the half: columns that this thread has read (c = 0: all of [0, 32))
+                tmem_st16(tdp + c * 16, w);
+            }
+            tmem_wait_st();
+            ptx::tc_fence_before();
+            ptx::mbar_arrive(ds_full);
+        }
+        if (ok && n > 0) ok = wait_warp(done, 0, ctl, p.timeout_ns);
+        if (ok && t.tile >= 0) {
+            ptx::tc_fence_after();
+            const long long at = static_cast<long long>(t.own.start) + row, col = static_cast<long long>(hk) * p.D;
+            if (half) store_accumulator<T>(t_dk + lanes, n > 0, live, static_cast<T*>(p.dk) + at * p.dk_stride + col, p.D, p.scale);
+            else store_accumulator<T>(t_dv + lanes, n > 0, live, static_cast<T*>(p.dv) + at * p.dv_stride + col, p.D, 1.f);
+        }
+        ptx::tc_fence_before();
+    }
+    __syncthreads();
+    if (warp == B::WARP_MMA) {
+        ptx::tc_fence_after();
+        ptx::tmem_dealloc(tmem, 512);
+    }
+}
+
+// ------------------------------------------------------------------------------------- dq
+template <class T, int DP>
+__global__ void __launch_bounds__(Bwd<DP>::THREADS, 1)
+    eqlin_attn_dq_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
+                            const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mdo,
+                            const __grid_constant__ BwdParams bp) {
+    using B = Bwd<DP>;
+    constexpr int ST = B::STAGES;
+    const Params& p = bp.p;
+    extern __shared__ uint8_t raw[];
+    uint8_t* base = ptx::smem_align_1k(raw);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(base + (ST + B::FIXED) * B::TILE_BYTES);
+    Ctl* ctl = reinterpret_cast<Ctl*>(bars + 48);
+    auto bar = [&](int i) { return ptx::smem_u32(bars + i); };
+    auto full = [&](int s) { return bar(s); };
+    auto empty = [&](int s) { return bar(ST + s); };
+    const uint32_t fixed_full = bar(2 * ST), dp_full = bar(2 * ST + 1), ds_full = bar(2 * ST + 2), done = bar(2 * ST + 3);
+    auto s_full = [&](int b) { return bar(2 * ST + 4 + b); };
+    uint8_t *q_tile = base, *do_tile = base + B::TILE_BYTES, *ring = base + 2 * B::TILE_BYTES;
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        ctl->abort = 0;
+        for (int s = 0; s < ST; ++s) {
+            ptx::mbar_init(full(s), 1);
+            ptx::mbar_init(empty(s), 1);
+        }
+        ptx::mbar_init(fixed_full, 1);
+        ptx::mbar_init(dp_full, 1);
+        ptx::mbar_init(ds_full, 256);
+        ptx::mbar_init(done, 1);
+        ptx::mbar_init(s_full(0), 1);
+        ptx::mbar_init(s_full(1), 1);
+        ptx::fence_mbar_init();
+    }
+    if (warp == B::WARP_MMA) {
+        ptx::tmem_alloc(ptx::smem_u32(&ctl->tmem_base), 512);
+        ptx::tmem_relinquish();
+    }
+    ptx::grid_dependency_wait();
+    const int h = blockIdx.x % p.heads, hk = h / (p.heads / p.kv_heads);
+    const int n_slots = gridDim.x / p.heads;
+    const int slot = p.causal ? n_slots - 1 - blockIdx.x / p.heads : blockIdx.x / p.heads;
+    const Tile t = find_tile<kTile>(p.q_offsets, p.sequences, p.q_rows, slot);
+    const Rows kr = sequence_rows(p.k_offsets, t.b, p.k_rows);
+    const int r0 = t.tile * kTile;
+    const int n = t.tile < 0 ? 0
+                             : (keys_seen(min(r0 + kTile, t.own.len) - 1, t.own.len, kr.len, p.causal) + kTile - 1) / kTile;
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    ptx::grid_launch_dependents();   // after the allocation, as in the forward
+    const uint32_t tmem = ctl->tmem_base;
+    auto t_s = [&](int j) { return tmem + (j & 1) * 128; };
+    const uint32_t t_dp = tmem + 256, t_dq = tmem + 384;
+
+    if (warp == B::WARP_LOAD) {
+        if (lane == 0 && n > 0) {
+            long long issued = 0;
+            auto load = [&](const CUtensorMap* m, uint8_t* dst, int head, int row, uint32_t b) {
+                for (int x = 0; x < B::BOXES; ++x)
+                    tma_load_3d(ptx::smem_u32(dst) + x * kBoxBytes, m, x * 64, head, row, b);
+            };
+            ptx::mbar_arrive_expect_tx(fixed_full, 2 * B::TILE_BYTES);
+            load(&mq, q_tile, h, t.own.start + r0, fixed_full);
+            load(&mdo, do_tile, h, t.own.start + r0, fixed_full);
+            for (int u = 0; u < 2 * n; ++u) {      // K_0, V_0, K_1, V_1, ...
+                const int s = u % ST;
+                if (u >= ST && !wait_bounded(empty(s), ((u / ST) & 1) ^ 1, ctl, p.timeout_ns)) break;
+                if (issued == bp.stop_after) break;
+                ptx::mbar_arrive_expect_tx(full(s), B::TILE_BYTES);
+                load(u & 1 ? &mv : &mk, ring + s * B::TILE_BYTES, hk, kr.start + (u >> 1) * kTile, full(s));
+                ++issued;
+            }
+            drain_wait(fixed_full, 0, p.timeout_ns);
+            for (int s = 0; s < ST; ++s) {
+                const long long times = issued > s ? (issued - s + ST - 1) / ST : 0;
+                if (times > 0) drain_wait(full(s), static_cast<uint32_t>((times - 1) & 1), p.timeout_ns);
+            }
+        }
+    } else if (warp == B::WARP_MMA) {
+        if (n > 0) {
+            const uint32_t id_s = idesc_f16kind_f32(128, 128, Io16<T>::kUmmaFormat, false);
+            const uint32_t id_o = idesc_f16kind_f32(128, (p.D + 15) / 16 * 16, Io16<T>::kUmmaFormat, false) | kBMnMajor;
+            const int steps = (p.D + 15) / 16;
+            auto stage = [&](int u) { return ring + (u % ST) * B::TILE_BYTES; };
+            auto wait_stage = [&](int u) { return wait_warp(full(u % ST), (u / ST) & 1, ctl, p.timeout_ns); };
+            auto scores = [&](int j) {
+                if (!wait_stage(2 * j)) return false;
+                const int valid = kr.len - j * kTile;
+                if (valid < kTile) zero_tail(stage(2 * j), B::BOXES, valid, lane);
+                if (lane == 0) {
+                    mma_features(t_s(j), ptx::smem_u32(q_tile), ptx::smem_u32(stage(2 * j)), steps, id_s);
+                    ptx::umma_commit(s_full(j & 1));
+                }
+                __syncwarp();
+                return true;
+            };
+            auto dp = [&](int j) {
+                if (!wait_stage(2 * j + 1)) return false;
+                if (lane == 0) {
+                    mma_features(t_dp, ptx::smem_u32(do_tile), ptx::smem_u32(stage(2 * j + 1)), steps, id_s);
+                    ptx::umma_commit(dp_full);
+                    ptx::umma_commit(empty((2 * j + 1) % ST));
+                }
+                __syncwarp();
+                return true;
+            };
+            bool ok = wait_warp(fixed_full, 0, ctl, p.timeout_ns) && scores(0) && dp(0);
+            if (ok && n > 1) ok = scores(1);
+            for (int j = 0; ok && j < n; ++j) {
+                // dS_j lies over S_j, and dP_j has been read
+                if (!(ok = wait_warp(ds_full, j & 1, ctl, p.timeout_ns))) break;
+                ptx::tc_fence_after();
+                if (j + 1 < n && !(ok = dp(j + 1))) break;
+                if (lane == 0) {
+                    mma_rows_halves(t_dq, t_s(j), ptx::smem_u32(stage(2 * j)), id_o, j > 0);
+                    ptx::umma_commit(empty((2 * j) % ST));
+                }
+                __syncwarp();
+                // MMAs of one thread run in order: S_{j+2} is written after dS_j has been read
+                if (j + 2 < n) ok = scores(j + 2);
+            }
+            if (lane == 0) {
+                ptx::umma_commit(done);
+                drain_wait(done, 0, p.timeout_ns);
+            }
+            __syncwarp();
+        }
+    } else {
+        const int half = warp >> 2;
+        const int row = r0 + (threadIdx.x & 127);                  // query of the sequence
+        const bool live = t.tile >= 0 && row < t.own.len;
+        const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+        const int seen = live ? keys_seen(row, t.own.len, kr.len, p.causal) : 0;
+        const int seen_all = p.causal ? keys_seen(r0, t.own.len, kr.len, 1) : kr.len;
+        const float c2 = p.scale * kLog2e;
+        const long long at = static_cast<long long>(t.own.start) + row;
+        float off = 0.f, delta = 0.f;
+        if (live && seen > 0) {
+            off = -p.lse[static_cast<long long>(h) * p.q_rows + at] * kLog2e;
+            delta = p.delta[static_cast<long long>(h) * p.q_rows + at];
+        }
+        bool ok = true;
+        for (int j = 0; j < n; ++j) {
+            const uint32_t ts = t_s(j) + lanes + half * 64, tdp = t_dp + lanes + half * 64;
+            if (!(ok = wait_warp(s_full(j & 1), (j >> 1) & 1, ctl, p.timeout_ns))) break;
+            ptx::tc_fence_after();
+            uint32_t s[2][32];
+            ptx::tmem_ld_32x32b<32>(ts, s[0]);
+            ptx::tmem_ld_32x32b<32>(ts + 32, s[1]);
+            ptx::tmem_wait_ld();
+            ptx::tmem_regs_ready(s[0]);
+            ptx::tmem_regs_ready(s[1]);
+            const bool masked = (j + 1) * kTile > seen_all;
+            const int n_seen = seen - j * kTile - half * 64;
+            if (masked) {
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        if (c * 32 + e >= n_seen) s[c][e] = 0xFF800000u;
+            }
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+#pragma unroll
+                for (int e = 0; e < 32; ++e) s[c][e] = __float_as_uint(ex2(fmaf(__uint_as_float(s[c][e]), c2, off)));
+            if (!(ok = wait_warp(dp_full, j & 1, ctl, p.timeout_ns))) break;
+            ptx::tc_fence_after();
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                uint32_t d[32], w[16];
+                ptx::tmem_ld_32x32b<32>(tdp + c * 32, d);
+                ptx::tmem_wait_ld();
+                ptx::tmem_regs_ready(d);
+                if (masked) {       // rows of V past the end may hold anything
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        if (c * 32 + e >= n_seen) d[e] = 0;
+                }
+#pragma unroll
+                for (int e = 0; e < 32; e += 2)
+                    w[e >> 1] = Io16<T>::pack(__uint_as_float(s[c][e]) * (__uint_as_float(d[e]) - delta),
+                                              __uint_as_float(s[c][e + 1]) * (__uint_as_float(d[e + 1]) - delta));
+                tmem_st16(ts + c * 16, w);
+            }
+            tmem_wait_st();
+            ptx::tc_fence_before();
+            ptx::mbar_arrive(ds_full);
+        }
+        if (ok && n > 0) ok = wait_warp(done, 0, ctl, p.timeout_ns);
+        if (ok && t.tile >= 0 && half == 0) {
+            ptx::tc_fence_after();
+            store_accumulator<T>(t_dq + lanes, n > 0, live,
+                                 static_cast<T*>(p.dq) + at * p.dq_stride + static_cast<long long>(h) * p.D, p.D, p.scale);
+        }
+        ptx::tc_fence_before();
+    }
+    __syncthreads();
+    if (warp == B::WARP_MMA) {
+        ptx::tc_fence_after();
+        ptx::tmem_dealloc(tmem, 512);
+    }
+}
+
+}  // namespace tc
+}  // namespace attn
+}  // namespace eqlin
