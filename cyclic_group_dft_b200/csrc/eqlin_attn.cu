@@ -10,6 +10,7 @@
 #include "eqlin_attn.cuh"
 #include "eqlin_attn_f32.cuh"
 #include "eqlin_attn_bwd_tc.cuh"
+#include "eqlin_attn_mma.cuh"
 #include "eqlin_attn_tc.cuh"
 #include "eqlin_host_util.h"
 
@@ -55,6 +56,7 @@ int check_tensor(const void* t, int64_t rows, int64_t width, int64_t stride, int
     return EQLIN_OK;
 }
 
+// fp32: blocks along x
 unsigned slots(int64_t rows, int64_t sequences, int m) { return static_cast<unsigned>(rows / m + sequences); }
 
 void fill(const eqlin_attention_shape* a, attn::Params& p) {
@@ -141,8 +143,89 @@ int forward_tc(attn::tc::FwdParams fp, int io, cudaStream_t st) {
     return launch(attn::tc::eqlin_attn_fwd_tc_kernel<T, DP, NQ>, dim3(grid), dim3(F::THREADS), F::SMEM, st,
                   "attention launch", mq, mk, mv, fp);
 }
+// ------------------------------------------------------------------------ choice of the forward
+enum class Fwd { kTiles, kShort, kFew };
+
+// By the average lengths, which the host knows (the single ones are device data); every kernel is right
+// for every length.
+//   few    at most 16 packed rows (queries times heads of a key head) a sequence and keys enough to
+//          split: the keys are read once for all heads of the group, by all SMs.
+//   short  at most 64 rows a sequence on both sides.
+//   tiles  the rest.
+Fwd forward_kind(const eqlin_attention_shape& a) {
+    const int64_t group = a.heads / a.kv_heads;
+    if (a.io_dtype == EQLIN_F32) return Fwd::kTiles;
+    if (a.q_rows * group <= 16 * a.sequences && a.k_rows >= 128 * a.sequences) return Fwd::kFew;
+    if (a.q_rows <= 64 * a.sequences && a.k_rows <= 64 * a.sequences) return Fwd::kShort;
+    return Fwd::kTiles;
+}
+
+constexpr int kB200Sms = 148;   // the plan does not depend on the device, so that sizes need none
+
+// Slices of the keys, where the tiles alone would leave SMs idle: as many as fill them once (fp32: three
+// blocks fit an SM), but no slice below 256 keys.
+int forward_splits(const eqlin_attention_shape& a) {
+    const Fwd kind = forward_kind(a);
+    const int64_t keys = a.k_rows / a.sequences;
+    int64_t units, room;
+    if (kind == Fwd::kFew) {
+        const int64_t rows = a.q_rows * (a.heads / a.kv_heads);
+        units = std::max(a.sequences, (rows + 15) / 16) * a.kv_heads;
+        room = kB200Sms;
+    } else if (a.io_dtype == EQLIN_F32) {
+        units = std::max(a.sequences, (a.q_rows + 63) / 64) * a.heads;
+        room = 3 * kB200Sms;
+    } else {
+        return 1;
+    }
+    return static_cast<int>(std::max<int64_t>(1, std::min({room / std::max<int64_t>(units, 1), keys / 256, int64_t(64)})));
+}
+
+size_t forward_workspace(const eqlin_attention_shape& a) {
+    const int n = forward_splits(a);
+    return n == 1 ? 0 : size_t(n) * size_t(a.heads) * size_t(a.q_rows) * size_t(a.head_dim + 1) * sizeof(float);
+}
+
 template <class T>
-int forward_16(attn::Params& p, int io, cudaStream_t st) {
+int launch_join(const attn::Params& p, cudaStream_t st) {
+    const long long units = static_cast<long long>(p.q_rows) * p.heads;
+    return launch(attn::eqlin_attn_join_kernel<T>, dim3(static_cast<unsigned>((units + 3) / 4)), dim3(128), 0, st,
+                  "attention launch", p);
+}
+
+template <class T, int DP, int M>
+int forward_short_m(const attn::Params& p, cudaStream_t st) {
+    constexpr int U = 64 / M;
+    unsigned grid = 0;
+    const int s = tc_grid(p.q_rows, p.sequences, M, (p.heads + U - 1) / U, &grid);
+    if (s != EQLIN_OK) return s;
+    return launch(attn::mma::eqlin_attn_fwd_short_kernel<T, DP, M>, dim3(grid), dim3(attn::mma::kShortThreads),
+                  attn::mma::short_smem<DP>(), st, "attention launch", p);
+}
+template <class T, int DP>
+int forward_short(const attn::Params& p, cudaStream_t st) {
+    const int64_t rows = std::max(p.q_rows, p.k_rows);
+    if (rows <= int64_t(16) * p.sequences) return forward_short_m<T, DP, 16>(p, st);
+    if (rows <= int64_t(32) * p.sequences) return forward_short_m<T, DP, 32>(p, st);
+    return forward_short_m<T, DP, 64>(p, st);
+}
+
+template <class T, int DP>
+int forward_few(const attn::Params& p, cudaStream_t st) {
+    using F = attn::mma::Few<DP>;
+    const int64_t rows = int64_t(p.q_rows) * (p.heads / p.kv_heads);
+    unsigned grid = 0;
+    int s = tc_grid(rows, p.sequences, 16, int64_t(p.kv_heads) * p.splits, &grid);
+    if (s != EQLIN_OK) return s;
+    s = launch(attn::mma::eqlin_attn_fwd_few_kernel<T, DP>, dim3(grid), dim3(F::WARPS * 32), F::SMEM, st,
+               "attention launch", p);
+    return s == EQLIN_OK && p.splits > 1 ? launch_join<T>(p, st) : s;
+}
+
+template <class T>
+int forward_16(attn::Params& p, Fwd kind, int io, cudaStream_t st) {
+    if (kind == Fwd::kShort) return p.D <= 64 ? forward_short<T, 64>(p, st) : forward_short<T, 128>(p, st);
+    if (kind == Fwd::kFew) return p.D <= 64 ? forward_few<T, 64>(p, st) : forward_few<T, 128>(p, st);
     p.timeout_ns = wait_timeout_ns();
     attn::tc::FwdParams fp = {p, stop_after()};
     return p.D <= 64 ? forward_tc<T, 64, 1>(fp, io, st) : forward_tc<T, 128, 2>(fp, io, st);
@@ -151,8 +234,9 @@ int forward_16(attn::Params& p, int io, cudaStream_t st) {
 template <class T, int DP>
 int forward_f32(const attn::Params& p, cudaStream_t st) {
     using namespace attn::f32;
-    return launch(eqlin_attn_fwd_f32_kernel<T, DP>, dim3(slots(p.q_rows, p.sequences, kM), p.heads), dim3(kThreads),
-                  Shape<DP>::FWD_BYTES, st, "attention launch", p);
+    const int s = launch(eqlin_attn_fwd_f32_kernel<T, DP>, dim3(slots(p.q_rows, p.sequences, kM), p.heads, p.splits),
+                         dim3(kThreads), Shape<DP>::FWD_BYTES, st, "attention launch", p);
+    return s == EQLIN_OK && p.splits > 1 ? launch_join<T>(p, st) : s;
 }
 template <class T>
 int forward_t(const attn::Params& p, cudaStream_t st) {
@@ -232,7 +316,7 @@ int eqlin_attention_workspace_size(const eqlin_attention_shape* shape, int backw
     if (!bytes) return report(EQLIN_ERR_INVALID_ARG, "NULL argument");
     const int s = check_shape(shape);
     if (s != EQLIN_OK) return s;
-    *bytes = backward ? size_t(shape->q_rows) * size_t(shape->heads) * sizeof(float) : 0;
+    *bytes = backward ? size_t(shape->q_rows) * size_t(shape->heads) * sizeof(float) : forward_workspace(*shape);
     return EQLIN_OK;
 }
 
@@ -263,9 +347,14 @@ int eqlin_attention_forward(const eqlin_attention_shape* shape, const void* q, c
     p.v = v;
     p.out = o;
     p.lse = lse;
+    p.splits = forward_splits(a);
+    p.part_o = static_cast<float*>(workspace);
+    if (p.splits > 1) p.part_lse = p.part_o + size_t(p.splits) * a.heads * a.q_rows * a.head_dim;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (a.io_dtype == EQLIN_F32) return forward_t<float>(p, st);
-    return a.io_dtype == EQLIN_F16 ? forward_16<__half>(p, a.io_dtype, st) : forward_16<__nv_bfloat16>(p, a.io_dtype, st);
+    const Fwd kind = forward_kind(a);
+    return a.io_dtype == EQLIN_F16 ? forward_16<__half>(p, kind, a.io_dtype, st)
+                                   : forward_16<__nv_bfloat16>(p, kind, a.io_dtype, st);
 }
 
 int eqlin_attention_device_status(int* status_out) {

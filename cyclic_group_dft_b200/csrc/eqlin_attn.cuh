@@ -31,6 +31,8 @@ struct Params {
     int q_rows, k_rows, sequences, heads, kv_heads, D;
     int causal;
     float scale;
+    int splits;                    // slices of the keys; above 1 a slice's o and lse go to
+    float *part_o, *part_lse;      // [splits][heads][q_rows][D] and [splits][heads][q_rows]
     unsigned long long timeout_ns;
 };
 
@@ -50,37 +52,59 @@ __device__ __forceinline__ Rows sequence_rows(const int32_t* offsets, int b, int
 // Blocks are given tiles of M consecutive rows of one sequence without knowing the lengths on the
 // host.  Sequence b owns the slots [off[b] / M + b, off[b+1] / M + b + 1): at least as many as it has
 // tiles, in order, and rows / M + sequences in all.  A slot past its sequence's last tile has none.
-// The slot's sequence is the last b whose first slot is not past it: a search in log2(sequences)
-// reads; with 32 lanes probing at once, in log32 rounds.  Every lane of the warp must call it.
+// The slot's sequence is the last b whose first slot is not past it.  Sequences of about one length put
+// it near slot * sequences / slots: 32 lanes probe the offsets around there in one read.  Otherwise 32
+// lanes probe at once over the whole range, in log32(sequences) reads.  Every lane of the warp must call
+// it.  `mult` rows of a tile for each row of the tensor (packed heads).
 struct Tile {
     int b;       // sequence
     int tile;    // tile within the sequence, or -1: none
     Rows own;    // the sequence's rows on this side
 };
 template <int M>
-__device__ __forceinline__ Tile find_tile(const int32_t* offsets, int sequences, int rows, int slot) {
-    int b = 0;
-    if (offsets) {
+__device__ __forceinline__ Tile find_tile(const int32_t* offsets, int sequences, int rows, int slot, int mult = 1) {
+    Tile t;
+    if (!offsets) {
+        t.b = 0;
+        t.own = {0, rows};
+        t.tile = static_cast<long long>(slot) * M < static_cast<long long>(rows) * mult ? slot : -1;
+        return t;
+    }
+    auto offset = [&](int b) { return min(max(offsets[b], 0), rows); };
+    auto first_slot = [&](int off, int b) { return static_cast<long long>(off) * mult / M + b; };
+    const int lane = threadIdx.x & 31;
+    const long long slots = static_cast<long long>(rows) * mult / M + sequences;
+    const int guess = static_cast<int>(static_cast<long long>(slot) * sequences / slots);
+    const int base = max(0, min(guess - 15, sequences - 31));
+    const int probe = base + lane;
+    const int off = offset(min(probe, sequences));
+    const unsigned m = __ballot_sync(0xFFFFFFFFu, probe < sequences && first_slot(off, probe) <= slot);
+    const int in = m ? 31 - __clz(m) : 0;
+    int start, end;
+    if ((m & 1u) && in < 31 && (m == (2u << in) - 1u)) {
+        // [base, base + in] begin at or before the slot, base + in + 1 does not or is past the last one
+        t.b = base + in;
+        start = __shfl_sync(0xFFFFFFFFu, off, in);
+        end = max(start, __shfl_sync(0xFFFFFFFFu, off, in + 1));
+    } else {
         int lo = 0, n = sequences;   // the answer lies in [lo, lo + n)
-        const int lane = threadIdx.x & 31;
         while (n > 1) {
             const int step = (n + 31) / 32;
-            const int probe = lo + lane * step;
-            const bool ok = lane * step < n && min(max(offsets[probe], 0), rows) / M + probe <= slot;
-            const unsigned m = __ballot_sync(0xFFFFFFFFu, ok);
-            const int last = m ? 31 - __clz(m) : 0;
+            const int at = lo + lane * step;
+            const bool ok = lane * step < n && first_slot(offset(at), at) <= slot;
+            const unsigned w = __ballot_sync(0xFFFFFFFFu, ok);
+            const int last = w ? 31 - __clz(w) : 0;
             const int rest = n - last * step;
             lo += last * step;
             n = rest < step ? rest : step;
         }
-        b = lo;
+        t.b = lo;
+        start = offset(lo);
+        end = max(start, offset(lo + 1));
     }
-    Tile t;
-    t.b = b;
-    t.own = sequence_rows(offsets, b, rows);
-    const int first = offsets ? min(max(offsets[b], 0), rows) / M + b : 0;
-    t.tile = slot - first;
-    if (t.tile < 0 || static_cast<long long>(t.tile) * M >= t.own.len) t.tile = -1;
+    t.own = {start, end - start};
+    const long long tile = slot - first_slot(start, t.b);
+    t.tile = tile >= 0 && tile * M < static_cast<long long>(t.own.len) * mult ? static_cast<int>(tile) : -1;
     return t;
 }
 

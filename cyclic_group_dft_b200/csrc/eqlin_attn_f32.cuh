@@ -148,7 +148,11 @@ __global__ void __launch_bounds__(kThreads) eqlin_attn_fwd_f32_kernel(const Para
     const int r0 = t.tile * kM, n = min(kM, t.own.len - r0);
     const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
     const int seen = keys_seen(r0 + n - 1, t.own.len, kr.len, p.causal);
-    load_tile<T, DP>(sq, p.q, p.q_stride, t.own.start + r0, n, p.D, h);
+    // this slice's tiles of keys (all of them unless the keys are split)
+    const int tiles = (seen + kM - 1) / kM;
+    const int begin = static_cast<int>(static_cast<long long>(tiles) * blockIdx.z / p.splits) * kM;
+    const int end = min(seen, static_cast<int>(static_cast<long long>(tiles) * (blockIdx.z + 1) / p.splits) * kM);
+    load_tile<T, DP>(sq, p.q, p.q_stride, static_cast<long long>(t.own.start) + r0, n, p.D, h);
     const float c2 = p.scale * kLog2e;
     float top[4], sum[4], acc[4][DP / 16];
 #pragma unroll
@@ -158,7 +162,7 @@ __global__ void __launch_bounds__(kThreads) eqlin_attn_fwd_f32_kernel(const Para
 #pragma unroll
         for (int j = 0; j < DP / 16; ++j) acc[i][j] = 0.f;
     }
-    for (int k0 = 0; k0 < seen; k0 += kM) {
+    for (int k0 = begin; k0 < end; k0 += kM) {
         const int kn = min(kM, kr.len - k0);
         __syncthreads();
         load_tile<T, DP>(sk, p.k, p.k_stride, static_cast<long long>(kr.start) + k0, kn, p.D, hk);
@@ -199,11 +203,17 @@ __global__ void __launch_bounds__(kThreads) eqlin_attn_fwd_f32_kernel(const Para
     for (int i = 0; i < 4; ++i) {
         sum[i] = row_sum(sum[i]);
         mul[i] = sum[i] > 0.f || sum[i] != sum[i] ? 1.f / sum[i] : 0.f;
-        if (p.lse && tx == 0 && ty * 4 + i < n)
-            p.lse[static_cast<long long>(h) * p.q_rows + t.own.start + r0 + ty * 4 + i] =
-                sum[i] == 0.f ? -INFINITY : fmaf(top[i], kLn2, logf(sum[i]));
+        const float lse = sum[i] == 0.f ? -INFINITY : fmaf(top[i], kLn2, logf(sum[i]));
+        const long long at = static_cast<long long>(h) * p.q_rows + t.own.start + r0 + ty * 4 + i;
+        if (tx != 0 || ty * 4 + i >= n) continue;
+        if (p.splits > 1) p.part_lse[static_cast<long long>(blockIdx.z) * p.heads * p.q_rows + at] = lse;
+        else if (p.lse) p.lse[at] = lse;
     }
-    store_rows<T, DP>(p.out, p.o_stride, static_cast<long long>(t.own.start) + r0, n, p.D, h, ty, tx, acc, mul);
+    if (p.splits > 1)   // rows of D floats, one head
+        store_rows<float, DP>(p.part_o + (static_cast<long long>(blockIdx.z) * p.heads + h) * p.q_rows * p.D, p.D,
+                              static_cast<long long>(t.own.start) + r0, n, p.D, 0, ty, tx, acc, mul);
+    else
+        store_rows<T, DP>(p.out, p.o_stride, static_cast<long long>(t.own.start) + r0, n, p.D, h, ty, tx, acc, mul);
 }
 
 // dk and dv: a tile of 64 keys walks the query rows that see it, for each query head of its group.

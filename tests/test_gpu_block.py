@@ -167,11 +167,15 @@ SELF = [
     ([63, 65, 1, 0, 128, 129, 200], 2, 1, 64, True), ([63, 65, 1, 0, 128, 129, 200], 2, 2, 128, False),
     ([5, 0, 0, 3], 6, 2, 40, True), ([256, 255, 257], 3, 1, 72, True), ([700], 2, 2, 96, False),
     ([130, 12], 4, 1, 16, False), ([31] * 9, 2, 1, 24, True), ([0, 0, 17], 1, 1, 32, False),
-    ([385, 2, 640], 2, 1, 120, True), ([2] * 70, 1, 1, 56, True), ([1] * 40 + [300], 2, 1, 128, True),
+    ([385, 2, 640], 2, 1, 120, True), ([2] * 70, 1, 1, 56, True), ([16] * 7, 5, 1, 128, True),
+    ([17, 30, 1, 32] * 3, 3, 3, 64, False), ([20] * 30 + [200, 0, 129], 6, 3, 80, True), ([1] * 40 + [300], 2, 1, 128, True),
 ]
 CROSS = [
     ([1, 1, 1], [300, 0, 7], 4, 2, 64, False), ([10, 0, 130, 3], [0, 20, 50, 400], 2, 1, 128, True),
     ([1], [2000], 8, 2, 64, False), ([200], [70], 2, 2, 48, True), ([5, 129], [513, 128], 3, 1, 80, False),
+    ([1, 0, 3, 1], [700, 50, 0, 1000], 6, 2, 128, True), ([2, 1], [300, 900], 12, 4, 72, False),
+    ([1] * 20, [200 + 7 * i for i in range(20)], 2, 1, 40, False), ([1, 1], [4000, 3], 8, 1, 64, False),
+    ([5, 1, 9], [600, 400, 8], 1, 1, 16, True), ([30], [5000], 1, 1, 128, True),
     ([0, 0], [5, 9], 2, 1, 64, True), ([5, 9], [0, 0], 2, 1, 64, True), ([2], [1500], 2, 1, 128, True),
 ]
 
