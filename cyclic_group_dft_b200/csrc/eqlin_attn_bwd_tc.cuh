@@ -9,7 +9,7 @@
 // Computing S and dP twice costs two more products than one kernel would (7 for 5), and saves the
 // atomics or the fp32 copy of dq that one kernel needs.
 // Warps: two warpgroups of 128 threads for the elementwise work (thread = TMEM lane; each warpgroup
-// takes 64 of the 128 columns), one warp of loads, one of MMAs.
+// takes 64 of the 128 columns, and its 32 words of the A operand lie at the start of them), one warp of loads, one of MMAs.
 #pragma once
 
 #include "eqlin_attn_tc.cuh"
@@ -34,12 +34,6 @@ struct BwdParams {
     Params p;
     long long stop_after;    // test hook, as in FwdParams
 };
-
-// the A operand in TMEM whose K index runs over 64 columns of each warpgroup: words [0, 32) and [64, 96)
-__device__ __forceinline__ void mma_rows_halves(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool add) {
-    for (int s = 0; s < 8; ++s)
-        umma_f16_ts(d, a + (s >> 2) * 64 + (s & 3) * 8, desc_mn(b + s * 2048), idesc, add || s > 0);
-}
 
 // 128 rows x D features of an fp32 accumulator in TMEM, times `mul`, to the rows of an output.
 template <class T>
@@ -86,7 +80,7 @@ __global__ void __launch_bounds__(Bwd<DP>::THREADS, 1)
                    rows_full = bar(2 * ST + 6);
     uint8_t *k_tile = base, *v_tile = base + B::TILE_BYTES, *ring = base + 2 * B::TILE_BYTES;
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;   // (uniform)
     if (threadIdx.x == 0) {
         ctl->abort = 0;
         for (int s = 0; s < ST; ++s) {
@@ -96,9 +90,9 @@ __global__ void __launch_bounds__(Bwd<DP>::THREADS, 1)
         ptx::mbar_init(fixed_full, 1);
         ptx::mbar_init(s_full, 1);
         ptx::mbar_init(dp_full, 1);
-        ptx::mbar_init(p_full, 256);
-        ptx::mbar_init(rows_full, 256);
-        ptx::mbar_init(ds_full, 256);
+        ptx::mbar_init(p_full, 8);
+        ptx::mbar_init(rows_full, 8);
+        ptx::mbar_init(ds_full, 8);
         ptx::mbar_init(done, 1);
         ptx::fence_mbar_init();
     }
@@ -161,8 +155,8 @@ __global__ void __launch_bounds__(Bwd<DP>::THREADS, 1)
                 return true;
             };
             auto product = [&](uint32_t d, uint8_t* fixed, int u, uint32_t b) {
-                if (lane == 0) {
-                    mma_features(d, ptx::smem_u32(fixed), ptx::smem_u32(stage(u)), steps, id_s);
+                if (elect_one()) {
+                    mma_features<DP>(d, ptx::smem_u32(fixed), ptx::smem_u32(stage(u)), steps, id_s);
                     ptx::umma_commit(b);
                 }
                 __syncwarp();
@@ -174,7 +168,7 @@ __global__ void __launch_bounds__(Bwd<DP>::THREADS, 1)
             for (int j = 0; ok && j < n; ++j) {
                 if (!(ok = wait_warp(p_full, j & 1, ctl, p.timeout_ns))) break;
                 ptx::tc_fence_after();
-                if (lane == 0) mma_rows_halves(t_dv, t_s, ptx::smem_u32(stage(2 * j + 1)), id_o, j > 0);
+                if (elect_one()) mma_rows<64>(t_dv, t_s, ptx::smem_u32(stage(2 * j + 1)), id_o, j > 0);
                 __syncwarp();
                 // MMAs of one thread run in order: S^T is written after P^T has been read out of it
                 if (j + 1 < n) {
@@ -183,8 +177,8 @@ __global__ void __launch_bounds__(Bwd<DP>::THREADS, 1)
                 }
                 if (!(ok = wait_warp(ds_full, j & 1, ctl, p.timeout_ns))) break;
                 ptx::tc_fence_after();
-                if (lane == 0) {
-                    mma_rows_halves(t_dk, t_dp, ptx::smem_u32(stage(2 * j)), id_o, j > 0);
+                if (elect_one()) {
+                    mma_rows<64>(t_dk, t_dp, ptx::smem_u32(stage(2 * j)), id_o, j > 0);
                     ptx::umma_commit(empty((2 * j) % ST));
                     ptx::umma_commit(empty((2 * j + 1) % ST));
                 }
@@ -194,7 +188,7 @@ __global__ void __launch_bounds__(Bwd<DP>::THREADS, 1)
                     product(t_dp, v_tile, 2 * j + 3, dp_full);
                 }
             }
-            if (lane == 0) {
+            if (elect_one()) {
                 ptx::umma_commit(done);
                 drain_wait(done, 0, p.timeout_ns);
             }
@@ -223,7 +217,7 @@ __global__ void __launch_bounds__(Bwd<DP>::THREADS, 1)
             float2* rj = rows + (j & 1) * kTile;
             // tile j - 2, which had this buffer, is read: dP of tile j - 1 was issued after all threads' dS of it
             reinterpret_cast<float*>(rj + (tid & 127))[half] = next;
-            ptx::mbar_arrive(rows_full);
+            arrive_warp(rows_full, lane);
             if (j + 1 < n) next = fetch(j + 1);
             if (!(ok = wait_warp(rows_full, j & 1, ctl, p.timeout_ns))) break;
             if (!(ok = wait_warp(s_full, j & 1, ctl, p.timeout_ns))) break;
@@ -260,7 +254,7 @@ __global__ void __launch_bounds__(Bwd<DP>::THREADS, 1)
             }
             tmem_wait_st();
             ptx::tc_fence_before();
-            ptx::mbar_arrive(p_full);
+            arrive_warp(p_full, lane);
             if (!(ok = wait_warp(dp_full, j & 1, ctl, p.timeout_ns))) break;
             ptx::tc_fence_after();
 #pragma unroll
@@ -281,7 +275,7 @@ __global__ void __launch_bounds__(Bwd<DP>::THREADS, 1)
             }
             tmem_wait_st();
             ptx::tc_fence_before();
-            ptx::mbar_arrive(ds_full);
+            arrive_warp(ds_full, lane);
         }
         if (ok && n > 0) ok = wait_warp(done, 0, ctl, p.timeout_ns);
         if (ok && t.tile >= 0) {
@@ -319,7 +313,7 @@ __global__ void __launch_bounds__(Bwd<DP>::THREADS, 1)
     auto s_full = [&](int b) { return bar(2 * ST + 4 + b); };
     uint8_t *q_tile = base, *do_tile = base + B::TILE_BYTES, *ring = base + 2 * B::TILE_BYTES;
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;   // (uniform)
     if (threadIdx.x == 0) {
         ctl->abort = 0;
         for (int s = 0; s < ST; ++s) {
@@ -328,7 +322,7 @@ __global__ void __launch_bounds__(Bwd<DP>::THREADS, 1)
         }
         ptx::mbar_init(fixed_full, 1);
         ptx::mbar_init(dp_full, 1);
-        ptx::mbar_init(ds_full, 256);
+        ptx::mbar_init(ds_full, 8);
         ptx::mbar_init(done, 1);
         ptx::mbar_init(s_full(0), 1);
         ptx::mbar_init(s_full(1), 1);
@@ -390,8 +384,8 @@ __global__ void __launch_bounds__(Bwd<DP>::THREADS, 1)
                 if (!wait_stage(2 * j)) return false;
                 const int valid = kr.len - j * kTile;
                 if (valid < kTile) zero_tail(stage(2 * j), B::BOXES, valid, lane);
-                if (lane == 0) {
-                    mma_features(t_s(j), ptx::smem_u32(q_tile), ptx::smem_u32(stage(2 * j)), steps, id_s);
+                if (elect_one()) {
+                    mma_features<DP>(t_s(j), ptx::smem_u32(q_tile), ptx::smem_u32(stage(2 * j)), steps, id_s);
                     ptx::umma_commit(s_full(j & 1));
                 }
                 __syncwarp();
@@ -399,8 +393,8 @@ __global__ void __launch_bounds__(Bwd<DP>::THREADS, 1)
             };
             auto dp = [&](int j) {
                 if (!wait_stage(2 * j + 1)) return false;
-                if (lane == 0) {
-                    mma_features(t_dp, ptx::smem_u32(do_tile), ptx::smem_u32(stage(2 * j + 1)), steps, id_s);
+                if (elect_one()) {
+                    mma_features<DP>(t_dp, ptx::smem_u32(do_tile), ptx::smem_u32(stage(2 * j + 1)), steps, id_s);
                     ptx::umma_commit(dp_full);
                     ptx::umma_commit(empty((2 * j + 1) % ST));
                 }
@@ -414,15 +408,15 @@ __global__ void __launch_bounds__(Bwd<DP>::THREADS, 1)
                 if (!(ok = wait_warp(ds_full, j & 1, ctl, p.timeout_ns))) break;
                 ptx::tc_fence_after();
                 if (j + 1 < n && !(ok = dp(j + 1))) break;
-                if (lane == 0) {
-                    mma_rows_halves(t_dq, t_s(j), ptx::smem_u32(stage(2 * j)), id_o, j > 0);
+                if (elect_one()) {
+                    mma_rows<64>(t_dq, t_s(j), ptx::smem_u32(stage(2 * j)), id_o, j > 0);
                     ptx::umma_commit(empty((2 * j) % ST));
                 }
                 __syncwarp();
                 // MMAs of one thread run in order: S_{j+2} is written after dS_j has been read
                 if (j + 2 < n) ok = scores(j + 2);
             }
-            if (lane == 0) {
+            if (elect_one()) {
                 ptx::umma_commit(done);
                 drain_wait(done, 0, p.timeout_ns);
             }
@@ -487,7 +481,7 @@ __global__ void __launch_bounds__(Bwd<DP>::THREADS, 1)
             }
             tmem_wait_st();
             ptx::tc_fence_before();
-            ptx::mbar_arrive(ds_full);
+            arrive_warp(ds_full, lane);
         }
         if (ok && n > 0) ok = wait_warp(done, 0, ctl, p.timeout_ns);
         if (ok && t.tile >= 0 && half == 0) {

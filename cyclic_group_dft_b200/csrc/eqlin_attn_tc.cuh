@@ -31,15 +31,16 @@ struct Ctl {
     uint32_t tmem_base;
 };
 
-// Bounded mbarrier wait.  Returns false (after flagging) on timeout or abort.
+// Bounded mbarrier wait.  Returns false (after flagging) on timeout or abort.  The limit is counted in SM
+// cycles, two for each nanosecond (the SM clock is below 2 GHz).
 __device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, Ctl* ctl, unsigned long long timeout_ns) {
     if (ptx::mbar_try_wait(bar, parity)) return true;
-    const uint64_t t0 = ptx::globaltimer_ns();
+    const long long t0 = clock64();
     for (uint32_t spin = 1;; ++spin) {
         if (ptx::mbar_try_wait_sleep(bar, parity, kWaitSleepNs)) return true;
         if ((spin & 7u) == 0) {
             if (ctl->abort) return false;
-            if (ptx::globaltimer_ns() - t0 > timeout_ns) {
+            if (static_cast<unsigned long long>(clock64() - t0) > 2 * timeout_ns) {
                 ctl->abort = 1;
                 atomicCAS(&g_status, 0, kErrTimeout);
                 return false;
@@ -51,11 +52,28 @@ __device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, Ctl*
 __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, Ctl* ctl, unsigned long long timeout_ns) {
     return __all_sync(0xFFFFFFFFu, wait_bounded(bar, parity, ctl, timeout_ns));
 }
+// True in one lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t is;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xFFFFFFFF;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(is));
+    return is != 0;
+}
+// One arrival for a whole warp (all lanes' work before it included): 32 single ones on one barrier would be
+// carried out one after the other.
+__device__ __forceinline__ void arrive_warp(uint32_t bar, int lane) {
+    __syncwarp();
+    if (lane == 0) ptx::mbar_arrive(bar);
+}
 // Bounded wait that ignores the abort flag, for copies or MMAs in flight before exit.
 __device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity, unsigned long long timeout_ns) {
-    const uint64_t t0 = ptx::globaltimer_ns();
-    while (!ptx::mbar_try_wait(bar, parity)) {
-        if (ptx::globaltimer_ns() - t0 > timeout_ns) {
+    if (ptx::mbar_try_wait(bar, parity)) return;
+    const long long t0 = clock64();
+    while (!ptx::mbar_try_wait_sleep(bar, parity, kWaitSleepNs)) {
+        if (static_cast<unsigned long long>(clock64() - t0) > 2 * timeout_ns) {
             atomicCAS(&g_status, 0, kErrTimeout);
             return;
         }
@@ -107,30 +125,91 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;"
+        : "=l"(reinterpret_cast<uint64_t&>(d))
+        : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)), "l"(reinterpret_cast<uint64_t&>(c)));
+    return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 d;
+    asm("add.rn.f32x2 %0, %1, %2;"
+        : "=l"(reinterpret_cast<uint64_t&>(d))
+        : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)));
+    return d;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
 // Descriptors of a tile, split in halves (the low half carries the start address >> 4).
 //   K-major SWIZZLE_128B: 8-row groups 1 KB apart; 16 features further: + 32 bytes; box: + 16 KB.
 //   MN-major SWIZZLE_128B: K groups of 8 rows 1 KB apart, the next 64 features one box (16 KB) on;
 //   16 rows further: + 2 KB.
-__device__ __forceinline__ uint64_t desc_k(uint32_t start) {
-    constexpr uint32_t hi = (1024u >> 4) | (1u << 14) | (2u << 29);
-    return (static_cast<uint64_t>(hi) << 32) | (1u << 16) | (start >> 4);
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 d;
+    asm("mul.rn.f32x2 %0, %1, %2;"
+        : "=l"(reinterpret_cast<uint64_t&>(d))
+        : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)));
+    return d;
 }
-__device__ __forceinline__ uint64_t desc_mn(uint32_t start) {
-    constexpr uint32_t hi = (1024u >> 4) | (1u << 14) | (2u << 29);
-    return (static_cast<uint64_t>(hi) << 32) | ((static_cast<uint32_t>(kBoxBytes) >> 4) << 16) | (start >> 4);
+// 2^x of two values in the FMA pipes (the exponential unit does 16 a cycle and SM, and bounds these kernels
+// where a head has 64 features).  x = n + f, n the nearest integer: adding 1.5 * 2^23 leaves n in the low
+// bits, 2^f is a polynomial, 2^n is built from its bits (Cody and Waite's reduction; the coefficients are a
+// Remez fit of the relative error on [-1/2, 1/2]: 2.7e-6 = 2^-18.5 with the fp32 evaluation, far below the
+// 2^-9 of the weights' rounding).  x <= 100; x <= -127, -infinity among it, gives exactly 0; NaN stays NaN.
+__device__ __forceinline__ float2 ex2_fma(float2 x) {
+    asm("max.NaN.f32 %0, %0, %1;" : "+f"(x.x) : "f"(-127.f));
+    asm("max.NaN.f32 %0, %0, %1;" : "+f"(x.y) : "f"(-127.f));
+    const float2 big = make_float2(12582912.f, 12582912.f), neg = make_float2(-12582912.f, -12582912.f);
+    const float2 t = add2(x, big);
+    const float2 n = add2(t, neg);
+    const float2 f = fma2(n, make_float2(-1.f, -1.f), x);
+    float2 p = fma2(f, make_float2(0.009570102207362652f, 0.009570102207362652f),
+                    make_float2(0.05591785907745361f, 0.05591785907745361f));
+    p = fma2(p, f, make_float2(0.240247443318367f, 0.240247443318367f));
+    p = fma2(p, f, make_float2(0.6931217908859253f, 0.6931217908859253f));
+    p = fma2(p, f, make_float2(0.9999992847442627f, 0.9999992847442627f));
+    return mul2(p, make_float2(__uint_as_float((__float_as_uint(t.x) << 23) + 0x3F800000u),
+                               __uint_as_float((__float_as_uint(t.y) << 23) + 0x3F800000u)));
 }
-// D[128 x 128] = A B^T over `steps` * 16 features, both tiles K-major.
+// 2^x of pair number `pair`: by the FMA pipes where its bit of MASK (of 8) is set.
+template <uint32_t MASK>
+__device__ __forceinline__ float2 ex2_pair(float2 x, int pair) {
+    if ((MASK >> (pair & 7)) & 1u) return ex2_fma(x);
+    return make_float2(ex2(x.x), ex2(x.y));
+}
+
+// The high halves of both descriptors are the same constant; the loops below only add to the low ones, and
+// are unrolled: one thread issues all MMAs, and what it computes between two of them delays the second.
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint64_t desc_of(uint32_t lo) { return (static_cast<uint64_t>(kDescHi) << 32) | lo; }
+__device__ __forceinline__ uint32_t desc_k_lo(uint32_t start) { return (1u << 16) | (start >> 4); }
+__device__ __forceinline__ uint32_t desc_mn_lo(uint32_t start) {
+    return ((static_cast<uint32_t>(kBoxBytes) >> 4) << 16) | (start >> 4);
+}
+// D[128 x 128] = A B^T over `steps` * 16 of DP features, both tiles K-major.
+template <int DP>
 __device__ __forceinline__ void mma_features(uint32_t d, uint32_t a, uint32_t b, int steps, uint32_t idesc) {
-    for (int s = 0; s < steps; ++s) {
-        const uint32_t off = static_cast<uint32_t>(s >> 2) * kBoxBytes + static_cast<uint32_t>(s & 3) * 32;
-        ptx::umma_f16(d, desc_k(a + off), desc_k(b + off), idesc, s > 0);
+    const uint32_t la = desc_k_lo(a), lb = desc_k_lo(b);
+#pragma unroll
+    for (int s = 0; s < DP / 16; ++s) {
+        const uint32_t off = (static_cast<uint32_t>(s >> 2) * kBoxBytes + static_cast<uint32_t>(s & 3) * 32) >> 4;
+        if (s < steps) ptx::umma_f16(d, desc_of(la + off), desc_of(lb + off), idesc, s > 0);
     }
 }
-// D[128 x N] (+)= A[tmem, 128 x 128] B over the 128 rows of tile b.
-__device__ __forceinline__ void mma_rows(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool add, int s0 = 0,
-                                         int s1 = 8) {
-    for (int s = s0; s < s1; ++s)
-        umma_f16_ts(d, a + s * 8, desc_mn(b + s * 2048), idesc, add || s > 0);
+// D[128 x N] (+)= A[tmem, 128 x 128] B over the 128 rows of tile b.  GAP: distance in TMEM between A's
+// first and second 64 K elements (32 columns when A is contiguous).
+template <int GAP, int FROM = 0, int TO = 8>
+__device__ __forceinline__ void mma_rows(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool add) {
+    const uint32_t lb = desc_mn_lo(b);
+#pragma unroll
+    for (int s = FROM; s < TO; ++s)
+        umma_f16_ts(d, a + (s >> 2) * GAP + (s & 3) * 8, desc_of(lb + s * (2048 >> 4)), idesc, add || s > 0);
 }
 constexpr uint32_t kBMnMajor = 1u << 16;         // instruction descriptor: B is MN-major
 
@@ -149,7 +228,7 @@ __device__ __forceinline__ void zero_tail(uint8_t* tile, int boxes, int valid, i
 // A block takes NQ tiles of 128 query rows of one head and walks their keys in tiles of 128.  Warps:
 // NQ warpgroups of softmax (thread = query row = TMEM lane), one warp of loads, one of MMAs.
 //   S_i = Q_i K^T                      (SS product, fp32 in TMEM)
-//   m, l running maximum and sum; P = exp2(c (S - m)) rounded to the I/O type, over S in TMEM
+//   m, l running maximum and sum; P = exp2(c (S - m)) rounded to the I/O type, in TMEM
 //   O_i += P V                         (A from TMEM)
 // The maximum that P refers to moves only when the true one has grown by more than 2^8: until then
 // P stays below 2^8, and the rescaling of O (a round trip through registers) is rarely needed.
@@ -162,7 +241,14 @@ struct Fwd {
     static constexpr int STAGES = NQ == 2 ? (227 * 1024 - 2048) / TILE_BYTES - NQ : 4;
     static constexpr int THREADS = NQ * 128 + 64;
     static constexpr int WARP_LOAD = NQ * 4, WARP_MMA = NQ * 4 + 1;
-    static constexpr int TMEM_COLS = NQ * (128 + DP) <= 256 ? 256 : 512;
+    // with room in TMEM, P gets columns of its own, and the scores of the next tile are computed while
+    // this one's weights are
+    static constexpr bool OWN_P = NQ * (128 + DP + 64) <= (NQ == 1 ? 256 : 512);
+    static constexpr int TMEM_COLS = NQ == 1 ? 256 : 512;
+    // Share of the exponentials in the FMA pipes, of 8 pairs.  D <= 64: us for a tile of 128 x 128 with two
+    // blocks on an SM: none 0.84, 2 of 8 0.75, 3 of 8 0.80, 4 of 8 0.85.  D = 128, where the products take
+    // twice as long: none 0.90, 2 of 8 0.94.
+    static constexpr uint32_t EX2_FMA = DP == 64 ? 0x44 : 0;
     static constexpr size_t SMEM = 1024 + 512 + static_cast<size_t>(STAGES + NQ) * TILE_BYTES;
 };
 
@@ -190,11 +276,13 @@ __global__ void __launch_bounds__(Fwd<DP, NQ>::THREADS, NQ == 2 ? 1 : 2)
     auto s_full = [&](int i) { return bar(2 * ST + NQ + i); };
     auto p_full = [&](int i) { return bar(2 * ST + 2 * NQ + i); };
     auto o_full = [&](int i) { return bar(2 * ST + 3 * NQ + i); };
-    const uint32_t drained = bar(2 * ST + 4 * NQ);
+    auto s_read = [&](int i) { return bar(2 * ST + 4 * NQ + i); };
+    auto p_half = [&](int i) { return bar(2 * ST + 5 * NQ + i); };   // the weights of the first 64 keys
+    const uint32_t drained = bar(2 * ST + 6 * NQ);
     uint8_t* q_tile = base;
     uint8_t* ring = base + NQ * F::TILE_BYTES;
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;   // (uniform)
     if (threadIdx.x == 0) {
         ctl->abort = 0;
         for (int s = 0; s < ST; ++s) {
@@ -204,8 +292,10 @@ __global__ void __launch_bounds__(Fwd<DP, NQ>::THREADS, NQ == 2 ? 1 : 2)
         for (int i = 0; i < NQ; ++i) {
             ptx::mbar_init(q_full(i), 1);
             ptx::mbar_init(s_full(i), 1);
-            ptx::mbar_init(p_full(i), 128);
+            ptx::mbar_init(p_full(i), 4);
+            ptx::mbar_init(p_half(i), 4);
             ptx::mbar_init(o_full(i), 1);
+            ptx::mbar_init(s_read(i), 4);
         }
         ptx::mbar_init(drained, 1);
         ptx::fence_mbar_init();
@@ -241,6 +331,7 @@ __global__ void __launch_bounds__(Fwd<DP, NQ>::THREADS, NQ == 2 ? 1 : 2)
     const uint32_t tmem = ctl->tmem_base;
     auto t_s = [&](int i) { return tmem + i * 128; };
     auto t_o = [&](int i) { return tmem + NQ * 128 + i * DP; };
+    auto t_p = [&](int i) { return F::OWN_P ? tmem + NQ * (128 + DP) + i * 64 : t_s(i); };
 
     if (warp == F::WARP_LOAD) {
         if (lane == 0 && n > 0) {
@@ -274,60 +365,85 @@ __global__ void __launch_bounds__(Fwd<DP, NQ>::THREADS, NQ == 2 ? 1 : 2)
             const uint32_t id_o = idesc_f16kind_f32(128, (p.D + 15) / 16 * 16, Io16<T>::kUmmaFormat, false) | kBMnMajor;
             const int steps = (p.D + 15) / 16;
             bool ok = true;
-            auto stage = [&](int u) { return ring + (u % ST) * F::TILE_BYTES; };
-            auto wait_stage = [&](int u) { return wait_warp(full(u % ST), (u / ST) & 1, ctl, p.timeout_ns); };
-            auto scores = [&](int i, int u) {
-                if (lane == 0) {
-                    mma_features(t_s(i), ptx::smem_u32(q_tile + i * F::TILE_BYTES), ptx::smem_u32(stage(u)), steps, id_s);
+            // ring position of a tile of keys (from 0) or values (from 1); both move on by two
+            struct At {
+                int s;
+                uint32_t ph;
+                __device__ void next() {
+                    s += 2;
+                    if (s >= ST) {
+                        s -= ST;
+                        ph ^= 1;
+                    }
+                }
+            };
+            At ks = {0, 0}, vs = {1 % ST, 1 / ST};
+            const uint32_t ring32 = ptx::smem_u32(ring), q32 = ptx::smem_u32(q_tile);
+            auto wait_stage = [&](const At& a) { return wait_warp(full(a.s), a.ph, ctl, p.timeout_ns); };
+            auto scores = [&](int i) {
+                if (elect_one()) {
+                    mma_features<DP>(t_s(i), q32 + i * F::TILE_BYTES, ring32 + ks.s * F::TILE_BYTES, steps, id_s);
                     ptx::umma_commit(s_full(i));
                 }
                 __syncwarp();
             };
-            ok = wait_stage(0);
+            ok = wait_stage(ks);
 #pragma unroll
             for (int i = 0; i < NQ; ++i)
                 if (ok && count[i] > 0) {
                     ok = wait_warp(q_full(i), 0, ctl, p.timeout_ns);
                     ptx::tc_fence_after();
-                    if (ok) scores(i, 0);
+                    if (ok) scores(i);
                 }
-            if (ok && lane == 0) ptx::umma_commit(empty(0));
+            if (ok && elect_one()) ptx::umma_commit(empty(ks.s));
+            ks.next();
             for (int j = 0; ok && j < n; ++j) {
                 bool have_v = false, have_k = false;
+                // the next scores of tile i: its S is free once it has been read (or, where P lies over
+                // it, once the product that reads P has been issued: MMAs of one thread run in order)
+                auto next_scores = [&](int i) {
+                    if (!have_k) {
+                        have_k = true;
+                        if (!wait_stage(ks)) return false;
+                    }
+                    if (F::OWN_P && !wait_warp(s_read(i), j & 1, ctl, p.timeout_ns)) return false;
+                    ptx::tc_fence_after();
+                    scores(i);
+                    return true;
+                };
 #pragma unroll
                 for (int i = 0; i < NQ; ++i) {
                     if (!ok || j >= count[i]) continue;
+                    if (F::OWN_P && j + 1 < count[i] && !(ok = next_scores(i))) break;
                     if (!have_v) {
                         have_v = true;
-                        if (!(ok = wait_stage(2 * j + 1))) break;
+                        if (!(ok = wait_stage(vs))) break;
                         const int valid = kr.len - j * kTile;
-                        if (valid < kTile) zero_tail(stage(2 * j + 1), F::BOXES, valid, lane);
+                        if (valid < kTile) zero_tail(ring + vs.s * F::TILE_BYTES, F::BOXES, valid, lane);
                     }
+                    // the product with the first half of the weights runs while the second is computed
+                    if (!(ok = wait_warp(p_half(i), j & 1, ctl, p.timeout_ns))) break;
+                    ptx::tc_fence_after();
+                    if (elect_one()) mma_rows<32, 0, 4>(t_o(i), t_p(i), ring32 + vs.s * F::TILE_BYTES, id_o, j > 0);
+                    __syncwarp();
                     if (!(ok = wait_warp(p_full(i), j & 1, ctl, p.timeout_ns))) break;
                     ptx::tc_fence_after();
-                    if (lane == 0) {
-                        mma_rows(t_o(i), t_s(i), ptx::smem_u32(stage(2 * j + 1)), id_o, j > 0);
+                    if (elect_one()) {
+                        mma_rows<32, 4, 8>(t_o(i), t_p(i), ring32 + vs.s * F::TILE_BYTES, id_o, j > 0);
                         ptx::umma_commit(o_full(i));
                     }
                     __syncwarp();
-                    if (j + 1 < count[i]) {
-                        // S_i is written after the product above has read P_i out of it: MMAs of one
-                        // thread run in order
-                        if (!have_k) {
-                            have_k = true;
-                            if (!(ok = wait_stage(2 * j + 2))) break;
-                            ptx::tc_fence_after();
-                        }
-                        scores(i, 2 * j + 2);
-                    }
+                    if (!F::OWN_P && j + 1 < count[i] && !(ok = next_scores(i))) break;
                 }
-                if (ok && lane == 0) {
-                    ptx::umma_commit(empty((2 * j + 1) % ST));
-                    if (j + 1 < n) ptx::umma_commit(empty((2 * j + 2) % ST));
+                if (ok && elect_one()) {
+                    ptx::umma_commit(empty(vs.s));
+                    if (j + 1 < n) ptx::umma_commit(empty(ks.s));
                 }
+                vs.next();
+                ks.next();
             }
             // every MMA, and every arrival that one owes a barrier, before shared memory and TMEM go
-            if (lane == 0) {
+            if (elect_one()) {
                 ptx::umma_commit(drained);
                 drain_wait(drained, 0, p.timeout_ns);
             }
@@ -339,7 +455,7 @@ __global__ void __launch_bounds__(Fwd<DP, NQ>::THREADS, NQ == 2 ? 1 : 2)
         const int row = r0 + i * kTile + (threadIdx.x & 127);      // row of the sequence
         const bool live = t.tile >= 0 && row < t.own.len;
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-        const uint32_t ts = t_s(i) + lanes, to = t_o(i) + lanes;
+        const uint32_t ts = t_s(i) + lanes, to = t_o(i) + lanes, tp = t_p(i) + lanes;
         // keys this row sees
         const int seen = live ? keys_seen(row, t.own.len, kr.len, p.causal) : 0;
         // keys that every row of the tile sees: tiles below need no mask
@@ -356,6 +472,10 @@ __global__ void __launch_bounds__(Fwd<DP, NQ>::THREADS, NQ == 2 ? 1 : 2)
             ptx::tmem_wait_ld();
 #pragma unroll
             for (int c = 0; c < 4; ++c) ptx::tmem_regs_ready(s[c]);
+            if (F::OWN_P) {
+                ptx::tc_fence_before();
+                arrive_warp(s_read(i), lane);
+            }
             if ((j + 1) * kTile > seen_all) {
                 const int n_seen = seen - j * kTile;
 #pragma unroll
@@ -364,15 +484,12 @@ __global__ void __launch_bounds__(Fwd<DP, NQ>::THREADS, NQ == 2 ? 1 : 2)
                     for (int e = 0; e < 32; ++e)
                         if (c * 32 + e >= n_seen) s[c][e] = 0xFF800000u;
             }
-            float m0 = -INFINITY, m1 = -INFINITY, m2 = -INFINITY, m3 = -INFINITY;
+            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-            for (int e = 0; e < 32; ++e) {
-                m0 = fmaxf(m0, __uint_as_float(s[0][e]));
-                m1 = fmaxf(m1, __uint_as_float(s[1][e]));
-                m2 = fmaxf(m2, __uint_as_float(s[2][e]));
-                m3 = fmaxf(m3, __uint_as_float(s[3][e]));
-            }
-            const float m = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3));
+            for (int e = 0; e < 32; e += 2)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) mx[c] = max3(mx[c], __uint_as_float(s[c][e]), __uint_as_float(s[c][e + 1]));
+            const float m = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
             bool move = (m - top) * c2 > 8.f;                       // also the first finite maximum
             if (j == 0) {
                 top = m;
@@ -394,23 +511,32 @@ __global__ void __launch_bounds__(Fwd<DP, NQ>::THREADS, NQ == 2 ? 1 : 2)
                 }
             }
             const float off = top == -INFINITY ? 0.f : -top * c2;
-            float part[4] = {0.f, 0.f, 0.f, 0.f};
+            const float2 c22 = make_float2(c2, c2), off2 = make_float2(off, off);
+            float2 part[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
                 uint32_t w[16];
 #pragma unroll
                 for (int e = 0; e < 32; e += 2) {
-                    const float a = ex2(fmaf(__uint_as_float(s[c][e]), c2, off));
-                    const float b = ex2(fmaf(__uint_as_float(s[c][e + 1]), c2, off));
-                    part[(e >> 1) & 3] += a + b;
-                    w[e >> 1] = Io16<T>::pack(a, b);
+                    float2 a = fma2(make_float2(__uint_as_float(s[c][e]), __uint_as_float(s[c][e + 1])), c22, off2);
+                    a = ex2_pair<F::EX2_FMA>(a, e >> 1);
+                    part[(e >> 1) & 1] = add2(part[(e >> 1) & 1], a);
+                    w[e >> 1] = Io16<T>::pack(a.x, a.y);
                 }
-                tmem_st16(ts + c * 16, w);
+                // P of the tile before has been read
+                if (F::OWN_P && c == 0 && j > 0 && !(ok = wait_warp(o_full(i), (j - 1) & 1, ctl, p.timeout_ns))) break;
+                tmem_st16(tp + c * 16, w);
+                if (c == 1) {
+                    tmem_wait_st();
+                    ptx::tc_fence_before();
+                    arrive_warp(p_half(i), lane);
+                }
             }
-            sum += (part[0] + part[1]) + (part[2] + part[3]);
+            if (!ok) break;
+            sum += (part[0].x + part[0].y) + (part[1].x + part[1].y);
             tmem_wait_st();
             ptx::tc_fence_before();
-            ptx::mbar_arrive(p_full(i));
+            arrive_warp(p_full(i), lane);
         }
         if (ok && cnt > 0) ok = wait_warp(o_full(i), (cnt - 1) & 1, ctl, p.timeout_ns);
         if (ok && t.tile >= 0) {
