@@ -42,6 +42,21 @@ for _f in ("eqlin_attention_device_status", "eqlin_add_rmsnorm", "eqlin_add_rmsn
     getattr(_lib, _f).restype = _int
 
 
+_current_stream = torch._C._cuda_getCurrentRawStream   # of a device number; the public call makes a Stream object
+
+
+def _run(name: str, device: torch.device, stream, *args) -> None:
+    """Calls library function `name` with `args` and the stream, with `device` current."""
+    f = getattr(_lib, name)
+    if torch.cuda.current_device() == device.index:
+        status = f(*args, _current_stream(device.index) if stream is None else _stream_ptr(stream))
+    else:
+        with torch.cuda.device(device):
+            status = f(*args, _stream_ptr(stream))
+    if status:
+        _check(status, name)
+
+
 def _features(t: torch.Tensor, name: str) -> None:
     if t.dim() != 3:
         raise ValueError(f"{name} must be [N, C, G], got {tuple(t.shape)}")
@@ -107,10 +122,8 @@ def eqlin_add_rmsnorm(x: torch.Tensor, residual: torch.Tensor | None = None, wei
         sum_out = torch.empty_like(x)
     if sum_out is not None and N > 0 and sum_out.data_ptr() == y.data_ptr():
         raise ValueError("y and sum_out must not be the same tensor")
-    with torch.cuda.device(x.device):
-        _check(_lib.eqlin_add_rmsnorm(x.data_ptr(), _ptr(residual), _ptr(weight), y.data_ptr(), _ptr(sum_out), N, C,
-                                      G, eps, _w_code(weight), _TORCH_TO_EQLIN[x.dtype], _stream_ptr(stream)),
-               "eqlin_add_rmsnorm")
+    _run("eqlin_add_rmsnorm", x.device, stream, x.data_ptr(), _ptr(residual), _ptr(weight), y.data_ptr(), _ptr(sum_out),
+         N, C, G, eps, _w_code(weight), _TORCH_TO_EQLIN[x.dtype])
     return y, (x if sum_out is None else sum_out)
 
 
@@ -131,10 +144,8 @@ def eqlin_add_rmsnorm_fp8(x: torch.Tensor, residual: torch.Tensor | None = None,
         raise ValueError(f"scale must be a contiguous [{N}] fp32 tensor on {x.device}")
     if sum_out is None and residual is not None:
         sum_out = torch.empty_like(x)
-    with torch.cuda.device(x.device):
-        _check(_lib.eqlin_add_rmsnorm_fp8(x.data_ptr(), _ptr(residual), _ptr(weight), y.data_ptr(), scale.data_ptr(),
-                                          _ptr(sum_out), N, C, G, eps, _w_code(weight), _TORCH_TO_EQLIN[x.dtype],
-                                          _stream_ptr(stream)), "eqlin_add_rmsnorm_fp8")
+    _run("eqlin_add_rmsnorm_fp8", x.device, stream, x.data_ptr(), _ptr(residual), _ptr(weight), y.data_ptr(),
+         scale.data_ptr(), _ptr(sum_out), N, C, G, eps, _w_code(weight), _TORCH_TO_EQLIN[x.dtype])
     return y, scale, (x if sum_out is None else sum_out)
 
 
@@ -174,11 +185,9 @@ def eqlin_rmsnorm_backward(dy: torch.Tensor, r: torch.Tensor, weight: torch.Tens
             need = eqlin_rmsnorm_backward_workspace_size(N, C, G, r.dtype)
             workspace = torch.empty((max(need, 16),), dtype=torch.uint8, device=r.device)
     _workspace(workspace, r)
-    with torch.cuda.device(r.device):
-        _check(_lib.eqlin_rmsnorm_backward(dy.data_ptr(), r.data_ptr(), _ptr(weight), _ptr(dsum), dx.data_ptr(),
-                                           _ptr(dweight), N, C, G, eps, _w_code(weight), _TORCH_TO_EQLIN[r.dtype],
-                                           _ptr(workspace), 0 if workspace is None else workspace.numel(),
-                                           _stream_ptr(stream)), "eqlin_rmsnorm_backward")
+    _run("eqlin_rmsnorm_backward", r.device, stream, dy.data_ptr(), r.data_ptr(), _ptr(weight), _ptr(dsum), dx.data_ptr(),
+         _ptr(dweight), N, C, G, eps, _w_code(weight), _TORCH_TO_EQLIN[r.dtype], _ptr(workspace),
+         0 if workspace is None else workspace.numel())
     return dx, dweight
 
 
@@ -210,10 +219,8 @@ def eqlin_rope(x: torch.Tensor, positions: torch.Tensor, heads: int, sections, b
         raise ValueError("out has the wrong shape, dtype or device")
     xs, ys = _rows(x, "x"), _rows(out, "out")
     table = (ctypes.c_int32 * max(len(sections), 1))(*sections)
-    with torch.cuda.device(x.device):
-        _check(_lib.eqlin_rope(x.data_ptr(), positions.data_ptr(), out.data_ptr(), N, heads, C // heads, G, table,
-                               len(sections), base, xs, ys, int(bool(inverse)), _TORCH_TO_EQLIN[x.dtype],
-                               _stream_ptr(stream)), "eqlin_rope")
+    _run("eqlin_rope", x.device, stream, x.data_ptr(), positions.data_ptr(), out.data_ptr(), N, heads, C // heads, G, table,
+         len(sections), base, xs, ys, int(bool(inverse)), _TORCH_TO_EQLIN[x.dtype])
     return out
 
 
@@ -277,12 +284,9 @@ def eqlin_attention_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, h
     elif lse.shape != (heads, q.shape[0]) or lse.dtype != torch.float32 or lse.device != q.device \
             or not lse.is_contiguous():
         raise ValueError(f"lse must be a contiguous [{heads}, {q.shape[0]}] fp32 tensor on {q.device}")
-    with torch.cuda.device(q.device):
-        workspace = _attention_workspace(shape, 0, workspace, q)
-        _check(_lib.eqlin_attention_forward(ctypes.byref(shape), q.data_ptr(), k.data_ptr(), v.data_ptr(),
-                                            o.data_ptr(), lse.data_ptr(), _ptr(workspace),
-                                            0 if workspace is None else workspace.numel(), _stream_ptr(stream)),
-               "eqlin_attention_forward")
+    workspace = _attention_workspace(shape, 0, workspace, q)
+    _run("eqlin_attention_forward", q.device, stream, ctypes.byref(shape), q.data_ptr(), k.data_ptr(), v.data_ptr(),
+         o.data_ptr(), lse.data_ptr(), _ptr(workspace), 0 if workspace is None else workspace.numel())
     return o, lse
 
 
@@ -307,13 +311,10 @@ def eqlin_attention_backward(do: torch.Tensor, q: torch.Tensor, k: torch.Tensor,
             or not lse.is_contiguous():
         raise ValueError(f"lse must be a contiguous [{heads}, {q.shape[0]}] fp32 tensor on {q.device}")
     strides = _GradStrides(_rows(do, "do"), _rows(dq, "dq"), _rows(dk, "dk"), _rows(dv, "dv"))
-    with torch.cuda.device(q.device):
-        workspace = _attention_workspace(shape, 1, workspace, q)
-        _check(_lib.eqlin_attention_backward(ctypes.byref(shape), ctypes.byref(strides), do.data_ptr(), q.data_ptr(),
-                                             k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(), dq.data_ptr(),
-                                             dk.data_ptr(), dv.data_ptr(), _ptr(workspace),
-                                             0 if workspace is None else workspace.numel(), _stream_ptr(stream)),
-               "eqlin_attention_backward")
+    workspace = _attention_workspace(shape, 1, workspace, q)
+    _run("eqlin_attention_backward", q.device, stream, ctypes.byref(shape), ctypes.byref(strides), do.data_ptr(),
+         q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(), dq.data_ptr(), dk.data_ptr(),
+         dv.data_ptr(), _ptr(workspace), 0 if workspace is None else workspace.numel())
     return dq, dk, dv
 
 

@@ -296,8 +296,33 @@ int backward_tc(const attn::tc::BwdParams& bp, int io, cudaStream_t st) {
                    "attention gradient launch", mq, mk, mv, mdo, bp);
     return s;
 }
+template <class T, int DP, int M>
+int backward_short_m(const attn::Params& p, cudaStream_t st) {
+    namespace mma = attn::mma;
+    constexpr int U = 64 / M;
+    unsigned grid_q = 0, grid_k = 0;
+    int s = tc_grid(p.q_rows, p.sequences, M, (p.heads + U - 1) / U, &grid_q);
+    if (s == EQLIN_OK) s = tc_grid(p.k_rows, p.sequences, M, (p.kv_heads + U - 1) / U, &grid_k);
+    if (s == EQLIN_OK && p.q_rows > 0)
+        s = launch(mma::eqlin_attn_dq_short_kernel<T, DP, M>, dim3(grid_q), dim3(mma::kShortThreads),
+                   mma::short_bwd_smem<DP>(), st, "attention gradient launch", p);
+    if (s == EQLIN_OK && p.k_rows > 0)
+        s = launch(mma::eqlin_attn_dkv_short_kernel<T, DP, M>, dim3(grid_k), dim3(mma::kShortThreads),
+                   mma::short_bwd_smem<DP>(), st, "attention gradient launch", p);
+    return s;
+}
+template <class T, int DP>
+int backward_short(const attn::Params& p, cudaStream_t st) {
+    const int64_t rows = std::max(p.q_rows, p.k_rows);
+    if (rows <= int64_t(16) * p.sequences) return backward_short_m<T, DP, 16>(p, st);
+    if (rows <= int64_t(32) * p.sequences) return backward_short_m<T, DP, 32>(p, st);
+    return backward_short_m<T, DP, 64>(p, st);
+}
+
 template <class T>
 int backward_16(attn::Params& p, int io, cudaStream_t st) {
+    if (std::max(p.q_rows, p.k_rows) <= int64_t(64) * p.sequences)
+        return p.D <= 64 ? backward_short<T, 64>(p, st) : backward_short<T, 128>(p, st);
     p.timeout_ns = wait_timeout_ns();
     const attn::tc::BwdParams bp = {p, stop_after()};
     return p.D <= 64 ? backward_tc<T, 64>(bp, io, st) : backward_tc<T, 128>(bp, io, st);

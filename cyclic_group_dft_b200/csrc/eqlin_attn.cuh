@@ -71,10 +71,12 @@ __device__ __forceinline__ Tile find_tile(const int32_t* offsets, int sequences,
         return t;
     }
     auto offset = [&](int b) { return min(max(offsets[b], 0), rows); };
-    auto first_slot = [&](int off, int b) { return static_cast<long long>(off) * mult / M + b; };
+    auto first_slot = [&](int off, int b) {   // mult is 1, or the product with it is small (a few packed rows)
+        return static_cast<long long>(static_cast<unsigned long long>(off) * mult / M) + b;
+    };
     const int lane = threadIdx.x & 31;
-    const long long slots = static_cast<long long>(rows) * mult / M + sequences;
-    const int guess = static_cast<int>(static_cast<long long>(slot) * sequences / slots);
+    const float slots = static_cast<float>(rows) * mult * (1.f / M) + sequences;
+    const int guess = static_cast<int>(__fdividef(static_cast<float>(slot) * sequences, slots));
     const int base = max(0, min(guess - 15, sequences - 31));
     const int probe = base + lane;
     const int off = offset(min(probe, sequences));

@@ -69,16 +69,32 @@ __device__ __forceinline__ float quad_sum(float v) {
     return v + __shfl_xor_sync(0xFFFFFFFFu, v, 2);
 }
 
+// What a lane adds to a tile's address to read 16 x 16 pieces of it with ldmatrix.  Tiles are aligned to
+// their row bytes, rows r and r + 8 have the same chunk order, and the chunks of piece k differ from those of
+// piece 0 in address bits 5 to 7 alone: (base + lane part) ^ (k << 5) is the whole address computation.
+template <int DP>
+struct Lane {
+    uint32_t a;   // rows 0-15 of the lower 16 bytes, then of the upper (operand A; B through a transpose)
+    uint32_t b;   // rows 0-7 lower, rows 0-7 upper, rows 8-15 lower, rows 8-15 upper (operand B)
+    __device__ __forceinline__ explicit Lane(int lane)
+        : a((lane & 15) * (DP * 2) + (((lane >> 4) ^ (lane & 7)) << 4)),
+          b(((lane & 7) + ((lane >> 4) << 3)) * (DP * 2) + ((((lane >> 3) & 1) ^ (lane & 7)) << 4)) {}
+};
+
 // acc[n8 tile] (16 rows of A x NT * 8 rows of B) += A B^T over the features, A and B row tiles.
 template <class T, int DP, int NT>
-__device__ __forceinline__ void rows_by_rows(float (&acc)[NT][4], uint32_t a_tile, uint32_t b_tile, int steps, int lane) {
-    for (int ks = 0; ks < steps; ++ks) {
+__device__ __forceinline__ void rows_by_rows(float (&acc)[NT][4], uint32_t a_tile, uint32_t b_tile, int steps,
+                                             const Lane<DP>& at) {
+    const uint32_t la = a_tile + at.a, lb = b_tile + at.b;
+#pragma unroll
+    for (int ks = 0; ks < DP / 16; ++ks) {
+        if (ks >= steps) break;
         uint32_t a[4];
-        ldm4(a, at<DP>(a_tile, lane & 15, ks * 2 + (lane >> 4)));
+        ldm4(a, la ^ (ks << 5));
 #pragma unroll
         for (int n = 0; n < NT; n += 2) {
             uint32_t b[4];
-            ldm4(b, at<DP>(b_tile, n * 8 + (lane & 7) + ((lane >> 4) << 3), ks * 2 + ((lane >> 3) & 1)));
+            ldm4(b, (lb ^ (ks << 5)) + n * 8 * (DP * 2));
             mma16816<T>(acc[n], a, b[0], b[1]);
             mma16816<T>(acc[n + 1], a, b[2], b[3]);
         }
@@ -86,8 +102,9 @@ __device__ __forceinline__ void rows_by_rows(float (&acc)[NT][4], uint32_t a_til
 }
 // o[feature tile] += P B: P = 16 rows x NT * 8 from accumulators rounded to T, B a row tile.
 template <class T, int DP, int NT>
-__device__ __forceinline__ void weights_by_rows(float (&o)[DP / 8][4], const float (&w)[NT][4], uint32_t b_tile, int D,
-                                                int lane) {
+__device__ __forceinline__ void weights_by_rows(float (&o)[DP / 8][4], const float (&w)[NT][4], uint32_t b_tile, int steps,
+                                                const Lane<DP>& at) {
+    const uint32_t lb = b_tile + at.a;
 #pragma unroll
     for (int kb = 0; kb < NT / 2; ++kb) {
         const uint32_t a[4] = {Io16<T>::pack(w[2 * kb][0], w[2 * kb][1]), Io16<T>::pack(w[2 * kb][2], w[2 * kb][3]),
@@ -95,9 +112,9 @@ __device__ __forceinline__ void weights_by_rows(float (&o)[DP / 8][4], const flo
                                Io16<T>::pack(w[2 * kb + 1][2], w[2 * kb + 1][3])};
 #pragma unroll
         for (int d = 0; d < DP / 16; ++d) {
-            if (d * 16 >= D) break;
+            if (d >= steps) break;
             uint32_t b[4];
-            ldm4t(b, at<DP>(b_tile, kb * 16 + (lane & 15), d * 2 + (lane >> 4)));
+            ldm4t(b, (lb ^ (d << 5)) + kb * 16 * (DP * 2));
             mma16816<T>(o[2 * d], a, b[0], b[1]);
             mma16816<T>(o[2 * d + 1], a, b[2], b[3]);
         }
@@ -105,24 +122,28 @@ __device__ __forceinline__ void weights_by_rows(float (&o)[DP / 8][4], const flo
 }
 
 // Running softmax of 16 rows x NT * 8 keys: masks keys >= last[i] (relative to this tile) of row i of
-// the pair, turns s into weights, moves the maximum and scales o and sum.
+// the pair where `masked`, turns s into weights, and past the `first` tile moves the maximum and scales o
+// and sum.
 template <int NT, int DT>
 __device__ __forceinline__ void softmax_step(float (&s)[NT][4], float (&o)[DT][4], float (&top)[2], float (&sum)[2],
-                                             const int (&last)[2], float c2, int lane) {
+                                             const int (&last)[2], bool masked, bool first, float c2, int lane) {
+    if (masked) {
+        const int col0 = (lane & 3) * 2;
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (col0 + n * 8 + (e & 1) >= last[e >> 1]) s[n][e] = -INFINITY;
+    }
+    float fade[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         float m = -INFINITY;
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int col = n * 8 + (lane & 3) * 2 + e;
-                s[n][2 * i + e] = col < last[i] ? s[n][2 * i + e] : -INFINITY;
-                m = fmaxf(m, s[n][2 * i + e]);
-            }
+        for (int n = 0; n < NT; ++n) m = fmaxf(m, fmaxf(s[n][2 * i], s[n][2 * i + 1]));
         m = fmaxf(top[i], quad_max(m));
         const float ref = m == -INFINITY ? 0.f : m * c2;
-        const float fade = ex2(fmaf(top[i], c2, -ref));        // 0 while top is -infinity
+        fade[i] = ex2(fmaf(top[i], c2, -ref));                 // 0 while top is -infinity
         top[i] = m;
         float part = 0.f;
 #pragma unroll
@@ -132,12 +153,13 @@ __device__ __forceinline__ void softmax_step(float (&s)[NT][4], float (&o)[DT][4
                 s[n][2 * i + e] = ex2(fmaf(s[n][2 * i + e], c2, -ref));
                 part += s[n][2 * i + e];
             }
-        sum[i] = fmaf(sum[i], fade, part);
+        sum[i] = first ? part : fmaf(sum[i], fade[i], part);
+    }
+    if (!first) {
 #pragma unroll
-        for (int d = 0; d < DT; ++d) {
-            o[d][2 * i] *= fade;
-            o[d][2 * i + 1] *= fade;
-        }
+        for (int d = 0; d < DT; ++d)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[d][e] *= fade[e >> 1];
     }
 }
 
@@ -152,22 +174,59 @@ constexpr size_t short_smem() {
     return size_t(3) * 64 * DP * 2;
 }
 
-// Rows [0, M) of a tile (zeros past n and past D) by the threads of one unit.
-template <class T, int DP, int M>
+// Rows [0, M) of a tile (zeros past n and past D) by THREADS threads: a thread keeps its 16-byte column.
+template <class T, int DP, int M, int THREADS>
 __device__ __forceinline__ void copy_tile(uint32_t dst, const void* src, long long stride, long long row0, int n, int D,
-                                          int head, int tid, int threads) {
-    for (int i = tid; i < M * (DP / 8); i += threads) {
-        const int r = i / (DP / 8), c = i % (DP / 8);
-        const bool take = r < n && c * 8 < D;
-        const T* g = static_cast<const T*>(src) + (take ? (row0 + r) * stride + static_cast<long long>(head) * D + c * 8 : 0);
-        cp_async16(at<DP>(dst, r, c), g, take);
+                                          int head, int tid) {
+    constexpr int ROWS = THREADS / (DP / 8);                // rows of one step
+    const int c = tid % (DP / 8), r0 = tid / (DP / 8);
+    const T* g = static_cast<const T*>(src) + (row0 + r0) * stride + static_cast<long long>(head) * D + c * 8;
+    const long long step = ROWS * stride;
+    const int left = c * 8 < D ? n - r0 : 0;                // rows k * ROWS below this are copied
+    const uint32_t d0 = at<DP>(dst, r0, c);
+#pragma unroll
+    for (int k = 0; k < M / ROWS; ++k) {
+        const bool take = k * ROWS < left;
+        const uint32_t d = ROWS % 8 == 0 ? d0 + k * ROWS * (DP * 2) : at<DP>(dst, r0 + k * ROWS, c);
+        cp_async16(d, take ? g : static_cast<const T*>(src), take);
+        g += step;
+    }
+}
+
+// Output rows of a warp through its 16 rows of a tile in shared memory, then as whole 16-byte chunks: the
+// accumulators times mul[i] (row lane / 4 + 8 i), rows below n.
+template <class T, int DP>
+__device__ __forceinline__ void store_rows(const float (&acc)[DP / 8][4], const float (&mul)[2], uint32_t tile, int warp_row,
+                                           int n, int D, T* out, long long stride, int lane) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const uint32_t base = at<DP>(tile, warp_row + (lane >> 2) + 8 * i, 0) + (lane & 3) * 4;
+#pragma unroll
+        for (int d = 0; d < DP / 8; ++d) {
+            const uint32_t w = Io16<T>::pack(acc[d][2 * i] * mul[i], acc[d][2 * i + 1] * mul[i]);
+            asm volatile("st.shared.b32 [%0], %1;" ::"r"(base ^ (d << 4)), "r"(w) : "memory");
+        }
+    }
+    __syncwarp();
+    constexpr int ROWS = 32 / (DP / 8);                     // rows of one step
+    const int c = lane % (DP / 8);
+#pragma unroll
+    for (int k = 0; k < 16 / ROWS; ++k) {
+        const int r = warp_row + lane / (DP / 8) + k * ROWS;
+        if (r >= n || c * 8 >= D) continue;
+        uint4 v;
+        asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                     : "r"(at<DP>(tile, r, c))
+                     : "memory");
+        *reinterpret_cast<uint4*>(out + r * stride + c * 8) = v;
     }
 }
 
 template <class T, int DP, int M>
-__global__ void __launch_bounds__(kShortThreads) eqlin_attn_fwd_short_kernel(const Params p) {
+__global__ void __launch_bounds__(kShortThreads, DP == 128 ? 4 : 5) eqlin_attn_fwd_short_kernel(const Params p) {
     constexpr int U = 64 / M, WU = 4 / U, NT = M / 8;      // heads of a block, warps of a head
-    extern __shared__ __align__(128) uint8_t smem[];
+    extern __shared__ __align__(1024) uint8_t smem[];
     ptx::grid_launch_dependents();
     ptx::grid_dependency_wait();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -182,7 +241,8 @@ __global__ void __launch_bounds__(kShortThreads) eqlin_attn_fwd_short_kernel(con
     const bool on = h < p.heads;                            // the last block may have fewer heads
     const int hk = h / (p.heads / p.kv_heads);
     const uint32_t sq = ptx::smem_u32(smem) + unit * (3 * M * DP * 2), sk = sq + M * DP * 2, sv = sk + M * DP * 2;
-    const int tid = threadIdx.x - unit * WU * 32, nth = WU * 32;
+    const int tid = threadIdx.x - unit * WU * 32;
+    const Lane<DP> la(lane);
     const int steps = (p.D + 15) / 16;
     const float c2 = p.scale * kLog2e;
     float o[DP / 8][4];
@@ -190,15 +250,15 @@ __global__ void __launch_bounds__(kShortThreads) eqlin_attn_fwd_short_kernel(con
     for (int d = 0; d < DP / 8; ++d) o[d][0] = o[d][1] = o[d][2] = o[d][3] = 0.f;
     float top[2] = {-INFINITY, -INFINITY}, sum[2] = {0.f, 0.f};
     const int row = rw * 16 + (lane >> 2);                  // of the tile; and row + 8
-    if (on) copy_tile<T, DP, M>(sq, p.q, p.q_stride, static_cast<long long>(t.own.start) + r0, n, p.D, h, tid, nth);
+    if (on) copy_tile<T, DP, M, WU * 32>(sq, p.q, p.q_stride, static_cast<long long>(t.own.start) + r0, n, p.D, h, tid);
     cp_async_commit();
     for (int k0 = 0; k0 < seen; k0 += M) {
         const int kn = min(M, kr.len - k0);
         if (k0 > 0) __syncthreads();
         if (on) {
-            copy_tile<T, DP, M>(sk, p.k, p.k_stride, static_cast<long long>(kr.start) + k0, kn, p.D, hk, tid, nth);
+            copy_tile<T, DP, M, WU * 32>(sk, p.k, p.k_stride, static_cast<long long>(kr.start) + k0, kn, p.D, hk, tid);
             cp_async_commit();
-            copy_tile<T, DP, M>(sv, p.v, p.v_stride, static_cast<long long>(kr.start) + k0, kn, p.D, hk, tid, nth);
+            copy_tile<T, DP, M, WU * 32>(sv, p.v, p.v_stride, static_cast<long long>(kr.start) + k0, kn, p.D, hk, tid);
             cp_async_commit();
         }
         cp_async_wait<1>();
@@ -208,64 +268,250 @@ __global__ void __launch_bounds__(kShortThreads) eqlin_attn_fwd_short_kernel(con
         for (int i = 0; i < NT; ++i) s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.f;
         const bool work = on && rw * 16 < n;
         if (work) {
-            rows_by_rows<T, DP, NT>(s, sq + rw * 16 * (DP * 2), sk, steps, lane);
+            rows_by_rows<T, DP, NT>(s, sq + rw * 16 * (DP * 2), sk, steps, la);
             int last[2];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const int lim = p.causal ? r0 + row + 8 * i + 1 + kr.len - t.own.len - k0 : kn;
                 last[i] = min(lim, kn);
             }
-            softmax_step<NT, DP / 8>(s, o, top, sum, last, c2, lane);
+            softmax_step<NT, DP / 8>(s, o, top, sum, last, p.causal || kn < M, k0 == 0, c2, lane);
         }
         cp_async_wait<0>();
         __syncthreads();
-        if (work) weights_by_rows<T, DP, NT>(o, s, sv, p.D, lane);
+        if (work) weights_by_rows<T, DP, NT>(o, s, sv, steps, la);
     }
     cp_async_wait<0>();
     __syncthreads();
     if (!on) return;
-    // outputs through shared memory (this warp's rows of Q), then as whole 16-byte chunks
+    float inv[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const float l = quad_sum(sum[i]);
-        const float inv = l == 0.f ? 0.f : 1.f / l;         // a row that sees no key
-        const int r = row + 8 * i;
-        if (p.lse && (lane & 3) == 0 && r < n)
-            p.lse[static_cast<long long>(h) * p.q_rows + t.own.start + r0 + r] =
+        inv[i] = l == 0.f ? 0.f : 1.f / l;                  // a row that sees no key
+        if (p.lse && (lane & 3) == 0 && row + 8 * i < n)
+            p.lse[static_cast<long long>(h) * p.q_rows + t.own.start + r0 + row + 8 * i] =
                 l == 0.f ? -INFINITY : fmaf(top[i], p.scale, logf(l));
+    }
+    store_rows<T, DP>(o, inv, sq, rw * 16, n, p.D,
+                      static_cast<T*>(p.out) + (static_cast<long long>(t.own.start) + r0) * p.o_stride +
+                          static_cast<long long>(h) * p.D, p.o_stride, lane);
+}
+
+// Gradients of short sequences: the forward's tiles, with four of them (Q, dO, K, V) in shared memory.
+template <int DP>
+constexpr size_t short_bwd_smem() {
+    return size_t(4) * 64 * DP * 2 + 2 * 64 * sizeof(float);
+}
+
+// dq, and delta = do . o of its rows, which the kernel for dk and dv (launched next) reads.
+template <class T, int DP, int M>
+__global__ void __launch_bounds__(kShortThreads, DP == 128 ? 3 : 4) eqlin_attn_dq_short_kernel(const Params p) {
+    constexpr int U = 64 / M, WU = 4 / U, NT = M / 8;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    ptx::grid_launch_dependents();
+    ptx::grid_dependency_wait();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int n_hb = (p.heads + U - 1) / U;
+    const int unit = warp / WU, rw = warp % WU;
+    const int h = (blockIdx.x % n_hb) * U + unit;
+    const Tile t = find_tile<M>(p.q_offsets, p.sequences, p.q_rows, blockIdx.x / n_hb);
+    if (t.tile < 0) return;
+    const Rows kr = p.k_offsets == p.q_offsets && p.k_rows == p.q_rows ? t.own : sequence_rows(p.k_offsets, t.b, p.k_rows);
+    const int r0 = t.tile * M, n = min(M, t.own.len - r0);
+    const int seen = keys_seen(r0 + n - 1, t.own.len, kr.len, p.causal);
+    const bool on = h < p.heads;
+    const int hk = h / (p.heads / p.kv_heads);
+    const uint32_t sq = ptx::smem_u32(smem) + unit * (4 * M * DP * 2), sdo = sq + M * DP * 2, sk = sdo + M * DP * 2,
+                   sv = sk + M * DP * 2;
+    const int tid = threadIdx.x - unit * WU * 32;
+    const Lane<DP> la(lane);
+    const int steps = (p.D + 15) / 16;
+    const float c2 = p.scale * kLog2e;
+    const int row = rw * 16 + (lane >> 2);
+    const long long first_row = static_cast<long long>(t.own.start) + r0;
+    float dq[DP / 8][4];
 #pragma unroll
-        for (int d = 0; d < DP / 8; ++d) {
-            const uint32_t w = Io16<T>::pack(o[d][2 * i] * inv, o[d][2 * i + 1] * inv);
-            asm volatile("st.shared.b32 [%0], %1;" ::"r"(at<DP>(sq, r, d) + (lane & 3) * 4), "r"(w) : "memory");
+    for (int d = 0; d < DP / 8; ++d) dq[d][0] = dq[d][1] = dq[d][2] = dq[d][3] = 0.f;
+    float off[2] = {0.f, 0.f}, delta[2];
+    if (on) {
+        copy_tile<T, DP, M, WU * 32>(sq, p.q, p.q_stride, first_row, n, p.D, h, tid);
+        copy_tile<T, DP, M, WU * 32>(sdo, p.dout, p.do_stride, first_row, n, p.D, h, tid);
+        // delta: two lanes a row, each half of its features
+        const int r = rw * 16 + (lane >> 1);
+        float sum = 0.f;
+        if (r < n) {
+            const T* po = static_cast<const T*>(p.o) + (first_row + r) * p.o_stride + static_cast<long long>(h) * p.D;
+            const T* pd = static_cast<const T*>(p.dout) + (first_row + r) * p.do_stride + static_cast<long long>(h) * p.D;
+#pragma unroll
+            for (int c = 0; c < DP / 16; ++c) {
+                const int at8 = (2 * c + (lane & 1)) * 8;
+                if (at8 >= p.D) break;
+                float a[8], b[8];
+                Vec<T, 8>::unpack(Vec<T, 8>::load(po + at8), a);
+                Vec<T, 8>::unpack(Vec<T, 8>::load(pd + at8), b);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) sum = fmaf(a[e], b[e], sum);
+            }
+        }
+        sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 1);
+        const long long stat = static_cast<long long>(h) * p.q_rows + first_row;
+        if (r < n && !(lane & 1)) p.delta[stat + r] = sum;
+        delta[0] = __shfl_sync(0xFFFFFFFFu, sum, (lane >> 2) * 2);
+        delta[1] = __shfl_sync(0xFFFFFFFFu, sum, (lane >> 2) * 2 + 16);
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            if (row + 8 * i < n) {
+                const float l = p.lse[stat + row + 8 * i];
+                off[i] = l == -INFINITY ? 0.f : -l * kLog2e;    // a row that sees no key: all of it is masked
+            }
+    }
+    for (int k0 = 0; k0 < seen; k0 += M) {
+        const int kn = min(M, kr.len - k0);
+        if (k0 > 0) __syncthreads();
+        if (on) {
+            copy_tile<T, DP, M, WU * 32>(sk, p.k, p.k_stride, static_cast<long long>(kr.start) + k0, kn, p.D, hk, tid);
+            copy_tile<T, DP, M, WU * 32>(sv, p.v, p.v_stride, static_cast<long long>(kr.start) + k0, kn, p.D, hk, tid);
+        }
+        cp_async_commit();
+        cp_async_wait<0>();
+        __syncthreads();
+        if (!on || rw * 16 >= n) continue;
+        float s[NT][4], dp[NT][4];
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[i][e] = dp[i][e] = 0.f;
+        rows_by_rows<T, DP, NT>(s, sq + rw * 16 * (DP * 2), sk, steps, la);
+        rows_by_rows<T, DP, NT>(dp, sdo + rw * 16 * (DP * 2), sv, steps, la);
+        int last[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) last[i] = min(kn, p.causal ? r0 + row + 8 * i + 1 + kr.len - t.own.len - k0 : kn);
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const bool vis = i * 8 + (lane & 3) * 2 + (e & 1) < last[e >> 1];
+                s[i][e] = vis ? ex2(fmaf(s[i][e], c2, off[e >> 1])) * (dp[i][e] - delta[e >> 1]) : 0.f;
+            }
+        weights_by_rows<T, DP, NT>(dq, s, sk, steps, la);
+    }
+    cp_async_commit();
+    cp_async_wait<0>();
+    __syncthreads();
+    if (!on) return;
+    const float mul[2] = {p.scale, p.scale};
+    store_rows<T, DP>(dq, mul, sq, rw * 16, n, p.D,
+                      static_cast<T*>(p.dq) + first_row * p.dq_stride + static_cast<long long>(h) * p.D, p.dq_stride, lane);
+}
+
+// dk and dv: a warp owns 16 keys; the query rows that see the tile pass by, for each head of the group.
+template <class T, int DP, int M>
+__global__ void __launch_bounds__(kShortThreads, DP == 128 ? 2 : 4) eqlin_attn_dkv_short_kernel(const Params p) {
+    constexpr int U = 64 / M, WU = 4 / U, NT = (M < 32 ? M : 32) / 8;   // queries in steps of 32 (or M) columns
+    extern __shared__ __align__(1024) uint8_t smem[];
+    ptx::grid_launch_dependents();
+    ptx::grid_dependency_wait();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int n_hb = (p.kv_heads + U - 1) / U, group = p.heads / p.kv_heads;
+    const int unit = warp / WU, rw = warp % WU;
+    const int hk = (blockIdx.x % n_hb) * U + unit;
+    const Tile t = find_tile<M>(p.k_offsets, p.sequences, p.k_rows, blockIdx.x / n_hb);
+    if (t.tile < 0) return;
+    const Rows qr = p.k_offsets == p.q_offsets && p.k_rows == p.q_rows ? t.own : sequence_rows(p.q_offsets, t.b, p.q_rows);
+    const int r0 = t.tile * M, n = min(M, t.own.len - r0);
+    const bool on = hk < p.kv_heads;
+    const uint32_t sk = ptx::smem_u32(smem) + unit * (4 * M * DP * 2), sv = sk + M * DP * 2, sq = sv + M * DP * 2,
+                   sdo = sq + M * DP * 2;
+    float* slse = reinterpret_cast<float*>(smem + 4 * 64 * DP * 2) + unit * 2 * M;   // lse, then delta, of the tile's rows
+    float* sdelta = slse + M;
+    const int tid = threadIdx.x - unit * WU * 32;
+    const Lane<DP> la(lane);
+    const int steps = (p.D + 15) / 16;
+    const float c2 = p.scale * kLog2e;
+    const int key = r0 + rw * 16 + (lane >> 2);
+    const long long first_row = static_cast<long long>(t.own.start) + r0;
+    float dk[DP / 8][4], dv[DP / 8][4];
+#pragma unroll
+    for (int d = 0; d < DP / 8; ++d)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) dk[d][e] = dv[d][e] = 0.f;
+    if (on) {
+        copy_tile<T, DP, M, WU * 32>(sk, p.k, p.k_stride, first_row, n, p.D, hk, tid);
+        copy_tile<T, DP, M, WU * 32>(sv, p.v, p.v_stride, first_row, n, p.D, hk, tid);
+    }
+    const int begin = first_query(r0, qr.len, t.own.len, p.causal) / M * M;
+    for (int g = 0; g < group; ++g) {
+        const int h = hk * group + g;
+        for (int q0 = begin; q0 < qr.len; q0 += M) {
+            const int qn = min(M, qr.len - q0);
+            if (g > 0 || q0 > begin) __syncthreads();
+            if (on) {
+                copy_tile<T, DP, M, WU * 32>(sq, p.q, p.q_stride, static_cast<long long>(qr.start) + q0, qn, p.D, h, tid);
+                copy_tile<T, DP, M, WU * 32>(sdo, p.dout, p.do_stride, static_cast<long long>(qr.start) + q0, qn, p.D, h, tid);
+                for (int i = tid; i < M; i += WU * 32) {
+                    const long long stat = static_cast<long long>(h) * p.q_rows + qr.start + q0 + i;
+                    const float l = i < qn ? p.lse[stat] : -INFINITY;
+                    slse[i] = l == -INFINITY ? INFINITY : l * kLog2e;      // weights of zero
+                    sdelta[i] = i < qn ? p.delta[stat] : 0.f;
+                }
+            }
+            cp_async_commit();
+            cp_async_wait<0>();
+            __syncthreads();
+            if (!on || rw * 16 >= n) continue;
+#pragma unroll 1
+            for (int c0 = 0; c0 < qn; c0 += NT * 8) {
+                float s[NT][4], dp[NT][4];
+#pragma unroll
+                for (int i = 0; i < NT; ++i)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) s[i][e] = dp[i][e] = 0.f;
+                rows_by_rows<T, DP, NT>(s, sk + rw * 16 * (DP * 2), sq + c0 * (DP * 2), steps, la);
+                rows_by_rows<T, DP, NT>(dp, sv + rw * 16 * (DP * 2), sdo + c0 * (DP * 2), steps, la);
+#pragma unroll
+                for (int i = 0; i < NT; ++i) {
+                    const int c = c0 + i * 8 + (lane & 3) * 2;
+                    const float2 l = *reinterpret_cast<const float2*>(slse + c), dl = *reinterpret_cast<const float2*>(sdelta + c);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        float w = ex2(fmaf(s[i][e], c2, e & 1 ? -l.y : -l.x));
+                        // key j is seen by queries from j - (keys - queries) on
+                        if (p.causal && q0 + c + (e & 1) < key + 8 * (e >> 1) - (t.own.len - qr.len)) w = 0.f;
+                        s[i][e] = w;
+                        dp[i][e] = w == 0.f ? 0.f : w * (dp[i][e] - (e & 1 ? dl.y : dl.x));
+                    }
+                }
+                weights_by_rows<T, DP, NT>(dv, s, sdo + c0 * (DP * 2), steps, la);
+                weights_by_rows<T, DP, NT>(dk, dp, sq + c0 * (DP * 2), steps, la);
+            }
         }
     }
-    __syncwarp();
-    const int chunks = p.D / 8;
-    for (int i = lane; i < 16 * (DP / 8); i += 32) {
-        const int r = rw * 16 + i / (DP / 8), c = i % (DP / 8);
-        if (r >= n || c >= chunks) continue;
-        uint4 v;
-        asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
-                     : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                     : "r"(at<DP>(sq, r, c))
-                     : "memory");
-        *reinterpret_cast<uint4*>(static_cast<T*>(p.out) + (static_cast<long long>(t.own.start) + r0 + r) * p.o_stride +
-                                  static_cast<long long>(h) * p.D + c * 8) = v;
-    }
+    cp_async_commit();
+    cp_async_wait<0>();
+    __syncthreads();
+    if (!on) return;
+    const float mul[2] = {p.scale, p.scale}, one[2] = {1.f, 1.f};
+    const long long col = static_cast<long long>(hk) * p.D;
+    store_rows<T, DP>(dk, mul, sk, rw * 16, n, p.D, static_cast<T*>(p.dk) + first_row * p.dk_stride + col, p.dk_stride, lane);
+    store_rows<T, DP>(dv, one, sv, rw * 16, n, p.D, static_cast<T*>(p.dv) + first_row * p.dv_stride + col, p.dv_stride, lane);
 }
 
 // ------------------------------------------------------------------- few queries over many keys
 //
 // The rows of a tile are the queries of one sequence for all query heads of one key head, query-major:
 // packed row i * group + g.  A block takes 16 of them and one of `splits` slices of the keys; its warps
-// take turns at blocks of 16 keys, each with its own ring of copies, and no barrier until their sums are
+// take turns at blocks of KEYS keys, each with its own ring of copies, and no barrier until their sums are
 // joined in shared memory.  With several slices the block writes o and lse in fp32 to the workspace
 // ([split][head][row]) and eqlin_attn_join_kernel joins them.
+//
+// Bound by memory: each key and value is read once.  Per SM about 128 KB of copies are in flight.
 template <int DP>
 struct Few {
     static constexpr int WARPS = 8;
-    static constexpr int STAGES = DP == 64 ? 4 : 3;
-    static constexpr int STAGE_BYTES = 2 * 16 * DP * 2;     // 16 keys of K, 16 of V
+    static constexpr int KEYS = DP == 64 ? 32 : 16;
+    static constexpr int STAGES = 3;
+    static constexpr int STAGE_BYTES = 2 * KEYS * DP * 2;   // K, then V
     static constexpr int Q_BYTES = 16 * DP * 2;
     static constexpr size_t RING = size_t(WARPS) * STAGES * STAGE_BYTES;
     static constexpr size_t JOIN = size_t(WARPS) * 16 * (DP + 4) * 4 + WARPS * 16 * 8;
@@ -277,7 +523,7 @@ __global__ void __launch_bounds__(Few<DP>::WARPS * 32)
     eqlin_attn_fwd_few_kernel(const Params p) {
     using F = Few<DP>;
     const int splits = p.splits;
-    extern __shared__ __align__(128) uint8_t smem[];
+    extern __shared__ __align__(1024) uint8_t smem[];
     ptx::grid_launch_dependents();
     ptx::grid_dependency_wait();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -290,12 +536,13 @@ __global__ void __launch_bounds__(Few<DP>::WARPS * 32)
     const int r0 = t.tile * 16;                             // packed row
     const int n = min(16, t.own.len * group - r0);
     const int seen = keys_seen((r0 + n - 1) / group, t.own.len, kr.len, p.causal);
-    // this slice's keys: blocks of 16, as evenly as possible
-    const int blocks = (seen + 15) / 16;
+    // this slice's keys: whole blocks, as evenly as possible
+    const int blocks = (seen + F::KEYS - 1) / F::KEYS;
     const int first = static_cast<int>(static_cast<long long>(blocks) * split / splits);
     const int end = static_cast<int>(static_cast<long long>(blocks) * (split + 1) / splits);
     const uint32_t sq = ptx::smem_u32(smem), ring = sq + F::Q_BYTES + warp * (F::STAGES * F::STAGE_BYTES);
     const int chunks = p.D / 8, steps = (p.D + 15) / 16;
+    const Lane<DP> la(lane);
     for (int i = threadIdx.x; i < 16 * (DP / 8); i += F::WARPS * 32) {
         const int r = i / (DP / 8), c = i % (DP / 8);
         const int q = (r0 + r) / group, h = hk * group + (r0 + r) - q * group;
@@ -309,10 +556,10 @@ __global__ void __launch_bounds__(Few<DP>::WARPS * 32)
         const int b = first + warp + u * F::WARPS;
         if (b < end) {
             const uint32_t dst = ring + (u % F::STAGES) * F::STAGE_BYTES;
-            const int kn = kr.len - b * 16;
-            copy_tile<T, DP, 16>(dst, p.k, p.k_stride, static_cast<long long>(kr.start) + b * 16, kn, p.D, hk, lane, 32);
-            copy_tile<T, DP, 16>(dst + 16 * DP * 2, p.v, p.v_stride, static_cast<long long>(kr.start) + b * 16, kn, p.D, hk,
-                                 lane, 32);
+            const int kn = kr.len - b * F::KEYS;
+            const long long row0 = static_cast<long long>(kr.start) + static_cast<long long>(b) * F::KEYS;
+            copy_tile<T, DP, F::KEYS, 32>(dst, p.k, p.k_stride, row0, kn, p.D, hk, lane);
+            copy_tile<T, DP, F::KEYS, 32>(dst + F::STAGE_BYTES / 2, p.v, p.v_stride, row0, kn, p.D, hk, lane);
         }
         cp_async_commit();
     };
@@ -332,13 +579,13 @@ __global__ void __launch_bounds__(Few<DP>::WARPS * 32)
     for (int u = 0; first + warp + u * F::WARPS < end; ++u) {
         cp_async_wait<F::STAGES - 2>();
         __syncwarp();
-        const int k0 = (first + warp + u * F::WARPS) * 16;
+        const int k0 = (first + warp + u * F::WARPS) * F::KEYS;
         const uint32_t kt = ring + (u % F::STAGES) * F::STAGE_BYTES;
-        float s[2][4] = {};
-        rows_by_rows<T, DP, 2>(s, sq, kt, steps, lane);
+        float s[F::KEYS / 8][4] = {};
+        rows_by_rows<T, DP, F::KEYS / 8>(s, sq, kt, steps, la);
         const int last[2] = {min(lim[0], kr.len) - k0, min(lim[1], kr.len) - k0};
-        softmax_step<2, DP / 8>(s, o, top, sum, last, c2, lane);
-        weights_by_rows<T, DP, 2>(o, s, kt + 16 * DP * 2, p.D, lane);
+        softmax_step<F::KEYS / 8, DP / 8>(s, o, top, sum, last, min(last[0], last[1]) < F::KEYS, u == 0, c2, lane);
+        weights_by_rows<T, DP, F::KEYS / 8>(o, s, kt + F::STAGE_BYTES / 2, steps, la);
         __syncwarp();
         fetch(u + F::STAGES - 1);
     }
