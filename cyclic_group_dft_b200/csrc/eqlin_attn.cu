@@ -162,8 +162,8 @@ Fwd forward_kind(const eqlin_attention_shape& a) {
 
 constexpr int kB200Sms = 148;   // the plan does not depend on the device, so that sizes need none
 
-// Slices of the keys, where the tiles alone would leave SMs idle: as many as fill them once (fp32: three
-// blocks fit an SM), but no slice below 256 keys.
+// Slices of the keys, where the tiles alone would leave SMs idle: as many as fill them once (fp32: two blocks
+// fit an SM; tiles of 16 rows), but no slice below 256 keys.
 int forward_splits(const eqlin_attention_shape& a) {
     const Fwd kind = forward_kind(a);
     const int64_t keys = a.k_rows / a.sequences;
@@ -173,8 +173,8 @@ int forward_splits(const eqlin_attention_shape& a) {
         units = std::max(a.sequences, (rows + 15) / 16) * a.kv_heads;
         room = kB200Sms;
     } else if (a.io_dtype == EQLIN_F32) {
-        units = std::max(a.sequences, (a.q_rows + 63) / 64) * a.heads;
-        room = 3 * kB200Sms;
+        units = std::max(a.sequences, (a.q_rows + 15) / 16) * a.heads;
+        room = 2 * kB200Sms;
     } else {
         return 1;
     }
@@ -231,16 +231,24 @@ int forward_16(attn::Params& p, Fwd kind, int io, cudaStream_t st) {
     return p.D <= 64 ? forward_tc<T, 64, 1>(fp, io, st) : forward_tc<T, 128, 2>(fp, io, st);
 }
 
-template <class T, int DP>
-int forward_f32(const attn::Params& p, cudaStream_t st) {
-    using namespace attn::f32;
-    const int s = launch(eqlin_attn_fwd_f32_kernel<T, DP>, dim3(slots(p.q_rows, p.sequences, kM), p.heads, p.splits),
-                         dim3(kThreads), Shape<DP>::FWD_BYTES, st, "attention launch", p);
-    return s == EQLIN_OK && p.splits > 1 ? launch_join<T>(p, st) : s;
+// ------------------------------------------------------------------------------------ fp32 I/O
+// Rows per thread of the fp32 kernels: 1 (tiles of 16 rows) where tiles of 64 would not give every SM a block.
+bool f32_small(int64_t rows, int64_t sequences, int64_t heads) {
+    return std::max(sequences, (rows + 63) / 64) * heads < kB200Sms;
 }
-template <class T>
-int forward_t(const attn::Params& p, cudaStream_t st) {
-    return p.D <= 64 ? forward_f32<T, 64>(p, st) : forward_f32<T, 128>(p, st);
+
+template <int DP, int R>
+int forward_f32_r(const attn::Params& p, cudaStream_t st) {
+    using namespace attn::f32;
+    using S = Shape<DP, R>;
+    const int s = launch(eqlin_attn_fwd_f32_kernel<DP, R>, dim3(slots(p.q_rows, p.sequences, S::M), p.heads, p.splits),
+                         dim3(kThreads), S::FWD_BYTES, st, "attention launch", p);
+    return s == EQLIN_OK && p.splits > 1 ? launch_join<float>(p, st) : s;
+}
+int forward_f32(const attn::Params& p, cudaStream_t st) {
+    const bool small = f32_small(p.q_rows, p.sequences, p.heads);
+    if (p.D <= 64) return small ? forward_f32_r<64, 1>(p, st) : forward_f32_r<64, 4>(p, st);
+    return small ? forward_f32_r<128, 1>(p, st) : forward_f32_r<128, 4>(p, st);
 }
 
 template <class T>
@@ -254,19 +262,34 @@ int launch_delta(const attn::Params& p, cudaStream_t st) {
                   "attention gradient launch", p, lanes);
 }
 
-template <class T, int DP>
-int backward_f32(const attn::Params& p, cudaStream_t st) {
+template <int DP, int R>
+int dkv_f32(const attn::Params& p, cudaStream_t st) {
     using namespace attn::f32;
+    using S = Shape<DP, R>;
+    return launch(eqlin_attn_dkv_f32_kernel<DP, R>, dim3(slots(p.k_rows, p.sequences, S::M), p.kv_heads), dim3(kThreads),
+                  S::DKV_BYTES, st, "attention gradient launch", p);
+}
+template <int DP, int R>
+int dq_f32(const attn::Params& p, cudaStream_t st) {
+    using namespace attn::f32;
+    using S = Shape<DP, R>;
+    return launch(eqlin_attn_dq_f32_kernel<DP, R>, dim3(slots(p.q_rows, p.sequences, S::M), p.heads), dim3(kThreads),
+                  S::DQ_BYTES, st, "attention gradient launch", p);
+}
+template <int DP>
+int backward_f32_d(const attn::Params& p, cudaStream_t st) {
     int s = EQLIN_OK;
-    if (p.q_rows > 0) s = launch_delta<T>(p, st);
+    if (p.q_rows > 0) s = launch_delta<float>(p, st);
     if (s == EQLIN_OK && p.k_rows > 0)
-        s = launch(eqlin_attn_dkv_f32_kernel<T, DP>, dim3(slots(p.k_rows, p.sequences, kM), p.kv_heads),
-                   dim3(kThreads), Shape<DP>::DKV_BYTES, st, "attention gradient launch", p);
+        s = f32_small(p.k_rows, p.sequences, p.kv_heads) ? dkv_f32<DP, 1>(p, st) : dkv_f32<DP, 4>(p, st);
     if (s == EQLIN_OK && p.q_rows > 0)
-        s = launch(eqlin_attn_dq_f32_kernel<T, DP>, dim3(slots(p.q_rows, p.sequences, kM), p.heads), dim3(kThreads),
-                   Shape<DP>::DQ_BYTES, st, "attention gradient launch", p);
+        s = f32_small(p.q_rows, p.sequences, p.heads) ? dq_f32<DP, 1>(p, st) : dq_f32<DP, 4>(p, st);
     return s;
 }
+int backward_f32(const attn::Params& p, cudaStream_t st) {
+    return p.D <= 64 ? backward_f32_d<64>(p, st) : backward_f32_d<128>(p, st);
+}
+
 template <class T, int DP>
 int backward_tc(const attn::tc::BwdParams& bp, int io, cudaStream_t st) {
     namespace tc = attn::tc;
@@ -328,11 +351,6 @@ int backward_16(attn::Params& p, int io, cudaStream_t st) {
     return p.D <= 64 ? backward_tc<T, 64>(bp, io, st) : backward_tc<T, 128>(bp, io, st);
 }
 
-template <class T>
-int backward_t(const attn::Params& p, cudaStream_t st) {
-    return p.D <= 64 ? backward_f32<T, 64>(p, st) : backward_f32<T, 128>(p, st);
-}
-
 }  // namespace
 
 extern "C" {
@@ -376,7 +394,7 @@ int eqlin_attention_forward(const eqlin_attention_shape* shape, const void* q, c
     p.part_o = static_cast<float*>(workspace);
     if (p.splits > 1) p.part_lse = p.part_o + size_t(p.splits) * a.heads * a.q_rows * a.head_dim;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (a.io_dtype == EQLIN_F32) return forward_t<float>(p, st);
+    if (a.io_dtype == EQLIN_F32) return forward_f32(p, st);
     const Fwd kind = forward_kind(a);
     return a.io_dtype == EQLIN_F16 ? forward_16<__half>(p, kind, a.io_dtype, st)
                                    : forward_16<__nv_bfloat16>(p, kind, a.io_dtype, st);
@@ -441,7 +459,7 @@ int eqlin_attention_backward(const eqlin_attention_shape* shape, const eqlin_att
     p.dk_stride = strides->dk;
     p.dv_stride = strides->dv;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (io == EQLIN_F32) return backward_t<float>(p, st);
+    if (io == EQLIN_F32) return backward_f32(p, st);
     return io == EQLIN_F16 ? backward_16<__half>(p, io, st) : backward_16<__nv_bfloat16>(p, io, st);
 }
 
