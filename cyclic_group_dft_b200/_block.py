@@ -5,7 +5,6 @@ positions.  Argument marshalling only, as in ``_capi``: torch supplies memory an
 from __future__ import annotations
 
 import ctypes
-import math
 
 import torch
 
@@ -42,14 +41,16 @@ for _f in ("eqlin_attention_device_status", "eqlin_add_rmsnorm", "eqlin_add_rmsn
     getattr(_lib, _f).restype = _int
 
 
-_current_stream = torch._C._cuda_getCurrentRawStream   # of a device number; the public call makes a Stream object
+# the current device, and a device's current stream, as numbers (the tensors show that CUDA is set up)
+_current_device = torch._C._cuda_getDevice
+_current_stream = torch._C._cuda_getCurrentRawStream
 
 
-def _run(name: str, device: torch.device, stream, *args) -> None:
-    """Calls library function `name` with `args` and the stream, with `device` current."""
+def _run(name: str, device: int, stream, *args) -> None:
+    """Calls library function `name` with `args` and the stream, with device number `device` current."""
     f = getattr(_lib, name)
-    if torch.cuda.current_device() == device.index:
-        status = f(*args, _current_stream(device.index) if stream is None else _stream_ptr(stream))
+    if _current_device() == device:
+        status = f(*args, _current_stream(device) if stream is None else _stream_ptr(stream))
     else:
         with torch.cuda.device(device):
             status = f(*args, _stream_ptr(stream))
@@ -57,49 +58,58 @@ def _run(name: str, device: torch.device, stream, *args) -> None:
         _check(status, name)
 
 
-def _features(t: torch.Tensor, name: str) -> None:
-    if t.dim() != 3:
-        raise ValueError(f"{name} must be [N, C, G], got {tuple(t.shape)}")
-    if t.device.type != "cuda":
+# These checks run on every call, whose kernels may take a few microseconds: each asks a tensor for as little as
+# it can (shape and strides once, the device as a number).
+
+def _features(t: torch.Tensor, name: str) -> torch.Size:
+    """The shape of a [N, C, G] CUDA tensor of a supported dtype."""
+    shape = t.shape
+    if len(shape) != 3:
+        raise ValueError(f"{name} must be [N, C, G], got {tuple(shape)}")
+    if t.get_device() < 0:
         raise ValueError(f"{name} must be a CUDA tensor")
     if t.dtype not in _TORCH_TO_EQLIN:
         raise ValueError(f"unsupported dtype {t.dtype}")
+    return shape
 
 
-def _like(t: torch.Tensor, name: str, ref: torch.Tensor, dtype: torch.dtype | None = None) -> None:
-    want = ref.dtype if dtype is None else dtype
-    if t.shape != ref.shape or t.dtype != want or t.device != ref.device or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {tuple(ref.shape)} {want} tensor on {ref.device}")
+def _like(t: torch.Tensor, name: str, shape, dtype: torch.dtype, device: int) -> None:
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {tuple(shape)} {dtype} tensor on cuda:{device}")
 
 
-def _rows(t: torch.Tensor, name: str) -> int:
+def _rows(t: torch.Tensor, name: str, shape, dtype: torch.dtype, device: int) -> int:
     """The features between two rows of a [N, C, G] tensor whose rows are contiguous."""
-    N, C, G = t.shape
-    if (G > 1 and t.stride(2) != 1) or (C > 1 and t.stride(1) != G):
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != device:
+        raise ValueError(f"{name} must be a {tuple(shape)} {dtype} tensor on cuda:{device}")
+    N, C, G = shape
+    row, channel, element = t.stride()
+    if (G > 1 and element != 1) or (C > 1 and channel != G):
         raise ValueError(f"{name} must have contiguous rows (a [N, C, G] tensor or a channel slice of one)")
-    return t.stride(0) if N > 1 else C * G
+    return row if N > 1 else C * G
 
 
 def _ptr(t: torch.Tensor | None):
     return None if t is None else t.data_ptr()
 
 
-def _norm_args(x: torch.Tensor, residual, weight, sum_out) -> None:
-    _features(x, "x")
-    _like(x, "x", x)
+def _norm_args(x: torch.Tensor, residual, weight, sum_out):
+    shape, dtype, device = _features(x, "x"), x.dtype, x.get_device()
+    if not x.is_contiguous():
+        raise ValueError("x must be contiguous")
     if residual is not None:
-        _like(residual, "residual", x)
-    _weight(weight, x)
+        _like(residual, "residual", shape, dtype, device)
+    if weight is not None:
+        _weight(weight, shape[1], device)
     if sum_out is not None:
-        _like(sum_out, "sum_out", x)
+        _like(sum_out, "sum_out", shape, dtype, device)
+    return shape, dtype, device
 
 
-def _weight(weight: torch.Tensor | None, x: torch.Tensor) -> None:
-    if weight is None:
-        return
-    if weight.shape != (x.shape[1],) or weight.device != x.device or not weight.is_contiguous() \
-            or weight.dtype not in _TORCH_TO_EQLIN:
-        raise ValueError(f"weight must be a contiguous [{x.shape[1]}] tensor of a supported dtype on {x.device}")
+def _weight(weight: torch.Tensor, C: int, device: int) -> None:
+    if weight.shape != (C,) or weight.get_device() != device or weight.dtype not in _TORCH_TO_EQLIN \
+            or not weight.is_contiguous():
+        raise ValueError(f"weight must be a contiguous [{C}] tensor of a supported dtype on cuda:{device}")
 
 
 def _w_code(weight: torch.Tensor | None) -> int:
@@ -113,17 +123,18 @@ def eqlin_add_rmsnorm(x: torch.Tensor, residual: torch.Tensor | None = None, wei
     channels and group elements of a token; x, residual, y and r are [N, C, G], weight [C] or
     None (ones).  Without a residual r is x itself, unless sum_out is given.  y and sum_out may
     be x or residual (in place)."""
-    _norm_args(x, residual, weight, sum_out)
-    N, C, G = x.shape
+    shape, dtype, device = _norm_args(x, residual, weight, sum_out)
+    N, C, G = shape
     if y is None:
         y = torch.empty_like(x)
-    _like(y, "y", x)
+    else:
+        _like(y, "y", shape, dtype, device)
     if sum_out is None and residual is not None:
         sum_out = torch.empty_like(x)
     if sum_out is not None and N > 0 and sum_out.data_ptr() == y.data_ptr():
         raise ValueError("y and sum_out must not be the same tensor")
-    _run("eqlin_add_rmsnorm", x.device, stream, x.data_ptr(), _ptr(residual), _ptr(weight), y.data_ptr(), _ptr(sum_out),
-         N, C, G, eps, _w_code(weight), _TORCH_TO_EQLIN[x.dtype])
+    _run("eqlin_add_rmsnorm", device, stream, x.data_ptr(), _ptr(residual), _ptr(weight), y.data_ptr(), _ptr(sum_out),
+         N, C, G, eps, _w_code(weight), _TORCH_TO_EQLIN[dtype])
     return y, (x if sum_out is None else sum_out)
 
 
@@ -133,19 +144,20 @@ def eqlin_add_rmsnorm_fp8(x: torch.Tensor, residual: torch.Tensor | None = None,
                           stream=None) -> tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
     """(y8, scale, r): eqlin_add_rmsnorm with y as float8_e4m3fn and one fp32 scale per token,
     y = y8 * scale[:, None, None], scale = max|y| / 448 (1 for a row of zeros)."""
-    _norm_args(x, residual, weight, sum_out)
-    N, C, G = x.shape
+    shape, dtype, device = _norm_args(x, residual, weight, sum_out)
+    N, C, G = shape
     if y is None:
-        y = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=x.device)
-    _like(y, "y", x, torch.float8_e4m3fn)
+        y = torch.empty(shape, dtype=torch.float8_e4m3fn, device=x.device)
+    else:
+        _like(y, "y", shape, torch.float8_e4m3fn, device)
     if scale is None:
         scale = torch.empty((N,), dtype=torch.float32, device=x.device)
-    elif scale.shape != (N,) or scale.dtype != torch.float32 or scale.device != x.device or not scale.is_contiguous():
-        raise ValueError(f"scale must be a contiguous [{N}] fp32 tensor on {x.device}")
+    else:
+        _like(scale, "scale", (N,), torch.float32, device)
     if sum_out is None and residual is not None:
         sum_out = torch.empty_like(x)
-    _run("eqlin_add_rmsnorm_fp8", x.device, stream, x.data_ptr(), _ptr(residual), _ptr(weight), y.data_ptr(),
-         scale.data_ptr(), _ptr(sum_out), N, C, G, eps, _w_code(weight), _TORCH_TO_EQLIN[x.dtype])
+    _run("eqlin_add_rmsnorm_fp8", device, stream, x.data_ptr(), _ptr(residual), _ptr(weight), y.data_ptr(),
+         scale.data_ptr(), _ptr(sum_out), N, C, G, eps, _w_code(weight), _TORCH_TO_EQLIN[dtype])
     return y, scale, (x if sum_out is None else sum_out)
 
 
@@ -165,36 +177,38 @@ def eqlin_rmsnorm_backward(dy: torch.Tensor, r: torch.Tensor, weight: torch.Tens
     eqlin_add_rmsnorm; dx is the gradient of x and of the residual alike and includes dsum, the
     gradient that reaches r through the residual stream.  The workspace (a uint8 CUDA tensor) is
     allocated by torch when not given."""
-    _features(r, "r")
-    _like(r, "r", r)
-    _like(dy, "dy", r)
-    _weight(weight, r)
+    shape, dtype, device = _features(r, "r"), r.dtype, r.get_device()
+    if not r.is_contiguous():
+        raise ValueError("r must be contiguous")
+    _like(dy, "dy", shape, dtype, device)
+    N, C, G = shape
+    if weight is not None:
+        _weight(weight, C, device)
     if dsum is not None:
-        _like(dsum, "dsum", r)
-    N, C, G = r.shape
+        _like(dsum, "dsum", shape, dtype, device)
     if dx is None:
         dx = torch.empty_like(r)
-    _like(dx, "dx", r)
-    if with_weight and dweight is None:
-        dweight = torch.empty((C,), dtype=torch.float32, device=r.device)
+    else:
+        _like(dx, "dx", shape, dtype, device)
     if dweight is not None:
-        if dweight.shape != (C,) or dweight.dtype != torch.float32 or dweight.device != r.device \
-                or not dweight.is_contiguous():
-            raise ValueError(f"dweight must be a contiguous [{C}] fp32 tensor on {r.device}")
-        if workspace is None:
-            need = eqlin_rmsnorm_backward_workspace_size(N, C, G, r.dtype)
-            workspace = torch.empty((max(need, 16),), dtype=torch.uint8, device=r.device)
-    _workspace(workspace, r)
-    _run("eqlin_rmsnorm_backward", r.device, stream, dy.data_ptr(), r.data_ptr(), _ptr(weight), _ptr(dsum), dx.data_ptr(),
-         _ptr(dweight), N, C, G, eps, _w_code(weight), _TORCH_TO_EQLIN[r.dtype], _ptr(workspace),
-         0 if workspace is None else workspace.numel())
+        _like(dweight, "dweight", (C,), torch.float32, device)
+    elif with_weight:
+        dweight = torch.empty((C,), dtype=torch.float32, device=r.device)
+    if dweight is not None and workspace is None:
+        need = eqlin_rmsnorm_backward_workspace_size(N, C, G, dtype)
+        workspace = torch.empty((max(need, 16),), dtype=torch.uint8, device=r.device)
+    _run("eqlin_rmsnorm_backward", device, stream, dy.data_ptr(), r.data_ptr(), _ptr(weight), _ptr(dsum), dx.data_ptr(),
+         _ptr(dweight), N, C, G, eps, _w_code(weight), _TORCH_TO_EQLIN[dtype], _ptr(workspace), _workspace(workspace, device))
     return dx, dweight
 
 
-def _workspace(workspace: torch.Tensor | None, ref: torch.Tensor) -> None:
-    if workspace is not None and (workspace.dtype != torch.uint8 or workspace.device != ref.device
-                                  or not workspace.is_contiguous()):
-        raise ValueError(f"workspace must be a contiguous uint8 tensor on {ref.device}")
+def _workspace(workspace: torch.Tensor | None, device: int) -> int:
+    """Bytes of a workspace (a contiguous uint8 tensor on the device)."""
+    if workspace is None:
+        return 0
+    if workspace.dtype is not torch.uint8 or workspace.get_device() != device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous uint8 tensor on cuda:{device}")
+    return workspace.numel()
 
 
 def eqlin_rope(x: torch.Tensor, positions: torch.Tensor, heads: int, sections, base: float = 10000.0,
@@ -203,62 +217,61 @@ def eqlin_rope(x: torch.Tensor, positions: torch.Tensor, heads: int, sections, b
     tensor will do): channel pair (c, c + Dh/2) of each head turns by positions[n, axis] *
     base^(-j / sections[axis]).  positions is [N, axes] int32; the sections add up to Dh/2.
     inverse turns back, which is also the gradient.  out may be x (in place)."""
-    _features(x, "x")
-    N, C, G = x.shape
+    shape, dtype, device = _features(x, "x"), x.dtype, x.get_device()
+    N, C, G = shape
     sections = [int(n) for n in sections]
     if heads < 1 or C % heads:
         raise ValueError(f"{C} channels are not {heads} heads")
-    if positions.shape != (N, len(sections)) or positions.dtype != torch.int32 or positions.device != x.device \
-            or not positions.is_contiguous():
-        raise ValueError(f"positions must be a contiguous [{N}, {len(sections)}] int32 tensor on {x.device}")
+    _like(positions, "positions", (N, len(sections)), torch.int32, device)
     if any(n < 0 or n > C for n in sections):
         raise ValueError("the sections must be counts that add up to half the channels of a head")
+    xs = _rows(x, "x", shape, dtype, device)
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    elif out.shape != x.shape or out.dtype != x.dtype or out.device != x.device:
-        raise ValueError("out has the wrong shape, dtype or device")
-    xs, ys = _rows(x, "x"), _rows(out, "out")
+        out, ys = torch.empty(shape, dtype=dtype, device=x.device), C * G
+    else:
+        ys = _rows(out, "out", shape, dtype, device)
     table = (ctypes.c_int32 * max(len(sections), 1))(*sections)
-    _run("eqlin_rope", x.device, stream, x.data_ptr(), positions.data_ptr(), out.data_ptr(), N, heads, C // heads, G, table,
-         len(sections), base, xs, ys, int(bool(inverse)), _TORCH_TO_EQLIN[x.dtype])
+    _run("eqlin_rope", device, stream, x.data_ptr(), positions.data_ptr(), out.data_ptr(), N, heads, C // heads, G, table,
+         len(sections), base, xs, ys, int(bool(inverse)), _TORCH_TO_EQLIN[dtype])
     return out
 
 
-def _attention_shape(q, k, v, o, heads, kv_heads, q_offsets, k_offsets, causal, scale) -> _AttentionShape:
-    for t, name in ((q, "q"), (k, "k"), (v, "v"), (o, "o")):
-        _features(t, name)
-        if t.dtype != q.dtype or t.device != q.device or t.shape[2] != q.shape[2]:
-            raise ValueError("q, k, v and o must share a dtype, a device and G")
+def _attention_shape(q, k, v, heads, kv_heads, q_offsets, k_offsets, causal, scale):
+    """(the C struct but for o's stride, q's shape, k's shape, dtype, device number)"""
+    q_shape, dtype, device = _features(q, "q"), q.dtype, q.get_device()
+    Nq, C, G = q_shape
     kv_heads = heads if kv_heads is None else kv_heads
-    if heads < 1 or kv_heads < 1 or q.shape[1] % heads:
-        raise ValueError(f"{q.shape[1]} channels are not {heads} heads")
-    Dh = q.shape[1] // heads
-    if k.shape[1] != kv_heads * Dh or v.shape != k.shape:
-        raise ValueError(f"k and v must be [Nk, {kv_heads * Dh}, G] (kv_heads heads of {Dh} channels)")
-    if o.shape != q.shape:
-        raise ValueError("o must have q's shape")
-    if (q_offsets is None) != (k_offsets is None):
-        raise ValueError("q_offsets and k_offsets go together")
+    if heads < 1 or kv_heads < 1 or C % heads:
+        raise ValueError(f"{C} channels are not {heads} heads")
+    Dh = C // heads
+    k_shape = k.shape
+    if len(k_shape) != 3 or k_shape[1] != kv_heads * Dh or k_shape[2] != G:
+        raise ValueError(f"k and v must be [Nk, {kv_heads * Dh}, {G}] ({kv_heads} heads of {Dh} channels)")
     n = 1
-    if q_offsets is not None:
-        for t, name in ((q_offsets, "q_offsets"), (k_offsets, "k_offsets")):
-            if t.dim() != 1 or t.dtype != torch.int32 or t.device != q.device or not t.is_contiguous() \
-                    or t.numel() < 2 or t.numel() != q_offsets.numel():
-                raise ValueError(f"{name} must be a contiguous [sequences + 1] int32 tensor on {q.device}")
-        n = q_offsets.numel() - 1
-    D = Dh * q.shape[2]
-    return _AttentionShape(q.shape[0], k.shape[0], n, heads, kv_heads, D, _ptr(q_offsets), _ptr(k_offsets),
-                           _rows(q, "q"), _rows(k, "k"), _rows(v, "v"), _rows(o, "o"), _TORCH_TO_EQLIN[q.dtype],
-                           int(bool(causal)), 1.0 / math.sqrt(D) if scale is None else scale)
+    if q_offsets is not None and k_offsets is not None:
+        n = len(q_offsets) - 1
+        for t, name in ((q_offsets, "q_offsets"),) if k_offsets is q_offsets else ((q_offsets, "q_offsets"),
+                                                                                  (k_offsets, "k_offsets")):
+            if n < 1 or t.shape != (n + 1,) or t.dtype is not torch.int32 or t.get_device() != device \
+                    or not t.is_contiguous():
+                raise ValueError(f"{name} must be a contiguous [sequences + 1] int32 tensor on cuda:{device}")
+    elif q_offsets is not None or k_offsets is not None:
+        raise ValueError("q_offsets and k_offsets go together")
+    D = Dh * G
+    s = _AttentionShape(Nq, k_shape[0], n, heads, kv_heads, D, _ptr(q_offsets), _ptr(k_offsets),
+                        _rows(q, "q", q_shape, dtype, device), _rows(k, "k", k_shape, dtype, device),
+                        _rows(v, "v", k_shape, dtype, device), C * G, _TORCH_TO_EQLIN[dtype], 1 if causal else 0,
+                        D ** -0.5 if scale is None else scale)
+    return s, q_shape, k_shape, dtype, device
 
 
 def _attention_workspace(shape: _AttentionShape, backward: int, workspace, ref: torch.Tensor):
     v = _sz()
-    _check(_lib.eqlin_attention_workspace_size(ctypes.byref(shape), backward, ctypes.byref(v)),
-           "eqlin_attention_workspace_size")
+    status = _lib.eqlin_attention_workspace_size(ctypes.byref(shape), backward, ctypes.byref(v))
+    if status:
+        _check(status, "eqlin_attention_workspace_size")
     if workspace is None and v.value:
         workspace = torch.empty((v.value,), dtype=torch.uint8, device=ref.device)
-    _workspace(workspace, ref)
     return workspace
 
 
@@ -275,18 +288,18 @@ def eqlin_attention_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, h
     k_offsets are [sequences + 1] int32 on the device: sequence b has the rows offsets[b] ..
     offsets[b + 1]; None means one sequence.  causal: the last query of a sequence sees its last
     key.  scale defaults to 1 / sqrt(Dh * G)."""
-    _features(q, "q")
+    shape, q_shape, _, dtype, device = _attention_shape(q, k, v, heads, kv_heads, q_offsets, k_offsets, causal, scale)
     if o is None:
-        o = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    shape = _attention_shape(q, k, v, o, heads, kv_heads, q_offsets, k_offsets, causal, scale)
+        o = torch.empty(q_shape, dtype=dtype, device=q.device)
+    else:
+        shape.o_stride = _rows(o, "o", q_shape, dtype, device)
     if lse is None:
-        lse = torch.empty((heads, q.shape[0]), dtype=torch.float32, device=q.device)
-    elif lse.shape != (heads, q.shape[0]) or lse.dtype != torch.float32 or lse.device != q.device \
-            or not lse.is_contiguous():
-        raise ValueError(f"lse must be a contiguous [{heads}, {q.shape[0]}] fp32 tensor on {q.device}")
+        lse = torch.empty((heads, q_shape[0]), dtype=torch.float32, device=q.device)
+    else:
+        _like(lse, "lse", (heads, q_shape[0]), torch.float32, device)
     workspace = _attention_workspace(shape, 0, workspace, q)
-    _run("eqlin_attention_forward", q.device, stream, ctypes.byref(shape), q.data_ptr(), k.data_ptr(), v.data_ptr(),
-         o.data_ptr(), lse.data_ptr(), _ptr(workspace), 0 if workspace is None else workspace.numel())
+    _run("eqlin_attention_forward", device, stream, ctypes.byref(shape), q.data_ptr(), k.data_ptr(), v.data_ptr(),
+         o.data_ptr(), lse.data_ptr(), _ptr(workspace), _workspace(workspace, device))
     return o, lse
 
 
@@ -299,22 +312,20 @@ def eqlin_attention_backward(do: torch.Tensor, q: torch.Tensor, k: torch.Tensor,
                              stream=None) -> tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
     """(dq, dk, dv) from do = dL/do and the forward's inputs, o and lse.  grads gives the three
     outputs (channel slices of one joint gradient will do); they are allocated when not given."""
-    _features(q, "q")
-    shape = _attention_shape(q, k, v, o, heads, kv_heads, q_offsets, k_offsets, causal, scale)
+    shape, q_shape, k_shape, dtype, device = _attention_shape(q, k, v, heads, kv_heads, q_offsets, k_offsets, causal,
+                                                              scale)
+    shape.o_stride = _rows(o, "o", q_shape, dtype, device)
+    _like(lse, "lse", (heads, q_shape[0]), torch.float32, device)
     if grads is None:
-        grads = tuple(torch.empty(t.shape, dtype=t.dtype, device=t.device) for t in (q, k, v))
-    dq, dk, dv = grads
-    for t, ref, name in ((do, q, "do"), (dq, q, "dq"), (dk, k, "dk"), (dv, v, "dv")):
-        if t.shape != ref.shape or t.dtype != ref.dtype or t.device != ref.device:
-            raise ValueError(f"{name} must be a {tuple(ref.shape)} {ref.dtype} tensor on {ref.device}")
-    if lse.shape != (heads, q.shape[0]) or lse.dtype != torch.float32 or lse.device != q.device \
-            or not lse.is_contiguous():
-        raise ValueError(f"lse must be a contiguous [{heads}, {q.shape[0]}] fp32 tensor on {q.device}")
-    strides = _GradStrides(_rows(do, "do"), _rows(dq, "dq"), _rows(dk, "dk"), _rows(dv, "dv"))
+        dq, dk, dv = (torch.empty(t, dtype=dtype, device=q.device) for t in (q_shape, k_shape, k_shape))
+    else:
+        dq, dk, dv = grads
+    strides = _GradStrides(_rows(do, "do", q_shape, dtype, device), _rows(dq, "dq", q_shape, dtype, device),
+                           _rows(dk, "dk", k_shape, dtype, device), _rows(dv, "dv", k_shape, dtype, device))
     workspace = _attention_workspace(shape, 1, workspace, q)
-    _run("eqlin_attention_backward", q.device, stream, ctypes.byref(shape), ctypes.byref(strides), do.data_ptr(),
+    _run("eqlin_attention_backward", device, stream, ctypes.byref(shape), ctypes.byref(strides), do.data_ptr(),
          q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(), dq.data_ptr(), dk.data_ptr(),
-         dv.data_ptr(), _ptr(workspace), 0 if workspace is None else workspace.numel())
+         dv.data_ptr(), _ptr(workspace), _workspace(workspace, device))
     return dq, dk, dv
 
 
