@@ -26,7 +26,7 @@ struct NormPlan {
 // the pair that covers the row with the fewest idle vectors; among equals the one with more
 // vectors per thread (fewer shuffle steps, more loads in flight).  p4 C = 96 in 16 bits: 48
 // vectors, 16 threads of 3.
-int plan_norm(int64_t N, int64_t C, int64_t G, int io, int sms, NormPlan* pl) {
+int plan_norm(int64_t N, int64_t C, int64_t G, int io, int sms, bool backward, NormPlan* pl) {
     const int64_t L = C * G;
     const int full = io == EQLIN_F32 ? 4 : 8;
     pl->vec = L % full == 0 ? full : 1;
@@ -48,7 +48,8 @@ int plan_norm(int64_t N, int64_t C, int64_t G, int io, int sms, NormPlan* pl) {
     pl->wide = pl->tpr > 32;
     const int64_t groups = pl->wide ? 1 : norm::kThreads / pl->tpr;
     const int64_t rows = (N + groups - 1) / groups;
-    pl->blocks = static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>(rows, int64_t(sms) * 4)));
+    const int per_sm = backward ? norm::bwd_blocks(pl->vpt, pl->wide) : norm::fwd_blocks(pl->vpt, pl->wide);
+    pl->blocks = static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>(rows, int64_t(sms) * per_sm)));
     return EQLIN_OK;
 }
 
@@ -97,7 +98,7 @@ template <class T, int VEC>
 int launch_norm_bwd(const NormPlan& pl, const norm::Params& p, cudaStream_t st) {
     return with_vpt<T, VEC>(pl, [&](auto vpt, auto wide) {
         return launch(norm::eqlin_rmsnorm_bwd_kernel<T, VEC, decltype(vpt)::value, decltype(wide)::value>,
-                      dim3(pl.blocks), dim3(pl.wide ? pl.tpr : norm::kThreads), p.partial ? bwd_smem(pl) : 0, st,
+                      dim3(pl.blocks), dim3(pl.wide ? pl.tpr : norm::kThreads), bwd_smem(pl), st,
                       "norm gradient launch", p);
     });
 }
@@ -108,7 +109,7 @@ int norm_forward(const void* x, const void* residual, const void* weight, void* 
     int s = check_norm(N, C, G, eps, w_dtype, io, &lg);
     if (s != EQLIN_OK) return s;
     NormPlan pl;
-    if ((s = plan_norm(N, C, G, io, 1, &pl)) != EQLIN_OK) return s;   // sizes first, without a device
+    if ((s = plan_norm(N, C, G, io, 1, false, &pl)) != EQLIN_OK) return s;   // sizes first, without a device
     if (N == 0) return EQLIN_OK;
     if (!x || !y || (out8 && !scale)) return report(EQLIN_ERR_INVALID_ARG, "x, y or scale is NULL");
     if (!aligned(x, 16) || !aligned(y, 16) || !aligned(residual, 16) || !aligned(sum_out, 16) || !aligned(scale, 4) ||
@@ -116,7 +117,7 @@ int norm_forward(const void* x, const void* residual, const void* weight, void* 
         return report(EQLIN_ERR_MISALIGNED, "x, residual, y and sum_out must be 16-byte aligned");
     int sms = 0;
     if ((s = current_device(nullptr, &sms)) != EQLIN_OK) return s;
-    plan_norm(N, C, G, io, sms, &pl);
+    plan_norm(N, C, G, io, sms, false, &pl);
     norm::Params p = {};
     p.x = x;
     p.residual = residual;
@@ -179,7 +180,7 @@ int eqlin_rmsnorm_backward_workspace_size(int64_t N, int64_t C, int64_t G, int i
     if (s != EQLIN_OK) return s;
     NormPlan pl;
     // the most blocks that any sm_100 device of up to 256 SMs takes, so that no device is needed
-    if ((s = plan_norm(N, C, G, io_dtype, 256, &pl)) != EQLIN_OK) return s;
+    if ((s = plan_norm(N, C, G, io_dtype, 256, true, &pl)) != EQLIN_OK) return s;
     *bytes = N == 0 ? 0 : size_t(pl.blocks) * size_t(C) * sizeof(float);
     return EQLIN_OK;
 }
@@ -191,7 +192,7 @@ int eqlin_rmsnorm_backward(const void* dy, const void* sum, const void* weight, 
     int s = check_norm(N, C, G, eps, w_dtype, io_dtype, &lg);
     if (s != EQLIN_OK) return s;
     NormPlan pl;
-    if ((s = plan_norm(N, C, G, io_dtype, 1, &pl)) != EQLIN_OK) return s;
+    if ((s = plan_norm(N, C, G, io_dtype, 1, true, &pl)) != EQLIN_OK) return s;
     if (!aligned(dweight, 4)) return report(EQLIN_ERR_MISALIGNED, "dweight must be 4-byte aligned");
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (N == 0) {   // the gradient of an empty batch is zero
@@ -213,7 +214,7 @@ int eqlin_rmsnorm_backward(const void* dy, const void* sum, const void* weight, 
     }
     int sms = 0;
     if ((s = current_device(nullptr, &sms)) != EQLIN_OK) return s;
-    plan_norm(N, C, G, io_dtype, std::min(sms, 256), &pl);
+    plan_norm(N, C, G, io_dtype, std::min(sms, 256), true, &pl);
     norm::Params p = {};
     p.x = dy;
     p.residual = sum;

@@ -27,6 +27,10 @@ constexpr int kThreads = 256;      // block of the narrow form: 256 / TPR row gr
 constexpr int kMaxWide = 512;      // the wide form: one row group of 64..512 threads
 constexpr int kMaxVpt = 4;
 constexpr float kE4m3Max = 448.f;
+// Blocks on an SM, by the vectors of a thread: what the registers allow (the gradients hold three tensors' vectors
+// and the sums of dw).  Grids are this many blocks for each SM, so that all run at once.
+constexpr int fwd_blocks(int vpt, bool wide) { return wide ? (vpt <= 2 ? 2 : 1) : vpt == 1 ? 6 : vpt == 2 ? 4 : 3; }
+constexpr int bwd_blocks(int vpt, bool wide) { return wide ? (vpt <= 2 ? 2 : 1) : vpt == 1 ? 4 : vpt == 2 ? 3 : 2; }
 
 struct Params {
     const void* x;          // fwd: x;  bwd: dy
@@ -98,7 +102,7 @@ __device__ __forceinline__ void load_weights(const Params& p, int lane, float (&
 // The dependent launch is let go at the start: its griddepcontrol.wait still waits for the
 // end of this grid.
 template <class T, int VEC, int VPT, bool WIDE, bool OUT8>
-__global__ void __launch_bounds__(WIDE ? kMaxWide : kThreads) eqlin_add_rmsnorm_kernel(const Params p) {
+__global__ void __launch_bounds__(WIDE ? kMaxWide : kThreads, fwd_blocks(VPT, WIDE)) eqlin_add_rmsnorm_kernel(const Params p) {
     using V = Vec<T, VEC>;
     __shared__ float red[16];
     const int groups = WIDE ? 1 : kThreads / p.tpr;
@@ -164,6 +168,9 @@ __global__ void __launch_bounds__(WIDE ? kMaxWide : kThreads) eqlin_add_rmsnorm_
             top = group_max<WIDE>(top, p.tpr, red);
             const float scale = top > 0.f ? top / kE4m3Max : 1.f;
             if (!live) continue;
+            // one reciprocal for the row: within 2 units in the last place of y / scale, far below half of an
+            // e4m3 step
+            const float inv = 1.f / scale;
             if (lane == 0) p.scale[row] = scale;
             uint8_t* out = static_cast<uint8_t*>(p.y) + row * p.L;
 #pragma unroll
@@ -171,15 +178,15 @@ __global__ void __launch_bounds__(WIDE ? kMaxWide : kThreads) eqlin_add_rmsnorm_
                 const int v = lane + j * p.tpr;
                 if (v >= nv) continue;
                 if constexpr (VEC == 1) {
-                    out[v] = __nv_cvt_float_to_fp8(r[j][0] / scale, __NV_SATFINITE, __NV_E4M3);
+                    out[v] = __nv_cvt_float_to_fp8(r[j][0] * inv, __NV_SATFINITE, __NV_E4M3);
                 } else {
                     uint32_t q[VEC / 4];
 #pragma unroll
                     for (int e = 0; e < VEC; e += 4) {
-                        const uint32_t a = __nv_cvt_float2_to_fp8x2(make_float2(r[j][e] / scale, r[j][e + 1] / scale),
+                        const uint32_t a = __nv_cvt_float2_to_fp8x2(make_float2(r[j][e] * inv, r[j][e + 1] * inv),
                                                                     __NV_SATFINITE, __NV_E4M3);
                         const uint32_t b = __nv_cvt_float2_to_fp8x2(
-                            make_float2(r[j][e + 2] / scale, r[j][e + 3] / scale), __NV_SATFINITE, __NV_E4M3);
+                            make_float2(r[j][e + 2] * inv, r[j][e + 3] * inv), __NV_SATFINITE, __NV_E4M3);
                         q[e / 4] = a | (b << 16);
                     }
                     if constexpr (VEC == 8) *reinterpret_cast<uint2*>(out + v * VEC) = make_uint2(q[0], q[1]);
@@ -198,9 +205,10 @@ __global__ void __launch_bounds__(WIDE ? kMaxWide : kThreads) eqlin_add_rmsnorm_
 }
 
 // The gradients: dx (of x and of the residual alike) and, per block, the sums of dw.
-// Dynamic shared memory (with p.partial): groups * tpr * VPT * VEC floats.
+// Dynamic shared memory: groups * tpr * VPT * VEC floats for the sums of dw; before that, at its start, the
+// weights of tpr * VPT * VEC columns (registers would cost a block per SM).
 template <class T, int VEC, int VPT, bool WIDE>
-__global__ void __launch_bounds__(WIDE ? kMaxWide : kThreads) eqlin_rmsnorm_bwd_kernel(const Params p) {
+__global__ void __launch_bounds__(WIDE ? kMaxWide : kThreads, bwd_blocks(VPT, WIDE)) eqlin_rmsnorm_bwd_kernel(const Params p) {
     using V = Vec<T, VEC>;
     __shared__ float red[32];
     extern __shared__ float acc_smem[];
@@ -210,12 +218,30 @@ __global__ void __launch_bounds__(WIDE ? kMaxWide : kThreads) eqlin_rmsnorm_bwd_
     const int nv = p.L / VEC;
     ptx::grid_launch_dependents();
     ptx::grid_dependency_wait();
-    float w[VPT][VEC], dw[VPT][VEC];
-    load_weights<VEC, VPT>(p, lane, w);
+    float dw[VPT][VEC];
 #pragma unroll
     for (int j = 0; j < VPT; ++j)
 #pragma unroll
         for (int e = 0; e < VEC; ++e) dw[j][e] = 0.f;
+    for (int i = threadIdx.x; i < p.tpr * VPT * VEC; i += blockDim.x)
+        acc_smem[i] = p.weight && i < p.L ? load_param(p.weight, p.w_dtype, i >> p.lg_g) : 1.f;
+    __syncthreads();
+    auto weights = [&](int j, float (&w)[VEC]) {
+        const float* s = acc_smem + (lane + j * p.tpr) * VEC;
+        if constexpr (VEC % 4 == 0) {
+#pragma unroll
+            for (int e = 0; e < VEC; e += 4) {
+                const float4 v = *reinterpret_cast<const float4*>(s + e);
+                w[e] = v.x;
+                w[e + 1] = v.y;
+                w[e + 2] = v.z;
+                w[e + 3] = v.w;
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) w[e] = s[e];
+        }
+    };
     const float inv_l = 1.f / static_cast<float>(p.L);
     for (long long base = static_cast<long long>(blockIdx.x) * groups; base < p.N;
          base += static_cast<long long>(gridDim.x) * groups) {
@@ -236,13 +262,14 @@ __global__ void __launch_bounds__(WIDE ? kMaxWide : kThreads) eqlin_rmsnorm_bwd_
         float s[2] = {0.f, 0.f};   // sum r^2 and sum w dy r
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
-            float dy[VEC], r[VEC];
+            float dy[VEC], r[VEC], w[VEC];
             V::unpack(rdy[j], dy);
             V::unpack(rs[j], r);
+            weights(j, w);
 #pragma unroll
             for (int e = 0; e < VEC; ++e) {
                 s[0] = fmaf(r[e], r[e], s[0]);
-                s[1] = fmaf(w[j][e] * dy[e], r[e], s[1]);
+                s[1] = fmaf(w[e] * dy[e], r[e], s[1]);
             }
         }
         group_sum<WIDE, 2>(s, p.tpr, red);
@@ -252,19 +279,21 @@ __global__ void __launch_bounds__(WIDE ? kMaxWide : kThreads) eqlin_rmsnorm_bwd_
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
             const int v = lane + j * p.tpr;
-            float dy[VEC], r[VEC], d[VEC];
+            float dy[VEC], r[VEC], d[VEC], w[VEC];
             V::unpack(rdy[j], dy);
             V::unpack(rs[j], r);
             V::unpack(rd[j], d);
+            weights(j, w);
 #pragma unroll
             for (int e = 0; e < VEC; ++e) {
                 dw[j][e] = fmaf(dy[e], r[e] * rstd, dw[j][e]);
-                d[e] += rstd * (w[j][e] * dy[e] - r[e] * inner);
+                d[e] += rstd * (w[e] * dy[e] - r[e] * inner);
             }
             if (live && v < nv) V::store(out + v * VEC, V::pack(d));
         }
     }
     if (!p.partial) return;
+    __syncthreads();   // the weights are read
     const int row_pad = p.tpr * VPT * VEC;
 #pragma unroll
     for (int j = 0; j < VPT; ++j)

@@ -42,13 +42,34 @@ struct Params {
 };
 
 template <class T, int VEC>
-__global__ void __launch_bounds__(kThreads) eqlin_rope_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(kThreads, 3) eqlin_rope_kernel(const __grid_constant__ Params p) {
     using V = Vec<T, VEC>;
     extern __shared__ float2 cs[];   // [tokens][pairs]: cos, sin
     const long long first = static_cast<long long>(blockIdx.x) * p.tokens;
     const int here = static_cast<int>(p.N - first < p.tokens ? p.N - first : p.tokens);
     ptx::grid_launch_dependents();
     ptx::grid_dependency_wait();
+    const int nv = p.half / VEC;               // vectors of half a head
+    const int per_token = p.heads * nv, total = here * per_token;
+    const T* x = static_cast<const T*>(p.x) + first * p.x_stride;
+    T* y = static_cast<T*>(p.y) + first * p.y_stride;
+    typename V::Raw lo[kUnroll], hi[kUnroll];
+    int tok[kUnroll], feat[kUnroll];           // token of the block, feature of the row
+    auto fetch = [&](int i0) {
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+            const int i = i0 + u * kThreads;
+            tok[u] = i / per_token;
+            const int r = i - tok[u] * per_token, h = r / nv;
+            feat[u] = r * VEC + h * p.half;    // h heads of 2 * half, of which r counts half
+            if (i < total) {
+                const T* at = x + tok[u] * p.x_stride + feat[u];
+                lo[u] = V::load(at);
+                hi[u] = V::load(at + p.half);
+            }
+        }
+    };
+    fetch(threadIdx.x);                        // on their way while the angles are computed
     for (int i = threadIdx.x; i < here * p.pairs; i += kThreads) {
         const int t = i / p.pairs, j = i - t * p.pairs;
         int a = 0;
@@ -61,25 +82,7 @@ __global__ void __launch_bounds__(kThreads) eqlin_rope_kernel(const __grid_const
         cs[i] = make_float2(c, s * p.sign);
     }
     __syncthreads();
-    const int nv = p.half / VEC;               // vectors of half a head
-    const int per_token = p.heads * nv, total = here * per_token;
-    for (int i0 = threadIdx.x; i0 < total; i0 += kThreads * kUnroll) {
-        typename V::Raw lo[kUnroll], hi[kUnroll];
-        long long at[kUnroll];
-        int tok[kUnroll], feat[kUnroll];
-#pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-            const int i = i0 + u * kThreads;
-            tok[u] = i / per_token;
-            const int r = i - tok[u] * per_token, h = r / nv;
-            feat[u] = (r - h * nv) * VEC;
-            at[u] = static_cast<long long>(h) * 2 * p.half + feat[u];
-            if (i < total) {
-                const T* x = static_cast<const T*>(p.x) + (first + tok[u]) * p.x_stride + at[u];
-                lo[u] = V::load(x);
-                hi[u] = V::load(x + p.half);
-            }
-        }
+    for (int i0 = threadIdx.x; i0 < total;) {
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
             if (i0 + u * kThreads >= total) break;
@@ -87,16 +90,19 @@ __global__ void __launch_bounds__(kThreads) eqlin_rope_kernel(const __grid_const
             V::unpack(lo[u], a);
             V::unpack(hi[u], b);
             const float2* t = cs + tok[u] * p.pairs;
+            const int in_half = feat[u] % p.half;
 #pragma unroll
             for (int e = 0; e < VEC; ++e) {
-                const float2 w = t[(feat[u] + e) >> p.lg_g];
+                const float2 w = t[(in_half + e) >> p.lg_g];
                 ya[e] = a[e] * w.x - b[e] * w.y;
                 yb[e] = b[e] * w.x + a[e] * w.y;
             }
-            T* y = static_cast<T*>(p.y) + (first + tok[u]) * p.y_stride + at[u];
-            V::store(y, V::pack(ya));
-            V::store(y + p.half, V::pack(yb));
+            T* to = y + tok[u] * p.y_stride + feat[u];
+            V::store(to, V::pack(ya));
+            V::store(to + p.half, V::pack(yb));
         }
+        i0 += kThreads * kUnroll;
+        if (i0 < total) fetch(i0);
     }
 }
 
