@@ -92,14 +92,15 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
 }
 
 // Tensor [rows][heads][D], rows `stride` features apart, read in boxes of 64 features of one head and
-// 128 rows with 128-byte swizzle.  Coordinates are (0 or 64, head, row): every copy starts on a
+// box_rows rows with 128-byte swizzle.  Coordinates are (0 or 64, head, row): every copy starts on a
 // 16-byte boundary.  What lies outside the tensor, features past D among it, reads as zero.
-int encode_map(const void* t, int64_t rows, int64_t heads, int64_t D, int64_t stride, int io, CUtensorMap* map) {
+int encode_map(const void* t, int64_t rows, int64_t heads, int64_t D, int64_t stride, int io, CUtensorMap* map,
+               int box_rows = attn::tc::kTile) {
     auto encode = tensor_map_encoder();
     if (!encode) return report(EQLIN_ERR_CUDA, "cuTensorMapEncodeTiled is unavailable");
     cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(heads), static_cast<cuuint64_t>(rows)};
     cuuint64_t strides[2] = {static_cast<cuuint64_t>(D * 2), static_cast<cuuint64_t>(stride * 2)};
-    cuuint32_t box[3] = {64, 1, static_cast<cuuint32_t>(attn::tc::kTile)};
+    cuuint32_t box[3] = {64, 1, static_cast<cuuint32_t>(box_rows)};
     cuuint32_t estr[3] = {1, 1, 1};
     const CUresult r = encode(map, io == EQLIN_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
                               const_cast<void*>(t), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
@@ -300,12 +301,12 @@ int backward_tc(const attn::tc::BwdParams& bp, int io, cudaStream_t st) {
     if (s == EQLIN_OK) s = tc_grid(p.q_rows, p.sequences, tc::kTile, p.heads, &grid_q);
     CUtensorMap mq, mk, mv, mdo;
     if (s == EQLIN_OK && p.q_rows > 0) {
-        s = encode_map(p.q, p.q_rows, p.heads, p.D, p.q_stride, io, &mq);
-        if (s == EQLIN_OK) s = encode_map(p.dout, p.q_rows, p.heads, p.D, p.do_stride, io, &mdo);
+        s = encode_map(p.q, p.q_rows, p.heads, p.D, p.q_stride, io, &mq, B::LOAD_ROWS);
+        if (s == EQLIN_OK) s = encode_map(p.dout, p.q_rows, p.heads, p.D, p.do_stride, io, &mdo, B::LOAD_ROWS);
     }
     if (s == EQLIN_OK && p.k_rows > 0) {
-        s = encode_map(p.k, p.k_rows, p.kv_heads, p.D, p.k_stride, io, &mk);
-        if (s == EQLIN_OK) s = encode_map(p.v, p.k_rows, p.kv_heads, p.D, p.v_stride, io, &mv);
+        s = encode_map(p.k, p.k_rows, p.kv_heads, p.D, p.k_stride, io, &mk, B::LOAD_ROWS);
+        if (s == EQLIN_OK) s = encode_map(p.v, p.k_rows, p.kv_heads, p.D, p.v_stride, io, &mv, B::LOAD_ROWS);
     }
     if (s != EQLIN_OK) return s;
     if (p.q_rows == 0) mq = mdo = mk;   // the side without rows is never read

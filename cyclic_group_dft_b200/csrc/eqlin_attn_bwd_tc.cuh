@@ -9,7 +9,7 @@
 // Computing S and dP twice costs two more products than one kernel would (7 for 5), and saves the
 // atomics or the fp32 copy of dq that one kernel needs.
 // Warps: two warpgroups of 128 threads for the elementwise work (thread = TMEM lane; each warpgroup
-// takes 64 of the 128 columns, and its 32 words of the A operand lie at the start of them), one warp of loads, one of MMAs.
+// takes half of the columns, and its words of the A operand lie at the start of them), one warp of loads, one of MMAs.
 #pragma once
 
 #include "eqlin_attn_tc.cuh"
@@ -18,16 +18,25 @@ namespace eqlin {
 namespace attn {
 namespace tc {
 
+// BN: rows of a tile of the side that is walked.  For heads of up to 64 features it is 64: then a block needs
+// half of the TMEM, and the chain of products and elementwise work of one block on an SM fills the gaps of the
+// other's.
 template <int DP>
 struct Bwd {
+    static constexpr int BN = DP;
+    static constexpr int HB = BN / 2;                    // columns of a warpgroup
     static constexpr int BOXES = DP / 64;
-    static constexpr int TILE_BYTES = BOXES * kBoxBytes;
-    static constexpr int FIXED = 2;                      // tiles that stay: K, V or Q, dO
-    static constexpr int STAGES = DP == 64 ? 8 : 4;      // ring
+    static constexpr int OWN_BYTES = BOXES * kBoxBytes;  // 128 rows
+    static constexpr int WALK_BYTES = BOXES * BN * 128;
+    static constexpr int LOAD_ROWS = BN;                 // rows of a TMA box, for both sides
+    static constexpr int STAGES = DP == 64 ? 8 : 5;
+    static constexpr int TMEM_COLS = DP == 64 ? 256 : 512;
+    static constexpr int BLOCKS = DP == 64 ? 2 : 1;
+    static constexpr uint32_t EX2_FMA = DP == 64 ? 0x44 : 0;   // as in the forward
     static constexpr int THREADS = 256 + 64;
     static constexpr int WARP_LOAD = 8, WARP_MMA = 9;
-    static constexpr size_t SMEM = 1024 + 512 + 4 * kTile * sizeof(float2) / 2 +
-                                   static_cast<size_t>(STAGES + FIXED) * TILE_BYTES;
+    static constexpr size_t SMEM = static_cast<size_t>(2) * OWN_BYTES + STAGES * WALK_BYTES + 2 * BN * sizeof(float2) + 256;
+    static_assert(SMEM <= 232448 / BLOCKS, "shared memory");
 };
 
 struct BwdParams {
@@ -60,26 +69,30 @@ __device__ __forceinline__ void store_accumulator(uint32_t taddr, bool filled, b
 
 // ------------------------------------------------------------------------------- dk and dv
 template <class T, int DP>
-__global__ void __launch_bounds__(Bwd<DP>::THREADS, 1)
+__global__ void __launch_bounds__(Bwd<DP>::THREADS, Bwd<DP>::BLOCKS)
     eqlin_attn_dkv_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                              const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mdo,
                              const __grid_constant__ BwdParams bp) {
     using B = Bwd<DP>;
     constexpr int ST = B::STAGES;
     const Params& p = bp.p;
-    extern __shared__ uint8_t raw[];
-    uint8_t* base = ptx::smem_align_1k(raw);
-    float2* rows = reinterpret_cast<float2*>(base + (ST + B::FIXED) * B::TILE_BYTES);   // [2][128]: lse, delta
-    uint64_t* bars = reinterpret_cast<uint64_t*>(rows + 2 * kTile);
-    Ctl* ctl = reinterpret_cast<Ctl*>(bars + 48);
+    constexpr int BN = B::BN, HB = B::HB;
+    extern __shared__ __align__(1024) uint8_t base[];
+    float2* rows = reinterpret_cast<float2*>(base + 2 * B::OWN_BYTES + ST * B::WALK_BYTES);   // [2][BN]: lse, delta
+    uint64_t* bars = reinterpret_cast<uint64_t*>(rows + 2 * BN);
+    Ctl* ctl = reinterpret_cast<Ctl*>(bars + 30);
     auto bar = [&](int i) { return ptx::smem_u32(bars + i); };
     auto full = [&](int s) { return bar(s); };
     auto empty = [&](int s) { return bar(ST + s); };
     const uint32_t fixed_full = bar(2 * ST), s_full = bar(2 * ST + 1), dp_full = bar(2 * ST + 2),
                    p_full = bar(2 * ST + 3), ds_full = bar(2 * ST + 4), done = bar(2 * ST + 5),
                    rows_full = bar(2 * ST + 6);
-    uint8_t *k_tile = base, *v_tile = base + B::TILE_BYTES, *ring = base + 2 * B::TILE_BYTES;
+    uint8_t *k_tile = base, *v_tile = base + B::OWN_BYTES, *ring = base + 2 * B::OWN_BYTES;
 
+    if (ptx::smem_u32(base) & 1023u) {   // the swizzled tiles rely on the declared alignment
+        if (threadIdx.x == 0) atomicCAS(&g_status, 0, kErrMisaligned);
+        return;
+    }
     const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;   // (uniform)
     if (threadIdx.x == 0) {
         ctl->abort = 0;
@@ -97,7 +110,7 @@ __global__ void __launch_bounds__(Bwd<DP>::THREADS, 1)
         ptx::fence_mbar_init();
     }
     if (warp == B::WARP_MMA) {
-        ptx::tmem_alloc(ptx::smem_u32(&ctl->tmem_base), 512);
+        ptx::tmem_alloc(ptx::smem_u32(&ctl->tmem_base), B::TMEM_COLS);
         ptx::tmem_relinquish();
     }
     ptx::grid_dependency_wait();
@@ -106,33 +119,34 @@ __global__ void __launch_bounds__(Bwd<DP>::THREADS, 1)
     const Rows qr = sequence_rows(p.q_offsets, t.b, p.q_rows);
     const int r0 = t.tile * kTile;
     // query tiles: from the first that sees the first key of this tile
-    const int begin = t.tile < 0 ? 0 : first_query(r0, qr.len, t.own.len, p.causal) / kTile;
-    const int per_head = t.tile < 0 ? 0 : max(0, (qr.len + kTile - 1) / kTile - begin);
+    const int begin = t.tile < 0 ? 0 : first_query(r0, qr.len, t.own.len, p.causal) / BN;
+    const int per_head = t.tile < 0 ? 0 : max(0, (qr.len + BN - 1) / BN - begin);
     const int n = per_head * group;
     ptx::tc_fence_before();
     __syncthreads();
     ptx::tc_fence_after();
     ptx::grid_launch_dependents();   // after the allocation, as in the forward
     const uint32_t tmem = ctl->tmem_base;
-    const uint32_t t_s = tmem, t_dp = tmem + 128, t_dv = tmem + 256, t_dk = tmem + 256 + DP;
+    const uint32_t t_s = tmem, t_dp = tmem + BN, t_dv = tmem + 2 * BN, t_dk = tmem + 2 * BN + DP;
 
     if (warp == B::WARP_LOAD) {
         if (lane == 0 && n > 0) {
             long long issued = 0;
-            auto load = [&](const CUtensorMap* m, uint8_t* dst, int head, int row, uint32_t b) {
+            auto load = [&](const CUtensorMap* m, uint8_t* dst, int rows, int head, int row, uint32_t b) {
                 for (int x = 0; x < B::BOXES; ++x)
-                    tma_load_3d(ptx::smem_u32(dst) + x * kBoxBytes, m, x * 64, head, row, b);
+                    for (int r = 0; r < rows; r += B::LOAD_ROWS)
+                        tma_load_3d(ptx::smem_u32(dst) + x * rows * 128 + r * 128, m, x * 64, head, row + r, b);
             };
-            ptx::mbar_arrive_expect_tx(fixed_full, 2 * B::TILE_BYTES);
-            load(&mk, k_tile, hk, t.own.start + r0, fixed_full);
-            load(&mv, v_tile, hk, t.own.start + r0, fixed_full);
+            ptx::mbar_arrive_expect_tx(fixed_full, 2 * B::OWN_BYTES);
+            load(&mk, k_tile, kTile, hk, t.own.start + r0, fixed_full);
+            load(&mv, v_tile, kTile, hk, t.own.start + r0, fixed_full);
             for (int u = 0; u < 2 * n; ++u) {      // Q_0, dO_0, Q_1, dO_1, ...
                 const int s = u % ST, it = u >> 1;
                 if (u >= ST && !wait_bounded(empty(s), ((u / ST) & 1) ^ 1, ctl, p.timeout_ns)) break;
                 if (issued == bp.stop_after) break;
-                ptx::mbar_arrive_expect_tx(full(s), B::TILE_BYTES);
-                load(u & 1 ? &mdo : &mq, ring + s * B::TILE_BYTES, hk * group + it / per_head,
-                     qr.start + (begin + it % per_head) * kTile, full(s));
+                ptx::mbar_arrive_expect_tx(full(s), B::WALK_BYTES);
+                load(u & 1 ? &mdo : &mq, ring + s * B::WALK_BYTES, BN, hk * group + it / per_head,
+                     qr.start + (begin + it % per_head) * BN, full(s));
                 ++issued;
             }
             drain_wait(fixed_full, 0, p.timeout_ns);
@@ -143,20 +157,20 @@ __global__ void __launch_bounds__(Bwd<DP>::THREADS, 1)
         }
     } else if (warp == B::WARP_MMA) {
         if (n > 0) {
-            const uint32_t id_s = idesc_f16kind_f32(128, 128, Io16<T>::kUmmaFormat, false);
+            const uint32_t id_s = idesc_f16kind_f32(128, BN, Io16<T>::kUmmaFormat, false);
             const uint32_t id_o = idesc_f16kind_f32(128, (p.D + 15) / 16 * 16, Io16<T>::kUmmaFormat, false) | kBMnMajor;
             const int steps = (p.D + 15) / 16;
-            auto stage = [&](int u) { return ring + (u % ST) * B::TILE_BYTES; };
+            auto stage = [&](int u) { return ring + (u % ST) * B::WALK_BYTES; };
             // a ring tile, with zeros for the rows past the sequence's end
             auto take = [&](int u) {
                 if (!wait_warp(full(u % ST), (u / ST) & 1, ctl, p.timeout_ns)) return false;
-                const int valid = qr.len - (begin + (u >> 1) % per_head) * kTile;
-                if (valid < kTile) zero_tail(stage(u), B::BOXES, valid, lane);
+                const int valid = qr.len - (begin + (u >> 1) % per_head) * BN;
+                if (valid < BN) zero_tail<BN>(stage(u), B::BOXES, valid, lane);
                 return true;
             };
             auto product = [&](uint32_t d, uint8_t* fixed, int u, uint32_t b) {
                 if (elect_one()) {
-                    mma_features<DP>(d, ptx::smem_u32(fixed), ptx::smem_u32(stage(u)), steps, id_s);
+                    mma_features<DP, BN>(d, ptx::smem_u32(fixed), ptx::smem_u32(stage(u)), steps, id_s);
                     ptx::umma_commit(b);
                 }
                 __syncwarp();
@@ -168,7 +182,7 @@ __global__ void __launch_bounds__(Bwd<DP>::THREADS, 1)
             for (int j = 0; ok && j < n; ++j) {
                 if (!(ok = wait_warp(p_full, j & 1, ctl, p.timeout_ns))) break;
                 ptx::tc_fence_after();
-                if (elect_one()) mma_rows<64>(t_dv, t_s, ptx::smem_u32(stage(2 * j + 1)), id_o, j > 0);
+                if (elect_one()) mma_rows<BN, HB, 2>(t_dv, t_s, ptx::smem_u32(stage(2 * j + 1)), id_o, j > 0);
                 __syncwarp();
                 // MMAs of one thread run in order: S^T is written after P^T has been read out of it
                 if (j + 1 < n) {
@@ -178,7 +192,7 @@ __global__ void __launch_bounds__(Bwd<DP>::THREADS, 1)
                 if (!(ok = wait_warp(ds_full, j & 1, ctl, p.timeout_ns))) break;
                 ptx::tc_fence_after();
                 if (elect_one()) {
-                    mma_rows<64>(t_dk, t_dp, ptx::smem_u32(stage(2 * j)), id_o, j > 0);
+                    mma_rows<BN, HB, 2>(t_dk, t_dp, ptx::smem_u32(stage(2 * j)), id_o, j > 0);
                     ptx::umma_commit(empty((2 * j) % ST));
                     ptx::umma_commit(empty((2 * j + 1) % ST));
                 }
@@ -199,14 +213,14 @@ __global__ void __launch_bounds__(Bwd<DP>::THREADS, 1)
         const int row = r0 + (tid & 127);                          // key of the sequence
         const bool live = t.tile >= 0 && row < t.own.len;
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-        const uint32_t ts = t_s + lanes + half * 64, tdp = t_dp + lanes + half * 64;
+        const uint32_t ts = t_s + lanes + half * HB, tdp = t_dp + lanes + half * HB;
         const float c2 = p.scale * kLog2e;
         bool ok = true;
         // lse (threads of the first warpgroup) or delta (second) of query tid & 127 of tile j; a row
         // that sees no key, or is past the end, gets lse = +infinity: weights of zero
         auto fetch = [&](int j) {
-            const int q = (begin + j % per_head) * kTile + (tid & 127);
-            if (q >= qr.len) return half ? 0.f : INFINITY;
+            const int q = (begin + j % per_head) * BN + (tid & 127);
+            if ((tid & 127) >= BN || q >= qr.len) return half ? 0.f : INFINITY;
             const long long at = static_cast<long long>(hk * group + j / per_head) * p.q_rows + qr.start + q;
             if (half) return p.delta[at];
             const float l = p.lse[at];
@@ -214,41 +228,42 @@ __global__ void __launch_bounds__(Bwd<DP>::THREADS, 1)
         };
         float next = n > 0 ? fetch(0) : 0.f;
         for (int j = 0; j < n; ++j) {
-            float2* rj = rows + (j & 1) * kTile;
+            float2* rj = rows + (j & 1) * BN;
             // tile j - 2, which had this buffer, is read: dP of tile j - 1 was issued after all threads' dS of it
-            reinterpret_cast<float*>(rj + (tid & 127))[half] = next;
+            if ((tid & 127) < BN) reinterpret_cast<float*>(rj + (tid & 127))[half] = next;
             arrive_warp(rows_full, lane);
             if (j + 1 < n) next = fetch(j + 1);
             if (!(ok = wait_warp(rows_full, j & 1, ctl, p.timeout_ns))) break;
             if (!(ok = wait_warp(s_full, j & 1, ctl, p.timeout_ns))) break;
             ptx::tc_fence_after();
-            uint32_t s[2][32];
-            ptx::tmem_ld_32x32b<32>(ts, s[0]);
-            ptx::tmem_ld_32x32b<32>(ts + 32, s[1]);
+            uint32_t s[HB / 32][32];
+#pragma unroll
+            for (int c = 0; c < HB / 32; ++c) ptx::tmem_ld_32x32b<32>(ts + c * 32, s[c]);
             ptx::tmem_wait_ld();
-            ptx::tmem_regs_ready(s[0]);
-            ptx::tmem_regs_ready(s[1]);
-            const int q0 = (begin + j % per_head) * kTile;
+#pragma unroll
+            for (int c = 0; c < HB / 32; ++c) ptx::tmem_regs_ready(s[c]);
+            const int q0 = (begin + j % per_head) * BN;
             if (p.causal && static_cast<long long>(r0) + kTile - 1 > static_cast<long long>(q0) + t.own.len - qr.len) {
                 // key `row` is seen by queries from row - (keys - queries) on
-                const long long first = static_cast<long long>(row) - (t.own.len - qr.len) - q0 - half * 64;
+                const long long first = static_cast<long long>(row) - (t.own.len - qr.len) - q0 - half * HB;
 #pragma unroll
-                for (int c = 0; c < 2; ++c)
+                for (int c = 0; c < HB / 32; ++c)
 #pragma unroll
                     for (int e = 0; e < 32; ++e)
                         if (c * 32 + e < first) s[c][e] = 0xFF800000u;
             }
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
+            for (int c = 0; c < HB / 32; ++c) {
                 uint32_t w[16];
 #pragma unroll
                 for (int e = 0; e < 32; e += 2) {
-                    const float4 ld = *reinterpret_cast<const float4*>(rj + half * 64 + c * 32 + e);   // lse, delta, lse, delta
-                    const float a = ex2(fmaf(__uint_as_float(s[c][e]), c2, -ld.x));
-                    const float b = ex2(fmaf(__uint_as_float(s[c][e + 1]), c2, -ld.z));
-                    s[c][e] = __float_as_uint(a);
-                    s[c][e + 1] = __float_as_uint(b);
-                    w[e >> 1] = Io16<T>::pack(a, b);
+                    const float4 ld = *reinterpret_cast<const float4*>(rj + half * HB + c * 32 + e);   // lse, delta, lse, delta
+                    const float2 a = ex2_pair<B::EX2_FMA>(
+                        fma2(make_float2(__uint_as_float(s[c][e]), __uint_as_float(s[c][e + 1])), make_float2(c2, c2),
+                             make_float2(-ld.x, -ld.z)), e >> 1);
+                    s[c][e] = __float_as_uint(a.x);
+                    s[c][e + 1] = __float_as_uint(a.y);
+                    w[e >> 1] = Io16<T>::pack(a.x, a.y);
                 }
                 tmem_st16(ts + c * 16, w);
             }
@@ -258,19 +273,20 @@ __global__ void __launch_bounds__(Bwd<DP>::THREADS, 1)
             if (!(ok = wait_warp(dp_full, j & 1, ctl, p.timeout_ns))) break;
             ptx::tc_fence_after();
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
+            for (int c = 0; c < HB / 32; ++c) {
                 uint32_t d[32], w[16];
                 ptx::tmem_ld_32x32b<32>(tdp + c * 32, d);
                 ptx::tmem_wait_ld();
                 ptx::tmem_regs_ready(d);
 #pragma unroll
                 for (int e = 0; e < 32; e += 2) {
-                    const float4 ld = *reinterpret_cast<const float4*>(rj + half * 64 + c * 32 + e);
-                    const float a = __uint_as_float(s[c][e]) * (__uint_as_float(d[e]) - ld.y);
-                    const float b = __uint_as_float(s[c][e + 1]) * (__uint_as_float(d[e + 1]) - ld.w);
-                    w[e >> 1] = Io16<T>::pack(a, b);
+                    const float4 ld = *reinterpret_cast<const float4*>(rj + half * HB + c * 32 + e);
+                    const float2 a = mul2(make_float2(__uint_as_float(s[c][e]), __uint_as_float(s[c][e + 1])),
+                                          add2(make_float2(__uint_as_float(d[e]), __uint_as_float(d[e + 1])),
+                                               make_float2(-ld.y, -ld.w)));
+                    w[e >> 1] = Io16<T>::pack(a.x, a.y);
                 }
-                // words [0, 32) of the half: columns that this thread has read (c = 0: all of [0, 32))
+                // words over columns that this thread has read
                 tmem_st16(tdp + c * 16, w);
             }
             tmem_wait_st();
@@ -289,30 +305,34 @@ __global__ void __launch_bounds__(Bwd<DP>::THREADS, 1)
     __syncthreads();
     if (warp == B::WARP_MMA) {
         ptx::tc_fence_after();
-        ptx::tmem_dealloc(tmem, 512);
+        ptx::tmem_dealloc(tmem, B::TMEM_COLS);
     }
 }
 
 // ------------------------------------------------------------------------------------- dq
 template <class T, int DP>
-__global__ void __launch_bounds__(Bwd<DP>::THREADS, 1)
+__global__ void __launch_bounds__(Bwd<DP>::THREADS, Bwd<DP>::BLOCKS)
     eqlin_attn_dq_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                             const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mdo,
                             const __grid_constant__ BwdParams bp) {
     using B = Bwd<DP>;
     constexpr int ST = B::STAGES;
     const Params& p = bp.p;
-    extern __shared__ uint8_t raw[];
-    uint8_t* base = ptx::smem_align_1k(raw);
-    uint64_t* bars = reinterpret_cast<uint64_t*>(base + (ST + B::FIXED) * B::TILE_BYTES);
-    Ctl* ctl = reinterpret_cast<Ctl*>(bars + 48);
+    constexpr int BN = B::BN, HB = B::HB;
+    extern __shared__ __align__(1024) uint8_t base[];
+    uint64_t* bars = reinterpret_cast<uint64_t*>(base + 2 * B::OWN_BYTES + ST * B::WALK_BYTES);
+    Ctl* ctl = reinterpret_cast<Ctl*>(bars + 30);
     auto bar = [&](int i) { return ptx::smem_u32(bars + i); };
     auto full = [&](int s) { return bar(s); };
     auto empty = [&](int s) { return bar(ST + s); };
     const uint32_t fixed_full = bar(2 * ST), dp_full = bar(2 * ST + 1), ds_full = bar(2 * ST + 2), done = bar(2 * ST + 3);
     auto s_full = [&](int b) { return bar(2 * ST + 4 + b); };
-    uint8_t *q_tile = base, *do_tile = base + B::TILE_BYTES, *ring = base + 2 * B::TILE_BYTES;
+    uint8_t *q_tile = base, *do_tile = base + B::OWN_BYTES, *ring = base + 2 * B::OWN_BYTES;
 
+    if (ptx::smem_u32(base) & 1023u) {   // the swizzled tiles rely on the declared alignment
+        if (threadIdx.x == 0) atomicCAS(&g_status, 0, kErrMisaligned);
+        return;
+    }
     const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;   // (uniform)
     if (threadIdx.x == 0) {
         ctl->abort = 0;
@@ -329,7 +349,7 @@ __global__ void __launch_bounds__(Bwd<DP>::THREADS, 1)
         ptx::fence_mbar_init();
     }
     if (warp == B::WARP_MMA) {
-        ptx::tmem_alloc(ptx::smem_u32(&ctl->tmem_base), 512);
+        ptx::tmem_alloc(ptx::smem_u32(&ctl->tmem_base), B::TMEM_COLS);
         ptx::tmem_relinquish();
     }
     ptx::grid_dependency_wait();
@@ -340,31 +360,32 @@ __global__ void __launch_bounds__(Bwd<DP>::THREADS, 1)
     const Rows kr = sequence_rows(p.k_offsets, t.b, p.k_rows);
     const int r0 = t.tile * kTile;
     const int n = t.tile < 0 ? 0
-                             : (keys_seen(min(r0 + kTile, t.own.len) - 1, t.own.len, kr.len, p.causal) + kTile - 1) / kTile;
+                             : (keys_seen(min(r0 + kTile, t.own.len) - 1, t.own.len, kr.len, p.causal) + BN - 1) / BN;
     ptx::tc_fence_before();
     __syncthreads();
     ptx::tc_fence_after();
     ptx::grid_launch_dependents();   // after the allocation, as in the forward
     const uint32_t tmem = ctl->tmem_base;
-    auto t_s = [&](int j) { return tmem + (j & 1) * 128; };
-    const uint32_t t_dp = tmem + 256, t_dq = tmem + 384;
+    auto t_s = [&](int j) { return tmem + (j & 1) * BN; };
+    const uint32_t t_dp = tmem + 2 * BN, t_dq = tmem + 3 * BN;
 
     if (warp == B::WARP_LOAD) {
         if (lane == 0 && n > 0) {
             long long issued = 0;
-            auto load = [&](const CUtensorMap* m, uint8_t* dst, int head, int row, uint32_t b) {
+            auto load = [&](const CUtensorMap* m, uint8_t* dst, int rows, int head, int row, uint32_t b) {
                 for (int x = 0; x < B::BOXES; ++x)
-                    tma_load_3d(ptx::smem_u32(dst) + x * kBoxBytes, m, x * 64, head, row, b);
+                    for (int r = 0; r < rows; r += B::LOAD_ROWS)
+                        tma_load_3d(ptx::smem_u32(dst) + x * rows * 128 + r * 128, m, x * 64, head, row + r, b);
             };
-            ptx::mbar_arrive_expect_tx(fixed_full, 2 * B::TILE_BYTES);
-            load(&mq, q_tile, h, t.own.start + r0, fixed_full);
-            load(&mdo, do_tile, h, t.own.start + r0, fixed_full);
+            ptx::mbar_arrive_expect_tx(fixed_full, 2 * B::OWN_BYTES);
+            load(&mq, q_tile, kTile, h, t.own.start + r0, fixed_full);
+            load(&mdo, do_tile, kTile, h, t.own.start + r0, fixed_full);
             for (int u = 0; u < 2 * n; ++u) {      // K_0, V_0, K_1, V_1, ...
                 const int s = u % ST;
                 if (u >= ST && !wait_bounded(empty(s), ((u / ST) & 1) ^ 1, ctl, p.timeout_ns)) break;
                 if (issued == bp.stop_after) break;
-                ptx::mbar_arrive_expect_tx(full(s), B::TILE_BYTES);
-                load(u & 1 ? &mv : &mk, ring + s * B::TILE_BYTES, hk, kr.start + (u >> 1) * kTile, full(s));
+                ptx::mbar_arrive_expect_tx(full(s), B::WALK_BYTES);
+                load(u & 1 ? &mv : &mk, ring + s * B::WALK_BYTES, BN, hk, kr.start + (u >> 1) * BN, full(s));
                 ++issued;
             }
             drain_wait(fixed_full, 0, p.timeout_ns);
@@ -375,17 +396,17 @@ __global__ void __launch_bounds__(Bwd<DP>::THREADS, 1)
         }
     } else if (warp == B::WARP_MMA) {
         if (n > 0) {
-            const uint32_t id_s = idesc_f16kind_f32(128, 128, Io16<T>::kUmmaFormat, false);
+            const uint32_t id_s = idesc_f16kind_f32(128, BN, Io16<T>::kUmmaFormat, false);
             const uint32_t id_o = idesc_f16kind_f32(128, (p.D + 15) / 16 * 16, Io16<T>::kUmmaFormat, false) | kBMnMajor;
             const int steps = (p.D + 15) / 16;
-            auto stage = [&](int u) { return ring + (u % ST) * B::TILE_BYTES; };
+            auto stage = [&](int u) { return ring + (u % ST) * B::WALK_BYTES; };
             auto wait_stage = [&](int u) { return wait_warp(full(u % ST), (u / ST) & 1, ctl, p.timeout_ns); };
             auto scores = [&](int j) {
                 if (!wait_stage(2 * j)) return false;
-                const int valid = kr.len - j * kTile;
-                if (valid < kTile) zero_tail(stage(2 * j), B::BOXES, valid, lane);
+                const int valid = kr.len - j * BN;
+                if (valid < BN) zero_tail<BN>(stage(2 * j), B::BOXES, valid, lane);
                 if (elect_one()) {
-                    mma_features<DP>(t_s(j), ptx::smem_u32(q_tile), ptx::smem_u32(stage(2 * j)), steps, id_s);
+                    mma_features<DP, BN>(t_s(j), ptx::smem_u32(q_tile), ptx::smem_u32(stage(2 * j)), steps, id_s);
                     ptx::umma_commit(s_full(j & 1));
                 }
                 __syncwarp();
@@ -394,7 +415,7 @@ __global__ void __launch_bounds__(Bwd<DP>::THREADS, 1)
             auto dp = [&](int j) {
                 if (!wait_stage(2 * j + 1)) return false;
                 if (elect_one()) {
-                    mma_features<DP>(t_dp, ptx::smem_u32(do_tile), ptx::smem_u32(stage(2 * j + 1)), steps, id_s);
+                    mma_features<DP, BN>(t_dp, ptx::smem_u32(do_tile), ptx::smem_u32(stage(2 * j + 1)), steps, id_s);
                     ptx::umma_commit(dp_full);
                     ptx::umma_commit(empty((2 * j + 1) % ST));
                 }
@@ -409,7 +430,7 @@ __global__ void __launch_bounds__(Bwd<DP>::THREADS, 1)
                 ptx::tc_fence_after();
                 if (j + 1 < n && !(ok = dp(j + 1))) break;
                 if (elect_one()) {
-                    mma_rows<64>(t_dq, t_s(j), ptx::smem_u32(stage(2 * j)), id_o, j > 0);
+                    mma_rows<BN, HB, 2>(t_dq, t_s(j), ptx::smem_u32(stage(2 * j)), id_o, j > 0);
                     ptx::umma_commit(empty((2 * j) % ST));
                 }
                 __syncwarp();
@@ -438,32 +459,38 @@ __global__ void __launch_bounds__(Bwd<DP>::THREADS, 1)
         }
         bool ok = true;
         for (int j = 0; j < n; ++j) {
-            const uint32_t ts = t_s(j) + lanes + half * 64, tdp = t_dp + lanes + half * 64;
+            const uint32_t ts = t_s(j) + lanes + half * HB, tdp = t_dp + lanes + half * HB;
             if (!(ok = wait_warp(s_full(j & 1), (j >> 1) & 1, ctl, p.timeout_ns))) break;
             ptx::tc_fence_after();
-            uint32_t s[2][32];
-            ptx::tmem_ld_32x32b<32>(ts, s[0]);
-            ptx::tmem_ld_32x32b<32>(ts + 32, s[1]);
+            uint32_t s[HB / 32][32];
+#pragma unroll
+            for (int c = 0; c < HB / 32; ++c) ptx::tmem_ld_32x32b<32>(ts + c * 32, s[c]);
             ptx::tmem_wait_ld();
-            ptx::tmem_regs_ready(s[0]);
-            ptx::tmem_regs_ready(s[1]);
-            const bool masked = (j + 1) * kTile > seen_all;
-            const int n_seen = seen - j * kTile - half * 64;
+#pragma unroll
+            for (int c = 0; c < HB / 32; ++c) ptx::tmem_regs_ready(s[c]);
+            const bool masked = (j + 1) * BN > seen_all;
+            const int n_seen = seen - j * BN - half * HB;
             if (masked) {
 #pragma unroll
-                for (int c = 0; c < 2; ++c)
+                for (int c = 0; c < HB / 32; ++c)
 #pragma unroll
                     for (int e = 0; e < 32; ++e)
                         if (c * 32 + e >= n_seen) s[c][e] = 0xFF800000u;
             }
 #pragma unroll
-            for (int c = 0; c < 2; ++c)
+            for (int c = 0; c < HB / 32; ++c)
 #pragma unroll
-                for (int e = 0; e < 32; ++e) s[c][e] = __float_as_uint(ex2(fmaf(__uint_as_float(s[c][e]), c2, off)));
+                for (int e = 0; e < 32; e += 2) {
+                    const float2 a = ex2_pair<B::EX2_FMA>(
+                        fma2(make_float2(__uint_as_float(s[c][e]), __uint_as_float(s[c][e + 1])), make_float2(c2, c2),
+                             make_float2(off, off)), e >> 1);
+                    s[c][e] = __float_as_uint(a.x);
+                    s[c][e + 1] = __float_as_uint(a.y);
+                }
             if (!(ok = wait_warp(dp_full, j & 1, ctl, p.timeout_ns))) break;
             ptx::tc_fence_after();
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
+            for (int c = 0; c < HB / 32; ++c) {
                 uint32_t d[32], w[16];
                 ptx::tmem_ld_32x32b<32>(tdp + c * 32, d);
                 ptx::tmem_wait_ld();
@@ -474,9 +501,12 @@ __global__ void __launch_bounds__(Bwd<DP>::THREADS, 1)
                         if (c * 32 + e >= n_seen) d[e] = 0;
                 }
 #pragma unroll
-                for (int e = 0; e < 32; e += 2)
-                    w[e >> 1] = Io16<T>::pack(__uint_as_float(s[c][e]) * (__uint_as_float(d[e]) - delta),
-                                              __uint_as_float(s[c][e + 1]) * (__uint_as_float(d[e + 1]) - delta));
+                for (int e = 0; e < 32; e += 2) {
+                    const float2 a = mul2(make_float2(__uint_as_float(s[c][e]), __uint_as_float(s[c][e + 1])),
+                                          add2(make_float2(__uint_as_float(d[e]), __uint_as_float(d[e + 1])),
+                                               make_float2(-delta, -delta)));
+                    w[e >> 1] = Io16<T>::pack(a.x, a.y);
+                }
                 tmem_st16(ts + c * 16, w);
             }
             tmem_wait_st();
@@ -494,7 +524,7 @@ __global__ void __launch_bounds__(Bwd<DP>::THREADS, 1)
     __syncthreads();
     if (warp == B::WARP_MMA) {
         ptx::tc_fence_after();
-        ptx::tmem_dealloc(tmem, 512);
+        ptx::tmem_dealloc(tmem, B::TMEM_COLS);
     }
 }
 

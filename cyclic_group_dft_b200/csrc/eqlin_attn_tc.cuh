@@ -22,6 +22,7 @@ namespace tc {
 constexpr int kTile = 128;                       // token rows of an operand tile
 constexpr int kBoxBytes = kTile * 128;           // one box: 128 rows of 64 features
 constexpr int kErrTimeout = -6;                  // EQLIN_ERR_TIMEOUT
+constexpr int kErrMisaligned = -3;               // EQLIN_ERR_MISALIGNED
 constexpr uint32_t kWaitSleepNs = 20000;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -189,36 +190,37 @@ __device__ __forceinline__ float2 ex2_pair(float2 x, int pair) {
 constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
 __device__ __forceinline__ uint64_t desc_of(uint32_t lo) { return (static_cast<uint64_t>(kDescHi) << 32) | lo; }
 __device__ __forceinline__ uint32_t desc_k_lo(uint32_t start) { return (1u << 16) | (start >> 4); }
-__device__ __forceinline__ uint32_t desc_mn_lo(uint32_t start) {
-    return ((static_cast<uint32_t>(kBoxBytes) >> 4) << 16) | (start >> 4);
-}
-// D[128 x 128] = A B^T over `steps` * 16 of DP features, both tiles K-major.
-template <int DP>
+// D[128 x N] = A B^T over `steps` * 16 of DP features, both tiles K-major; A has 128 rows, B BN.
+template <int DP, int BN = kTile>
 __device__ __forceinline__ void mma_features(uint32_t d, uint32_t a, uint32_t b, int steps, uint32_t idesc) {
     const uint32_t la = desc_k_lo(a), lb = desc_k_lo(b);
 #pragma unroll
     for (int s = 0; s < DP / 16; ++s) {
-        const uint32_t off = (static_cast<uint32_t>(s >> 2) * kBoxBytes + static_cast<uint32_t>(s & 3) * 32) >> 4;
-        if (s < steps) ptx::umma_f16(d, desc_of(la + off), desc_of(lb + off), idesc, s > 0);
+        const uint32_t in = static_cast<uint32_t>(s & 3) * 32, box = static_cast<uint32_t>(s >> 2);
+        if (s < steps)
+            ptx::umma_f16(d, desc_of(la + ((box * kBoxBytes + in) >> 4)), desc_of(lb + ((box * BN * 128 + in) >> 4)), idesc,
+                          s > 0);
     }
 }
-// D[128 x N] (+)= A[tmem, 128 x 128] B over the 128 rows of tile b.  GAP: distance in TMEM between A's
-// first and second 64 K elements (32 columns when A is contiguous).
-template <int GAP, int FROM = 0, int TO = 8>
+// D[128 x N] (+)= A[tmem, 128 x BN] B over the BN rows of tile b, steps [FROM, TO) of 16.  A's K elements lie in
+// `HALVES` equal parts, GAP columns apart.
+template <int BN, int GAP, int HALVES, int FROM = 0, int TO = BN / 16>
 __device__ __forceinline__ void mma_rows(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool add) {
-    const uint32_t lb = desc_mn_lo(b);
+    constexpr int PER = BN / 16 / HALVES;
+    const uint32_t lb = ((static_cast<uint32_t>(BN) * 128 >> 4) << 16) | (b >> 4);   // LBO: the next 64 features
 #pragma unroll
     for (int s = FROM; s < TO; ++s)
-        umma_f16_ts(d, a + (s >> 2) * GAP + (s & 3) * 8, desc_of(lb + s * (2048 >> 4)), idesc, add || s > 0);
+        umma_f16_ts(d, a + (s / PER) * GAP + (s % PER) * 8, desc_of(lb + s * (2048 >> 4)), idesc, add || s > 0);
 }
 constexpr uint32_t kBMnMajor = 1u << 16;         // instruction descriptor: B is MN-major
 
-// Rows [valid, 128) of a tile as zeros (all lanes of one warp): a row of another sequence would turn a
+// Rows [valid, BN) of a tile as zeros (all lanes of one warp): a row of another sequence would turn a
 // weight of zero into NaN if it holds an infinity or NaN.
+template <int BN = kTile>
 __device__ __forceinline__ void zero_tail(uint8_t* tile, int boxes, int valid, int lane) {
     for (int b = 0; b < boxes; ++b)
-        for (int i = valid * 8 + lane; i < kTile * 8; i += 32)
-            *reinterpret_cast<uint4*>(tile + b * kBoxBytes + i * 16) = make_uint4(0, 0, 0, 0);
+        for (int i = valid * 8 + lane; i < BN * 8; i += 32)
+            *reinterpret_cast<uint4*>(tile + b * (BN * 128) + i * 16) = make_uint4(0, 0, 0, 0);
     ptx::fence_proxy_async_smem();
     __syncwarp();
 }
@@ -424,12 +426,12 @@ __global__ void __launch_bounds__(Fwd<DP, NQ>::THREADS, NQ == 2 ? 1 : 2)
                     // the product with the first half of the weights runs while the second is computed
                     if (!(ok = wait_warp(p_half(i), j & 1, ctl, p.timeout_ns))) break;
                     ptx::tc_fence_after();
-                    if (elect_one()) mma_rows<32, 0, 4>(t_o(i), t_p(i), ring32 + vs.s * F::TILE_BYTES, id_o, j > 0);
+                    if (elect_one()) mma_rows<kTile, 0, 1, 0, 4>(t_o(i), t_p(i), ring32 + vs.s * F::TILE_BYTES, id_o, j > 0);
                     __syncwarp();
                     if (!(ok = wait_warp(p_full(i), j & 1, ctl, p.timeout_ns))) break;
                     ptx::tc_fence_after();
                     if (elect_one()) {
-                        mma_rows<32, 4, 8>(t_o(i), t_p(i), ring32 + vs.s * F::TILE_BYTES, id_o, j > 0);
+                        mma_rows<kTile, 0, 1, 4, 8>(t_o(i), t_p(i), ring32 + vs.s * F::TILE_BYTES, id_o, j > 0);
                         ptx::umma_commit(o_full(i));
                     }
                     __syncwarp();
