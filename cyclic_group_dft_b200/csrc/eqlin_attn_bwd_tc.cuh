@@ -32,10 +32,9 @@ struct Bwd {
     static constexpr int STAGES = DP == 64 ? 8 : 5;
     static constexpr int TMEM_COLS = DP == 64 ? 256 : 512;
     static constexpr int BLOCKS = DP == 64 ? 2 : 1;
-    static constexpr uint32_t EX2_FMA = DP == 64 ? 0x44 : 0;   // as in the forward
     static constexpr int THREADS = 256 + 64;
     static constexpr int WARP_LOAD = 8, WARP_MMA = 9;
-    static constexpr size_t SMEM = static_cast<size_t>(2) * OWN_BYTES + STAGES * WALK_BYTES + 2 * BN * sizeof(float2) + 256;
+    static constexpr size_t SMEM = static_cast<size_t>(2) * OWN_BYTES + STAGES * WALK_BYTES + 4 * BN * sizeof(float) + 256;
     static_assert(SMEM <= 232448 / BLOCKS, "shared memory");
 };
 
@@ -78,8 +77,8 @@ __global__ void __launch_bounds__(Bwd<DP>::THREADS, Bwd<DP>::BLOCKS)
     const Params& p = bp.p;
     constexpr int BN = B::BN, HB = B::HB;
     extern __shared__ __align__(1024) uint8_t base[];
-    float2* rows = reinterpret_cast<float2*>(base + 2 * B::OWN_BYTES + ST * B::WALK_BYTES);   // [2][BN]: lse, delta
-    uint64_t* bars = reinterpret_cast<uint64_t*>(rows + 2 * BN);
+    float* rows = reinterpret_cast<float*>(base + 2 * B::OWN_BYTES + ST * B::WALK_BYTES);   // [2]: lse [BN], delta [BN]
+    uint64_t* bars = reinterpret_cast<uint64_t*>(rows + 4 * BN);
     Ctl* ctl = reinterpret_cast<Ctl*>(bars + 30);
     auto bar = [&](int i) { return ptx::smem_u32(bars + i); };
     auto full = [&](int s) { return bar(s); };
@@ -228,9 +227,9 @@ __global__ void __launch_bounds__(Bwd<DP>::THREADS, Bwd<DP>::BLOCKS)
         };
         float next = n > 0 ? fetch(0) : 0.f;
         for (int j = 0; j < n; ++j) {
-            float2* rj = rows + (j & 1) * BN;
+            float* rj = rows + (j & 1) * 2 * BN;
             // tile j - 2, which had this buffer, is read: dP of tile j - 1 was issued after all threads' dS of it
-            if ((tid & 127) < BN) reinterpret_cast<float*>(rj + (tid & 127))[half] = next;
+            if ((tid & 127) < BN) rj[half * BN + (tid & 127)] = next;
             arrive_warp(rows_full, lane);
             if (j + 1 < n) next = fetch(j + 1);
             if (!(ok = wait_warp(rows_full, j & 1, ctl, p.timeout_ns))) break;
@@ -256,14 +255,17 @@ __global__ void __launch_bounds__(Bwd<DP>::THREADS, Bwd<DP>::BLOCKS)
             for (int c = 0; c < HB / 32; ++c) {
                 uint32_t w[16];
 #pragma unroll
-                for (int e = 0; e < 32; e += 2) {
-                    const float4 ld = *reinterpret_cast<const float4*>(rj + half * HB + c * 32 + e);   // lse, delta, lse, delta
-                    const float2 a = ex2_pair<B::EX2_FMA>(
-                        fma2(make_float2(__uint_as_float(s[c][e]), __uint_as_float(s[c][e + 1])), make_float2(c2, c2),
-                             make_float2(-ld.x, -ld.z)), e >> 1);
-                    s[c][e] = __float_as_uint(a.x);
-                    s[c][e + 1] = __float_as_uint(a.y);
-                    w[e >> 1] = Io16<T>::pack(a.x, a.y);
+                for (int e = 0; e < 32; e += 4) {
+                    const float4 l = *reinterpret_cast<const float4*>(rj + half * HB + c * 32 + e);
+                    const float2 a = fma2(make_float2(__uint_as_float(s[c][e]), __uint_as_float(s[c][e + 1])),
+                                          make_float2(c2, c2), make_float2(-l.x, -l.y));
+                    const float2 b = fma2(make_float2(__uint_as_float(s[c][e + 2]), __uint_as_float(s[c][e + 3])),
+                                          make_float2(c2, c2), make_float2(-l.z, -l.w));
+                    const float v[4] = {ex2(a.x), ex2(a.y), ex2(b.x), ex2(b.y)};
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) s[c][e + k] = __float_as_uint(v[k]);
+                    w[e >> 1] = Io16<T>::pack(v[0], v[1]);
+                    w[(e >> 1) + 1] = Io16<T>::pack(v[2], v[3]);
                 }
                 tmem_st16(ts + c * 16, w);
             }
@@ -279,12 +281,16 @@ __global__ void __launch_bounds__(Bwd<DP>::THREADS, Bwd<DP>::BLOCKS)
                 ptx::tmem_wait_ld();
                 ptx::tmem_regs_ready(d);
 #pragma unroll
-                for (int e = 0; e < 32; e += 2) {
-                    const float4 ld = *reinterpret_cast<const float4*>(rj + half * HB + c * 32 + e);
+                for (int e = 0; e < 32; e += 4) {
+                    const float4 l = *reinterpret_cast<const float4*>(rj + BN + half * HB + c * 32 + e);
                     const float2 a = mul2(make_float2(__uint_as_float(s[c][e]), __uint_as_float(s[c][e + 1])),
                                           add2(make_float2(__uint_as_float(d[e]), __uint_as_float(d[e + 1])),
-                                               make_float2(-ld.y, -ld.w)));
+                                               make_float2(-l.x, -l.y)));
+                    const float2 b = mul2(make_float2(__uint_as_float(s[c][e + 2]), __uint_as_float(s[c][e + 3])),
+                                          add2(make_float2(__uint_as_float(d[e + 2]), __uint_as_float(d[e + 3])),
+                                               make_float2(-l.z, -l.w)));
                     w[e >> 1] = Io16<T>::pack(a.x, a.y);
+                    w[(e >> 1) + 1] = Io16<T>::pack(b.x, b.y);
                 }
                 // words over columns that this thread has read
                 tmem_st16(tdp + c * 16, w);
@@ -481,11 +487,10 @@ __global__ void __launch_bounds__(Bwd<DP>::THREADS, Bwd<DP>::BLOCKS)
             for (int c = 0; c < HB / 32; ++c)
 #pragma unroll
                 for (int e = 0; e < 32; e += 2) {
-                    const float2 a = ex2_pair<B::EX2_FMA>(
-                        fma2(make_float2(__uint_as_float(s[c][e]), __uint_as_float(s[c][e + 1])), make_float2(c2, c2),
-                             make_float2(off, off)), e >> 1);
-                    s[c][e] = __float_as_uint(a.x);
-                    s[c][e + 1] = __float_as_uint(a.y);
+                    const float2 a = fma2(make_float2(__uint_as_float(s[c][e]), __uint_as_float(s[c][e + 1])),
+                                          make_float2(c2, c2), make_float2(off, off));
+                    s[c][e] = __float_as_uint(ex2(a.x));
+                    s[c][e + 1] = __float_as_uint(ex2(a.y));
                 }
             if (!(ok = wait_warp(dp_full, j & 1, ctl, p.timeout_ns))) break;
             ptx::tc_fence_after();
