@@ -43,6 +43,30 @@ struct BwdParams {
     long long stop_after;    // test hook, as in FwdParams
 };
 
+// Position in the ring: one step of the order in which its tiles are loaded.
+template <int ST>
+struct RingAt {
+    int s = 0;
+    uint32_t ph = 0;
+    __device__ __forceinline__ void next() {
+        if (++s == ST) {
+            s = 0;
+            ph ^= 1;
+        }
+    }
+};
+// The walked query tiles in order: tiles [begin, end) of each head of a group.  Counted, not divided: the
+// divisions of a flat index cost more than the waits that they stood before.
+struct WalkAt {
+    int tile, head, begin, end;
+    __device__ __forceinline__ void next() {
+        if (++tile == end) {
+            tile = begin;
+            ++head;
+        }
+    }
+};
+
 // 128 rows x D features of an fp32 accumulator in TMEM, times `mul`, to the rows of an output.
 template <class T>
 __device__ __forceinline__ void store_accumulator(uint32_t taddr, bool filled, bool live, T* out, int D, float mul) {
@@ -139,14 +163,16 @@ __global__ void __launch_bounds__(Bwd<DP>::THREADS, Bwd<DP>::BLOCKS)
             ptx::mbar_arrive_expect_tx(fixed_full, 2 * B::OWN_BYTES);
             load(&mk, k_tile, kTile, hk, t.own.start + r0, fixed_full);
             load(&mv, v_tile, kTile, hk, t.own.start + r0, fixed_full);
+            RingAt<ST> at;
+            WalkAt w = {begin, hk * group, begin, begin + per_head};
             for (int u = 0; u < 2 * n; ++u) {      // Q_0, dO_0, Q_1, dO_1, ...
-                const int s = u % ST, it = u >> 1;
-                if (u >= ST && !wait_bounded(empty(s), ((u / ST) & 1) ^ 1, ctl, p.timeout_ns)) break;
+                if (u >= ST && !wait_bounded(empty(at.s), at.ph ^ 1, ctl, p.timeout_ns)) break;
                 if (issued == bp.stop_after) break;
-                ptx::mbar_arrive_expect_tx(full(s), B::WALK_BYTES);
-                load(u & 1 ? &mdo : &mq, ring + s * B::WALK_BYTES, BN, hk * group + it / per_head,
-                     qr.start + (begin + it % per_head) * BN, full(s));
+                ptx::mbar_arrive_expect_tx(full(at.s), B::WALK_BYTES);
+                load(u & 1 ? &mdo : &mq, ring + at.s * B::WALK_BYTES, BN, w.head, qr.start + w.tile * BN, full(at.s));
                 ++issued;
+                at.next();
+                if (u & 1) w.next();
             }
             drain_wait(fixed_full, 0, p.timeout_ns);
             for (int s = 0; s < ST; ++s) {
@@ -159,46 +185,53 @@ __global__ void __launch_bounds__(Bwd<DP>::THREADS, Bwd<DP>::BLOCKS)
             const uint32_t id_s = idesc_f16kind_f32(128, BN, Io16<T>::kUmmaFormat, false);
             const uint32_t id_o = idesc_f16kind_f32(128, (p.D + 15) / 16 * 16, Io16<T>::kUmmaFormat, false) | kBMnMajor;
             const int steps = (p.D + 15) / 16;
-            auto stage = [&](int u) { return ring + (u % ST) * B::WALK_BYTES; };
-            // a ring tile, with zeros for the rows past the sequence's end
-            auto take = [&](int u) {
-                if (!wait_warp(full(u % ST), (u / ST) & 1, ctl, p.timeout_ns)) return false;
-                const int valid = qr.len - (begin + (u >> 1) % per_head) * BN;
-                if (valid < BN) zero_tail<BN>(stage(u), B::BOXES, valid, lane);
-                return true;
+            const uint32_t ring32 = ptx::smem_u32(ring), k32 = ptx::smem_u32(k_tile), v32 = ptx::smem_u32(v_tile);
+            RingAt<ST> at;
+            WalkAt w = {begin, 0, begin, begin + per_head};
+            // the ring's next tile, with zeros for the rows past the sequence's end; its stage, or -1
+            auto take = [&](bool last_of_pair) {
+                if (!wait_warp(full(at.s), at.ph, ctl, p.timeout_ns)) return -1;
+                const int valid = qr.len - w.tile * BN;
+                if (valid < BN) zero_tail<BN>(ring + at.s * B::WALK_BYTES, B::BOXES, valid, lane);
+                const int s = at.s;
+                at.next();
+                if (last_of_pair) w.next();
+                return s;
             };
-            auto product = [&](uint32_t d, uint8_t* fixed, int u, uint32_t b) {
+            auto product = [&](uint32_t d, uint32_t fixed, int s, uint32_t b) {
                 if (elect_one()) {
-                    mma_features<DP, BN>(d, ptx::smem_u32(fixed), ptx::smem_u32(stage(u)), steps, id_s);
+                    mma_features<DP, BN>(d, fixed, ring32 + s * B::WALK_BYTES, steps, id_s);
                     ptx::umma_commit(b);
                 }
                 __syncwarp();
             };
-            bool ok = wait_warp(fixed_full, 0, ctl, p.timeout_ns) && take(0);
-            if (ok) product(t_s, k_tile, 0, s_full);
-            ok = ok && take(1);
-            if (ok) product(t_dp, v_tile, 1, dp_full);
+            int sq = -1, sdo = -1, sq_next = -1;
+            bool ok = wait_warp(fixed_full, 0, ctl, p.timeout_ns) && (sq = take(false)) >= 0;
+            if (ok) product(t_s, k32, sq, s_full);
+            ok = ok && (sdo = take(true)) >= 0;
+            if (ok) product(t_dp, v32, sdo, dp_full);
             for (int j = 0; ok && j < n; ++j) {
                 if (!(ok = wait_warp(p_full, j & 1, ctl, p.timeout_ns))) break;
                 ptx::tc_fence_after();
-                if (elect_one()) mma_rows<BN, HB, 2>(t_dv, t_s, ptx::smem_u32(stage(2 * j + 1)), id_o, j > 0);
+                if (elect_one()) mma_rows<BN, HB, 2>(t_dv, t_s, ring32 + sdo * B::WALK_BYTES, id_o, j > 0);
                 __syncwarp();
                 // MMAs of one thread run in order: S^T is written after P^T has been read out of it
                 if (j + 1 < n) {
-                    if (!(ok = take(2 * j + 2))) break;
-                    product(t_s, k_tile, 2 * j + 2, s_full);
+                    if (!(ok = (sq_next = take(false)) >= 0)) break;
+                    product(t_s, k32, sq_next, s_full);
                 }
                 if (!(ok = wait_warp(ds_full, j & 1, ctl, p.timeout_ns))) break;
                 ptx::tc_fence_after();
                 if (elect_one()) {
-                    mma_rows<BN, HB, 2>(t_dk, t_dp, ptx::smem_u32(stage(2 * j)), id_o, j > 0);
-                    ptx::umma_commit(empty((2 * j) % ST));
-                    ptx::umma_commit(empty((2 * j + 1) % ST));
+                    mma_rows<BN, HB, 2>(t_dk, t_dp, ring32 + sq * B::WALK_BYTES, id_o, j > 0);
+                    ptx::umma_commit(empty(sq));
+                    ptx::umma_commit(empty(sdo));
                 }
                 __syncwarp();
+                sq = sq_next;
                 if (j + 1 < n) {
-                    if (!(ok = take(2 * j + 3))) break;
-                    product(t_dp, v_tile, 2 * j + 3, dp_full);
+                    if (!(ok = (sdo = take(true)) >= 0)) break;
+                    product(t_dp, v32, sdo, dp_full);
                 }
             }
             if (elect_one()) {
@@ -215,23 +248,26 @@ __global__ void __launch_bounds__(Bwd<DP>::THREADS, Bwd<DP>::BLOCKS)
         const uint32_t ts = t_s + lanes + half * HB, tdp = t_dp + lanes + half * HB;
         const float c2 = p.scale * kLog2e;
         bool ok = true;
-        // lse (threads of the first warpgroup) or delta (second) of query tid & 127 of tile j; a row
-        // that sees no key, or is past the end, gets lse = +infinity: weights of zero
-        auto fetch = [&](int j) {
-            const int q = (begin + j % per_head) * BN + (tid & 127);
-            if ((tid & 127) >= BN || q >= qr.len) return half ? 0.f : INFINITY;
-            const long long at = static_cast<long long>(hk * group + j / per_head) * p.q_rows + qr.start + q;
-            if (half) return p.delta[at];
-            const float l = p.lse[at];
-            return l == -INFINITY ? INFINITY : l * kLog2e;
+        // lse (threads of the first warpgroup) or delta (second) of query tid & 127 of the next tile, as loaded:
+        // nothing waits for it before the tile after this one
+        const float* source = half ? p.delta : p.lse;
+        WalkAt fw = {begin, hk * group, begin, begin + per_head}, cw = fw;
+        auto fetch = [&] {
+            const int q = fw.tile * BN + (tid & 127);
+            float v = half ? 0.f : -INFINITY;
+            if ((tid & 127) < BN && q < qr.len) v = source[static_cast<long long>(fw.head) * p.q_rows + qr.start + q];
+            fw.next();
+            return v;
         };
-        float next = n > 0 ? fetch(0) : 0.f;
+        float next = n > 0 ? fetch() : 0.f;
         for (int j = 0; j < n; ++j) {
             float* rj = rows + (j & 1) * 2 * BN;
-            // tile j - 2, which had this buffer, is read: dP of tile j - 1 was issued after all threads' dS of it
-            if ((tid & 127) < BN) rj[half * BN + (tid & 127)] = next;
+            // tile j - 2, which had this buffer, is read: dP of tile j - 1 was issued after all threads' dS of it.
+            // A query that sees no key, or is past the end, gets lse = +infinity: weights of zero.
+            if ((tid & 127) < BN)
+                rj[half * BN + (tid & 127)] = half ? next : next == -INFINITY ? INFINITY : next * kLog2e;
             arrive_warp(rows_full, lane);
-            if (j + 1 < n) next = fetch(j + 1);
+            if (j + 1 < n) next = fetch();
             if (!(ok = wait_warp(rows_full, j & 1, ctl, p.timeout_ns))) break;
             if (!(ok = wait_warp(s_full, j & 1, ctl, p.timeout_ns))) break;
             ptx::tc_fence_after();
@@ -241,7 +277,8 @@ __global__ void __launch_bounds__(Bwd<DP>::THREADS, Bwd<DP>::BLOCKS)
             ptx::tmem_wait_ld();
 #pragma unroll
             for (int c = 0; c < HB / 32; ++c) ptx::tmem_regs_ready(s[c]);
-            const int q0 = (begin + j % per_head) * BN;
+            const int q0 = cw.tile * BN;
+            cw.next();
             if (p.causal && static_cast<long long>(r0) + kTile - 1 > static_cast<long long>(q0) + t.own.len - qr.len) {
                 // key `row` is seen by queries from row - (keys - queries) on
                 const long long first = static_cast<long long>(row) - (t.own.len - qr.len) - q0 - half * HB;
@@ -386,13 +423,14 @@ __global__ void __launch_bounds__(Bwd<DP>::THREADS, Bwd<DP>::BLOCKS)
             ptx::mbar_arrive_expect_tx(fixed_full, 2 * B::OWN_BYTES);
             load(&mq, q_tile, kTile, h, t.own.start + r0, fixed_full);
             load(&mdo, do_tile, kTile, h, t.own.start + r0, fixed_full);
+            RingAt<ST> at;
             for (int u = 0; u < 2 * n; ++u) {      // K_0, V_0, K_1, V_1, ...
-                const int s = u % ST;
-                if (u >= ST && !wait_bounded(empty(s), ((u / ST) & 1) ^ 1, ctl, p.timeout_ns)) break;
+                if (u >= ST && !wait_bounded(empty(at.s), at.ph ^ 1, ctl, p.timeout_ns)) break;
                 if (issued == bp.stop_after) break;
-                ptx::mbar_arrive_expect_tx(full(s), B::WALK_BYTES);
-                load(u & 1 ? &mv : &mk, ring + s * B::WALK_BYTES, BN, hk, kr.start + (u >> 1) * BN, full(s));
+                ptx::mbar_arrive_expect_tx(full(at.s), B::WALK_BYTES);
+                load(u & 1 ? &mv : &mk, ring + at.s * B::WALK_BYTES, BN, hk, kr.start + (u >> 1) * BN, full(at.s));
                 ++issued;
+                at.next();
             }
             drain_wait(fixed_full, 0, p.timeout_ns);
             for (int s = 0; s < ST; ++s) {
@@ -405,41 +443,49 @@ __global__ void __launch_bounds__(Bwd<DP>::THREADS, Bwd<DP>::BLOCKS)
             const uint32_t id_s = idesc_f16kind_f32(128, BN, Io16<T>::kUmmaFormat, false);
             const uint32_t id_o = idesc_f16kind_f32(128, (p.D + 15) / 16 * 16, Io16<T>::kUmmaFormat, false) | kBMnMajor;
             const int steps = (p.D + 15) / 16;
-            auto stage = [&](int u) { return ring + (u % ST) * B::WALK_BYTES; };
-            auto wait_stage = [&](int u) { return wait_warp(full(u % ST), (u / ST) & 1, ctl, p.timeout_ns); };
+            const uint32_t ring32 = ptx::smem_u32(ring), q32 = ptx::smem_u32(q_tile), do32 = ptx::smem_u32(do_tile);
+            // the ring positions of the next K (for the scores), V, and K (for dQ)
+            RingAt<ST> ks, vs, ks_dq;
+            vs.next();
             auto scores = [&](int j) {
-                if (!wait_stage(2 * j)) return false;
+                if (!wait_warp(full(ks.s), ks.ph, ctl, p.timeout_ns)) return false;
                 const int valid = kr.len - j * BN;
-                if (valid < BN) zero_tail<BN>(stage(2 * j), B::BOXES, valid, lane);
+                if (valid < BN) zero_tail<BN>(ring + ks.s * B::WALK_BYTES, B::BOXES, valid, lane);
                 if (elect_one()) {
-                    mma_features<DP, BN>(t_s(j), ptx::smem_u32(q_tile), ptx::smem_u32(stage(2 * j)), steps, id_s);
+                    mma_features<DP, BN>(t_s(j), q32, ring32 + ks.s * B::WALK_BYTES, steps, id_s);
                     ptx::umma_commit(s_full(j & 1));
                 }
                 __syncwarp();
+                ks.next();
+                ks.next();
                 return true;
             };
-            auto dp = [&](int j) {
-                if (!wait_stage(2 * j + 1)) return false;
+            auto dp = [&] {
+                if (!wait_warp(full(vs.s), vs.ph, ctl, p.timeout_ns)) return false;
                 if (elect_one()) {
-                    mma_features<DP, BN>(t_dp, ptx::smem_u32(do_tile), ptx::smem_u32(stage(2 * j + 1)), steps, id_s);
+                    mma_features<DP, BN>(t_dp, do32, ring32 + vs.s * B::WALK_BYTES, steps, id_s);
                     ptx::umma_commit(dp_full);
-                    ptx::umma_commit(empty((2 * j + 1) % ST));
+                    ptx::umma_commit(empty(vs.s));
                 }
                 __syncwarp();
+                vs.next();
+                vs.next();
                 return true;
             };
-            bool ok = wait_warp(fixed_full, 0, ctl, p.timeout_ns) && scores(0) && dp(0);
+            bool ok = wait_warp(fixed_full, 0, ctl, p.timeout_ns) && scores(0) && dp();
             if (ok && n > 1) ok = scores(1);
             for (int j = 0; ok && j < n; ++j) {
                 // dS_j lies over S_j, and dP_j has been read
                 if (!(ok = wait_warp(ds_full, j & 1, ctl, p.timeout_ns))) break;
                 ptx::tc_fence_after();
-                if (j + 1 < n && !(ok = dp(j + 1))) break;
+                if (j + 1 < n && !(ok = dp())) break;
                 if (elect_one()) {
-                    mma_rows<BN, HB, 2>(t_dq, t_s(j), ptx::smem_u32(stage(2 * j)), id_o, j > 0);
-                    ptx::umma_commit(empty((2 * j) % ST));
+                    mma_rows<BN, HB, 2>(t_dq, t_s(j), ring32 + ks_dq.s * B::WALK_BYTES, id_o, j > 0);
+                    ptx::umma_commit(empty(ks_dq.s));
                 }
                 __syncwarp();
+                ks_dq.next();
+                ks_dq.next();
                 // MMAs of one thread run in order: S_{j+2} is written after dS_j has been read
                 if (j + 2 < n) ok = scores(j + 2);
             }
