@@ -182,6 +182,17 @@ int forward_splits(const eqlin_attention_shape& a) {
     return static_cast<int>(std::max<int64_t>(1, std::min({room / std::max<int64_t>(units, 1), keys / 256, int64_t(64)})));
 }
 
+// The gradients of sequences of up to 64 rows on average use 16-row products.
+bool backward_short_rows(int64_t q_rows, int64_t k_rows, int64_t sequences) {
+    return std::max(q_rows, k_rows) <= 64 * sequences;
+}
+
+size_t backward_workspace(const eqlin_attention_shape& a) {
+    if (a.io_dtype == EQLIN_F32 || backward_short_rows(a.q_rows, a.k_rows, a.sequences))
+        return size_t(a.q_rows) * size_t(a.heads) * sizeof(float);
+    return size_t(a.q_rows / attn::tc::kTile + a.sequences) * size_t(a.heads) * 2 * attn::tc::kTile * sizeof(float);
+}
+
 size_t forward_workspace(const eqlin_attention_shape& a) {
     const int n = forward_splits(a);
     return n == 1 ? 0 : size_t(n) * size_t(a.heads) * size_t(a.q_rows) * size_t(a.head_dim + 1) * sizeof(float);
@@ -311,7 +322,8 @@ int backward_tc(const attn::tc::BwdParams& bp, int io, cudaStream_t st) {
     if (s != EQLIN_OK) return s;
     if (p.q_rows == 0) mq = mdo = mk;   // the side without rows is never read
     if (p.k_rows == 0) mk = mv = mq;
-    if (p.q_rows > 0) s = launch_delta<T>(p, st);
+    if (p.q_rows > 0)
+        s = launch(tc::eqlin_attn_stats_kernel<T>, dim3(grid_q), dim3(256), 0, st, "attention gradient launch", p);
     if (s == EQLIN_OK && p.k_rows > 0)
         s = launch(tc::eqlin_attn_dkv_tc_kernel<T, DP>, dim3(grid_k), dim3(B::THREADS), B::SMEM, st,
                    "attention gradient launch", mq, mk, mv, mdo, bp);
@@ -345,7 +357,7 @@ int backward_short(const attn::Params& p, cudaStream_t st) {
 
 template <class T>
 int backward_16(attn::Params& p, int io, cudaStream_t st) {
-    if (std::max(p.q_rows, p.k_rows) <= int64_t(64) * p.sequences)
+    if (backward_short_rows(p.q_rows, p.k_rows, p.sequences))
         return p.D <= 64 ? backward_short<T, 64>(p, st) : backward_short<T, 128>(p, st);
     p.timeout_ns = wait_timeout_ns();
     const attn::tc::BwdParams bp = {p, stop_after()};
@@ -360,7 +372,7 @@ int eqlin_attention_workspace_size(const eqlin_attention_shape* shape, int backw
     if (!bytes) return report(EQLIN_ERR_INVALID_ARG, "NULL argument");
     const int s = check_shape(shape);
     if (s != EQLIN_OK) return s;
-    *bytes = backward ? size_t(shape->q_rows) * size_t(shape->heads) * sizeof(float) : forward_workspace(*shape);
+    *bytes = backward ? backward_workspace(*shape) : forward_workspace(*shape);
     return EQLIN_OK;
 }
 

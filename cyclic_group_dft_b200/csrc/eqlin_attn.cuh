@@ -25,7 +25,7 @@ struct Params {
     const void *q, *k, *v, *o, *dout;
     void *out, *dq, *dk, *dv;      // out: the forward's o
     float* lse;                    // [heads][q_rows], or NULL
-    float* delta;                  // [heads][q_rows] (gradients)
+    float* delta;                  // gradients: delta [heads][q_rows], or the tensor-core kernels' statistics
     const int32_t *q_offsets, *k_offsets;   // [sequences + 1], or NULL: one sequence of all rows
     long long q_stride, k_stride, v_stride, o_stride, do_stride, dq_stride, dk_stride, dv_stride;
     int q_rows, k_rows, sequences, heads, kv_heads, D;

@@ -34,7 +34,9 @@ struct Bwd {
     static constexpr int BLOCKS = DP == 64 ? 2 : 1;
     static constexpr int THREADS = 256 + 64;
     static constexpr int WARP_LOAD = 8, WARP_MMA = 9;
-    static constexpr size_t SMEM = static_cast<size_t>(2) * OWN_BYTES + STAGES * WALK_BYTES + 4 * BN * sizeof(float) + 256;
+    static constexpr int ROW_BUFS = STAGES / 2;          // of lse and delta, which come with dO
+    static constexpr size_t SMEM =
+        static_cast<size_t>(2) * OWN_BYTES + STAGES * WALK_BYTES + ROW_BUFS * 2 * BN * sizeof(float) + 256;
     static_assert(SMEM <= 232448 / BLOCKS, "shared memory");
 };
 
@@ -90,6 +92,45 @@ __device__ __forceinline__ void store_accumulator(uint32_t taddr, bool filled, b
     }
 }
 
+// What the kernels below read of each query row: lse in units of log2 and delta = do . o, as
+// [head][slot][lse 128, delta 128] with the slots of find_tile<128>, so that a tile's values are one aligned piece.
+// A row that sees no key, or is past its sequence's end, gets lse = +infinity: weights of zero.  Both tensors are
+// read once; bound by memory.
+template <class T>
+__global__ void __launch_bounds__(256) eqlin_attn_stats_kernel(const Params p) {
+    using V = Vec<T, 8>;
+    ptx::grid_launch_dependents();
+    ptx::grid_dependency_wait();
+    const int h = blockIdx.x % p.heads, slot = blockIdx.x / p.heads, n_slots = gridDim.x / p.heads;
+    const Tile t = find_tile<kTile>(p.q_offsets, p.sequences, p.q_rows, slot);
+    if (t.tile < 0) return;
+    const int r0 = t.tile * kTile, n = min(kTile, t.own.len - r0);
+    const int lanes = p.D <= 64 ? 8 : 16;                // threads of a row
+    const int lane = threadIdx.x & (lanes - 1), rows = 256 / lanes;
+    const long long first = static_cast<long long>(t.own.start) + r0;
+    float* out = p.delta + (static_cast<long long>(h) * n_slots + slot) * 2 * kTile;
+    const bool in = lane * 8 < p.D;
+    const T* a = static_cast<const T*>(p.dout) + first * p.do_stride + static_cast<long long>(h) * p.D + lane * 8;
+    const T* b = static_cast<const T*>(p.o) + first * p.o_stride + static_cast<long long>(h) * p.D + lane * 8;
+#pragma unroll 4
+    for (int r = threadIdx.x / lanes; r < kTile; r += rows) {
+        float sum = 0.f;
+        if (in && r < n) {
+            float x[8], y[8];
+            V::unpack(V::load(a + r * p.do_stride), x);
+            V::unpack(V::load(b + r * p.o_stride), y);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) sum = fmaf(x[e], y[e], sum);
+        }
+        for (int o = lanes >> 1; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+        if (lane == 0) {
+            const float l = r < n ? p.lse[static_cast<long long>(h) * p.q_rows + first + r] : -INFINITY;
+            out[r] = l == -INFINITY ? INFINITY : l * kLog2e;
+            out[kTile + r] = sum;
+        }
+    }
+}
+
 // ------------------------------------------------------------------------------- dk and dv
 template <class T, int DP>
 __global__ void __launch_bounds__(Bwd<DP>::THREADS, Bwd<DP>::BLOCKS)
@@ -101,15 +142,14 @@ __global__ void __launch_bounds__(Bwd<DP>::THREADS, Bwd<DP>::BLOCKS)
     const Params& p = bp.p;
     constexpr int BN = B::BN, HB = B::HB;
     extern __shared__ __align__(1024) uint8_t base[];
-    float* rows = reinterpret_cast<float*>(base + 2 * B::OWN_BYTES + ST * B::WALK_BYTES);   // [2]: lse [BN], delta [BN]
-    uint64_t* bars = reinterpret_cast<uint64_t*>(rows + 4 * BN);
+    float* rows = reinterpret_cast<float*>(base + 2 * B::OWN_BYTES + ST * B::WALK_BYTES);   // buffers: lse [BN], delta [BN]
+    uint64_t* bars = reinterpret_cast<uint64_t*>(rows + B::ROW_BUFS * 2 * BN);
     Ctl* ctl = reinterpret_cast<Ctl*>(bars + 30);
     auto bar = [&](int i) { return ptx::smem_u32(bars + i); };
     auto full = [&](int s) { return bar(s); };
     auto empty = [&](int s) { return bar(ST + s); };
     const uint32_t fixed_full = bar(2 * ST), s_full = bar(2 * ST + 1), dp_full = bar(2 * ST + 2),
-                   p_full = bar(2 * ST + 3), ds_full = bar(2 * ST + 4), done = bar(2 * ST + 5),
-                   rows_full = bar(2 * ST + 6);
+                   p_full = bar(2 * ST + 3), ds_full = bar(2 * ST + 4), done = bar(2 * ST + 5);
     uint8_t *k_tile = base, *v_tile = base + B::OWN_BYTES, *ring = base + 2 * B::OWN_BYTES;
 
     if (ptx::smem_u32(base) & 1023u) {   // the swizzled tiles rely on the declared alignment
@@ -127,7 +167,6 @@ __global__ void __launch_bounds__(Bwd<DP>::THREADS, Bwd<DP>::BLOCKS)
         ptx::mbar_init(s_full, 1);
         ptx::mbar_init(dp_full, 1);
         ptx::mbar_init(p_full, 8);
-        ptx::mbar_init(rows_full, 8);
         ptx::mbar_init(ds_full, 8);
         ptx::mbar_init(done, 1);
         ptx::fence_mbar_init();
@@ -145,6 +184,9 @@ __global__ void __launch_bounds__(Bwd<DP>::THREADS, Bwd<DP>::BLOCKS)
     const int begin = t.tile < 0 ? 0 : first_query(r0, qr.len, t.own.len, p.causal) / BN;
     const int per_head = t.tile < 0 ? 0 : max(0, (qr.len + BN - 1) / BN - begin);
     const int n = per_head * group;
+    const long long q_slots = p.q_rows / kTile + p.sequences;
+    // slot of the sequence's first query tile (see find_tile)
+    const int q_slot = p.q_offsets ? qr.start / kTile + max(t.b, 0) : 0;
     ptx::tc_fence_before();
     __syncthreads();
     ptx::tc_fence_after();
@@ -168,8 +210,15 @@ __global__ void __launch_bounds__(Bwd<DP>::THREADS, Bwd<DP>::BLOCKS)
             for (int u = 0; u < 2 * n; ++u) {      // Q_0, dO_0, Q_1, dO_1, ...
                 if (u >= ST && !wait_bounded(empty(at.s), at.ph ^ 1, ctl, p.timeout_ns)) break;
                 if (issued == bp.stop_after) break;
-                ptx::mbar_arrive_expect_tx(full(at.s), B::WALK_BYTES);
+                ptx::mbar_arrive_expect_tx(full(at.s), B::WALK_BYTES + (u & 1 ? 2 * BN * 4 : 0));
                 load(u & 1 ? &mdo : &mq, ring + at.s * B::WALK_BYTES, BN, w.head, qr.start + w.tile * BN, full(at.s));
+                if (u & 1) {   // with dO: lse and delta of its rows
+                    const int row = w.tile * BN;
+                    const float* src = p.delta + (w.head * q_slots + q_slot + row / kTile) * 2 * kTile + row % kTile;
+                    const uint32_t dst = ptx::smem_u32(rows + ((u >> 1) % B::ROW_BUFS) * 2 * BN);
+                    ptx::bulk_load(dst, src, BN * 4, full(at.s));
+                    ptx::bulk_load(dst + BN * 4, src + kTile, BN * 4, full(at.s));
+                }
                 ++issued;
                 at.next();
                 if (u & 1) w.next();
@@ -248,27 +297,14 @@ __global__ void __launch_bounds__(Bwd<DP>::THREADS, Bwd<DP>::BLOCKS)
         const uint32_t ts = t_s + lanes + half * HB, tdp = t_dp + lanes + half * HB;
         const float c2 = p.scale * kLog2e;
         bool ok = true;
-        // lse (threads of the first warpgroup) or delta (second) of query tid & 127 of the next tile, as loaded:
-        // nothing waits for it before the tile after this one
-        const float* source = half ? p.delta : p.lse;
-        WalkAt fw = {begin, hk * group, begin, begin + per_head}, cw = fw;
-        auto fetch = [&] {
-            const int q = fw.tile * BN + (tid & 127);
-            float v = half ? 0.f : -INFINITY;
-            if ((tid & 127) < BN && q < qr.len) v = source[static_cast<long long>(fw.head) * p.q_rows + qr.start + q];
-            fw.next();
-            return v;
-        };
-        float next = n > 0 ? fetch() : 0.f;
+        WalkAt cw = {begin, 0, begin, begin + per_head};
+        RingAt<ST> at;
+        at.next();                                                 // dO_0
         for (int j = 0; j < n; ++j) {
-            float* rj = rows + (j & 1) * 2 * BN;
-            // tile j - 2, which had this buffer, is read: dP of tile j - 1 was issued after all threads' dS of it.
-            // A query that sees no key, or is past the end, gets lse = +infinity: weights of zero.
-            if ((tid & 127) < BN)
-                rj[half * BN + (tid & 127)] = half ? next : next == -INFINITY ? INFINITY : next * kLog2e;
-            arrive_warp(rows_full, lane);
-            if (j + 1 < n) next = fetch();
-            if (!(ok = wait_warp(rows_full, j & 1, ctl, p.timeout_ns))) break;
+            const float* rj = rows + (j % B::ROW_BUFS) * 2 * BN;
+            if (!(ok = wait_warp(full(at.s), at.ph, ctl, p.timeout_ns))) break;
+            at.next();
+            at.next();
             if (!(ok = wait_warp(s_full, j & 1, ctl, p.timeout_ns))) break;
             ptx::tc_fence_after();
             uint32_t s[HB / 32][32];
@@ -506,8 +542,9 @@ __global__ void __launch_bounds__(Bwd<DP>::THREADS, Bwd<DP>::BLOCKS)
         const long long at = static_cast<long long>(t.own.start) + row;
         float off = 0.f, delta = 0.f;
         if (live && seen > 0) {
-            off = -p.lse[static_cast<long long>(h) * p.q_rows + at] * kLog2e;
-            delta = p.delta[static_cast<long long>(h) * p.q_rows + at];
+            const float* stat = p.delta + (static_cast<long long>(h) * n_slots + slot) * 2 * kTile + (threadIdx.x & 127);
+            off = -stat[0];
+            delta = stat[kTile];
         }
         bool ok = true;
         for (int j = 0; j < n; ++j) {
