@@ -466,3 +466,33 @@ def test_transformer_block(dtype):
         assert err <= tol, (name, err, tol)
     qkv_layer.close()
     out_layer.close()
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("backward", [False, True])
+def test_attention_wait_timeout_is_reported_and_the_gpu_stays_usable(D, backward, monkeypatch):
+    """The load warp stops early (test hook, read on each call), so that the bounded waits of the other
+    warps run out: the kernel returns, the status word tells, and the next call is right."""
+    H, G, n = 2, 4, 700
+    q, k, v, do = (_randn(n, H * D // G, G, seed=i, dtype=torch.bfloat16).to(DEV) for i in range(4))
+    o, lse = eq.eqlin_attention_forward(q, k, v, heads=H)
+    want = (o, lse) + eq.eqlin_attention_backward(do, q, k, v, o, lse, heads=H)
+    assert eq.eqlin_attention_device_status() == eq.EQLIN_OK
+    monkeypatch.setenv("EQLIN_WAIT_TIMEOUT_MS", "100")
+    monkeypatch.setenv("EQLIN_TEST_STOP_AFTER", "3")
+    if backward:
+        eq.eqlin_attention_backward(do, q, k, v, o, lse, heads=H)
+    else:
+        eq.eqlin_attention_forward(q, k, v, heads=H)
+    assert eq.eqlin_attention_device_status() == eq.EQLIN_ERR_TIMEOUT
+    assert eq.eqlin_attention_device_status() == eq.EQLIN_OK         # reading the word clears it
+    monkeypatch.delenv("EQLIN_TEST_STOP_AFTER")
+    monkeypatch.delenv("EQLIN_WAIT_TIMEOUT_MS")
+    got = eq.eqlin_attention_forward(q, k, v, heads=H)
+    got += eq.eqlin_attention_backward(do, q, k, v, *got, heads=H)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert eq.eqlin_attention_device_status() == eq.EQLIN_OK
+
+
+def test_device_status_follows_the_device():
+    assert eq.eqlin_attention_device_status("cuda:0") == eq.EQLIN_OK
