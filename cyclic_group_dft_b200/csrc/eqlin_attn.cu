@@ -275,31 +275,24 @@ int launch_delta(const attn::Params& p, cudaStream_t st) {
 }
 
 template <int DP, int R>
-int dkv_f32(const attn::Params& p, cudaStream_t st) {
+int backward_f32_r(const attn::Params& p, cudaStream_t st) {
     using namespace attn::f32;
     using S = Shape<DP, R>;
-    return launch(eqlin_attn_dkv_f32_kernel<DP, R>, dim3(slots(p.k_rows, p.sequences, S::M), p.kv_heads), dim3(kThreads),
-                  S::DKV_BYTES, st, "attention gradient launch", p);
-}
-template <int DP, int R>
-int dq_f32(const attn::Params& p, cudaStream_t st) {
-    using namespace attn::f32;
-    using S = Shape<DP, R>;
-    return launch(eqlin_attn_dq_f32_kernel<DP, R>, dim3(slots(p.q_rows, p.sequences, S::M), p.heads), dim3(kThreads),
-                  S::DQ_BYTES, st, "attention gradient launch", p);
-}
-template <int DP>
-int backward_f32_d(const attn::Params& p, cudaStream_t st) {
+    unsigned k_blocks = 0, q_blocks = 0;
     int s = EQLIN_OK;
-    if (p.q_rows > 0) s = launch_delta<float>(p, st);
-    if (s == EQLIN_OK && p.k_rows > 0)
-        s = f32_small(p.k_rows, p.sequences, p.kv_heads) ? dkv_f32<DP, 1>(p, st) : dkv_f32<DP, 4>(p, st);
-    if (s == EQLIN_OK && p.q_rows > 0)
-        s = f32_small(p.q_rows, p.sequences, p.heads) ? dq_f32<DP, 1>(p, st) : dq_f32<DP, 4>(p, st);
-    return s;
+    if (p.k_rows > 0) s = tc_grid(p.k_rows, p.sequences, S::M, p.kv_heads, &k_blocks);
+    if (s == EQLIN_OK && p.q_rows > 0) s = tc_grid(p.q_rows, p.sequences, S::M, p.heads, &q_blocks);
+    if (s == EQLIN_OK && int64_t(k_blocks) + q_blocks >= (int64_t(1) << 31))
+        s = report(EQLIN_ERR_UNSUPPORTED, "too many rows, sequences and heads for one call");
+    if (s == EQLIN_OK && p.q_rows > 0) s = launch_delta<float>(p, st);
+    if (s != EQLIN_OK) return s;
+    return launch(eqlin_attn_bwd_f32_kernel<DP, R>, dim3(k_blocks + q_blocks), dim3(kThreads),
+                  std::max(S::DKV_BYTES, S::DQ_BYTES), st, "attention gradient launch", p, k_blocks);
 }
 int backward_f32(const attn::Params& p, cudaStream_t st) {
-    return p.D <= 64 ? backward_f32_d<64>(p, st) : backward_f32_d<128>(p, st);
+    const bool small = f32_small(std::max(p.q_rows, p.k_rows), p.sequences, p.heads);
+    if (p.D <= 64) return small ? backward_f32_r<64, 1>(p, st) : backward_f32_r<64, 4>(p, st);
+    return small ? backward_f32_r<128, 1>(p, st) : backward_f32_r<128, 4>(p, st);
 }
 
 template <class T, int DP>

@@ -230,16 +230,13 @@ __global__ void __launch_bounds__(kThreads) eqlin_attn_fwd_f32_kernel(const Para
 
 // dk and dv: a tile of keys walks the query rows that see it, for each query head of its group.
 template <int DP, int R>
-__global__ void __launch_bounds__(kThreads) eqlin_attn_dkv_f32_kernel(const Params p) {
-    extern __shared__ __align__(16) float smem[];
+__device__ __forceinline__ void dkv_tile(const Params& p, float* smem, int slot, int hk) {
     using S = Shape<DP, R>;
     constexpr int STAGE = 2 * S::WALK + 2 * kN;      // Q, dO, lse, delta
     float *sk = smem, *sv = sk + S::OWN, *walk = sv + S::OWN;
     float *sp = walk + S::STAGES * STAGE, *sds = sp + S::W;
-    ptx::grid_launch_dependents();
-    ptx::grid_dependency_wait();
-    const int hk = blockIdx.y, group = p.heads / p.kv_heads;
-    const Tile t = find_tile<S::M>(p.k_offsets, p.sequences, p.k_rows, blockIdx.x);
+    const int group = p.heads / p.kv_heads;
+    const Tile t = find_tile<S::M>(p.k_offsets, p.sequences, p.k_rows, slot);
     if (t.tile < 0) return;
     const Rows qr = sequence_rows(p.q_offsets, t.b, p.q_rows);
     const int r0 = t.tile * S::M, n = min(S::M, t.own.len - r0);
@@ -302,14 +299,11 @@ __global__ void __launch_bounds__(kThreads) eqlin_attn_dkv_f32_kernel(const Para
 
 // dq: a tile of queries walks the keys that it sees.
 template <int DP, int R>
-__global__ void __launch_bounds__(kThreads) eqlin_attn_dq_f32_kernel(const Params p) {
-    extern __shared__ __align__(16) float smem[];
+__device__ __forceinline__ void dq_tile(const Params& p, float* smem, int slot, int h) {
     using S = Shape<DP, R>;
     float *sq = smem, *sdo = sq + S::OWN, *walk = sdo + S::OWN, *sds = walk + S::STAGES * 2 * S::WALK;
-    ptx::grid_launch_dependents();
-    ptx::grid_dependency_wait();
-    const int h = blockIdx.y, hk = h / (p.heads / p.kv_heads);
-    const Tile t = find_tile<S::M>(p.q_offsets, p.sequences, p.q_rows, blockIdx.x);
+    const int hk = h / (p.heads / p.kv_heads);
+    const Tile t = find_tile<S::M>(p.q_offsets, p.sequences, p.q_rows, slot);
     if (t.tile < 0) return;
     const Rows kr = sequence_rows(p.k_offsets, t.b, p.k_rows);
     const int r0 = t.tile * S::M, n = min(S::M, t.own.len - r0);
@@ -360,6 +354,21 @@ __global__ void __launch_bounds__(kThreads) eqlin_attn_dq_f32_kernel(const Param
 #pragma unroll
     for (int i = 0; i < R; ++i) sc[i] = p.scale;
     store_rows<DP, R>(p.dq, p.dq_stride, static_cast<long long>(t.own.start) + r0, n, p.D, h, ty, tx, dq, sc);
+}
+
+// All gradients in one launch: the first k_blocks blocks take tiles of keys, the rest tiles of queries (heads
+// fastest).  Neither side waits for the other, and small problems fill more SMs.
+template <int DP, int R>
+__global__ void __launch_bounds__(kThreads) eqlin_attn_bwd_f32_kernel(const Params p, unsigned k_blocks) {
+    extern __shared__ __align__(16) float smem[];
+    ptx::grid_launch_dependents();
+    ptx::grid_dependency_wait();
+    if (blockIdx.x < k_blocks) {
+        dkv_tile<DP, R>(p, smem, blockIdx.x / p.kv_heads, blockIdx.x % p.kv_heads);
+    } else {
+        const unsigned b = blockIdx.x - k_blocks;
+        dq_tile<DP, R>(p, smem, b / p.heads, b % p.heads);
+    }
 }
 
 }  // namespace f32
