@@ -110,6 +110,11 @@ __device__ __forceinline__ Tile find_tile(const int32_t* offsets, int sequences,
     return t;
 }
 
+// The other side's rows of the tile's sequence; without a further read where both sides share their offsets.
+__device__ __forceinline__ Rows other_rows(const Params& p, const Tile& t, const int32_t* offsets, int rows) {
+    return p.k_offsets == p.q_offsets && p.k_rows == p.q_rows ? t.own : sequence_rows(offsets, t.b, rows);
+}
+
 // Keys [0, n) that query rows up to `last` (within the sequence) may see.
 __device__ __forceinline__ int keys_seen(int last, int q_len, int k_len, int causal) {
     if (!causal) return k_len;

@@ -158,6 +158,7 @@ __global__ void __launch_bounds__(Bwd<DP>::THREADS, Bwd<DP>::BLOCKS)
     }
     const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;   // (uniform)
     if (threadIdx.x == 0) {
+        for (const CUtensorMap* m : {&mq, &mk, &mv, &mdo}) ptx::prefetch_tmap(m);
         ctl->abort = 0;
         for (int s = 0; s < ST; ++s) {
             ptx::mbar_init(full(s), 1);
@@ -178,7 +179,7 @@ __global__ void __launch_bounds__(Bwd<DP>::THREADS, Bwd<DP>::BLOCKS)
     ptx::grid_dependency_wait();
     const int hk = blockIdx.x % p.kv_heads, slot = blockIdx.x / p.kv_heads, group = p.heads / p.kv_heads;
     const Tile t = find_tile<kTile>(p.k_offsets, p.sequences, p.k_rows, slot);
-    const Rows qr = sequence_rows(p.q_offsets, t.b, p.q_rows);
+    const Rows qr = other_rows(p, t, p.q_offsets, p.q_rows);
     const int r0 = t.tile * kTile;
     // query tiles: from the first that sees the first key of this tile
     const int begin = t.tile < 0 ? 0 : first_query(r0, qr.len, t.own.len, p.causal) / BN;
@@ -414,6 +415,7 @@ __global__ void __launch_bounds__(Bwd<DP>::THREADS, Bwd<DP>::BLOCKS)
     }
     const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;   // (uniform)
     if (threadIdx.x == 0) {
+        for (const CUtensorMap* m : {&mq, &mk, &mv, &mdo}) ptx::prefetch_tmap(m);
         ctl->abort = 0;
         for (int s = 0; s < ST; ++s) {
             ptx::mbar_init(full(s), 1);
@@ -436,7 +438,7 @@ __global__ void __launch_bounds__(Bwd<DP>::THREADS, Bwd<DP>::BLOCKS)
     const int n_slots = gridDim.x / p.heads;
     const int slot = p.causal ? n_slots - 1 - blockIdx.x / p.heads : blockIdx.x / p.heads;
     const Tile t = find_tile<kTile>(p.q_offsets, p.sequences, p.q_rows, slot);
-    const Rows kr = sequence_rows(p.k_offsets, t.b, p.k_rows);
+    const Rows kr = other_rows(p, t, p.k_offsets, p.k_rows);
     const int r0 = t.tile * kTile;
     const int n = t.tile < 0 ? 0
                              : (keys_seen(min(r0 + kTile, t.own.len) - 1, t.own.len, kr.len, p.causal) + BN - 1) / BN;

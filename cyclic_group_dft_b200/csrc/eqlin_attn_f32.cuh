@@ -147,7 +147,7 @@ __global__ void __launch_bounds__(kThreads) eqlin_attn_fwd_f32_kernel(const Para
     const int h = blockIdx.y, hk = h / (p.heads / p.kv_heads);
     const Tile t = find_tile<S::M>(p.q_offsets, p.sequences, p.q_rows, blockIdx.x);
     if (t.tile < 0) return;
-    const Rows kr = sequence_rows(p.k_offsets, t.b, p.k_rows);
+    const Rows kr = other_rows(p, t, p.k_offsets, p.k_rows);
     const int r0 = t.tile * S::M, n = min(S::M, t.own.len - r0);
     const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
     const int seen = keys_seen(r0 + n - 1, t.own.len, kr.len, p.causal);
@@ -238,7 +238,7 @@ __device__ __forceinline__ void dkv_tile(const Params& p, float* smem, int slot,
     const int group = p.heads / p.kv_heads;
     const Tile t = find_tile<S::M>(p.k_offsets, p.sequences, p.k_rows, slot);
     if (t.tile < 0) return;
-    const Rows qr = sequence_rows(p.q_offsets, t.b, p.q_rows);
+    const Rows qr = other_rows(p, t, p.q_offsets, p.q_rows);
     const int r0 = t.tile * S::M, n = min(S::M, t.own.len - r0);
     const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
     const int begin = first_query(r0, qr.len, t.own.len, p.causal) / kN;
@@ -305,7 +305,7 @@ __device__ __forceinline__ void dq_tile(const Params& p, float* smem, int slot, 
     const int hk = h / (p.heads / p.kv_heads);
     const Tile t = find_tile<S::M>(p.q_offsets, p.sequences, p.q_rows, slot);
     if (t.tile < 0) return;
-    const Rows kr = sequence_rows(p.k_offsets, t.b, p.k_rows);
+    const Rows kr = other_rows(p, t, p.k_offsets, p.k_rows);
     const int r0 = t.tile * S::M, n = min(S::M, t.own.len - r0);
     const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
     const int steps = (keys_seen(r0 + n - 1, t.own.len, kr.len, p.causal) + kN - 1) / kN;

@@ -40,12 +40,12 @@ __device__ __forceinline__ void ldm4t(uint32_t (&r)[4], uint32_t addr) {
 template <class T>
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     if constexpr (Io16<T>::kUmmaFormat == 1)
-        asm volatile(
+        asm(
             "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
             : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
             : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
     else
-        asm volatile(
+        asm(
             "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
             : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
             : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
@@ -86,17 +86,22 @@ template <class T, int DP, int NT>
 __device__ __forceinline__ void rows_by_rows(float (&acc)[NT][4], uint32_t a_tile, uint32_t b_tile, int steps,
                                              const Lane<DP>& at) {
     const uint32_t la = a_tile + at.a, lb = b_tile + at.b;
+    // the pieces of the next 16 features are on their way while these are multiplied
+    uint32_t a[2][4], b[2][NT / 2][4];
+    auto fetch = [&](int ks) {
+        ldm4(a[ks & 1], la ^ (ks << 5));
+#pragma unroll
+        for (int n = 0; n < NT / 2; ++n) ldm4(b[ks & 1][n], (lb ^ (ks << 5)) + n * 16 * (DP * 2));
+    };
+    fetch(0);
 #pragma unroll
     for (int ks = 0; ks < DP / 16; ++ks) {
         if (ks >= steps) break;
-        uint32_t a[4];
-        ldm4(a, la ^ (ks << 5));
+        if (ks + 1 < DP / 16) fetch(ks + 1);      // (past the head's features: zeros)
 #pragma unroll
-        for (int n = 0; n < NT; n += 2) {
-            uint32_t b[4];
-            ldm4(b, (lb ^ (ks << 5)) + n * 8 * (DP * 2));
-            mma16816<T>(acc[n], a, b[0], b[1]);
-            mma16816<T>(acc[n + 1], a, b[2], b[3]);
+        for (int n = 0; n < NT / 2; ++n) {
+            mma16816<T>(acc[2 * n], a[ks & 1], b[ks & 1][n][0], b[ks & 1][n][1]);
+            mma16816<T>(acc[2 * n + 1], a[ks & 1], b[ks & 1][n][2], b[ks & 1][n][3]);
         }
     }
 }
@@ -105,35 +110,42 @@ template <class T, int DP, int NT>
 __device__ __forceinline__ void weights_by_rows(float (&o)[DP / 8][4], const float (&w)[NT][4], uint32_t b_tile, int steps,
                                                 const Lane<DP>& at) {
     const uint32_t lb = b_tile + at.a;
+    constexpr int GROUP = 4;                      // pieces of 16 features in flight
 #pragma unroll
     for (int kb = 0; kb < NT / 2; ++kb) {
         const uint32_t a[4] = {Io16<T>::pack(w[2 * kb][0], w[2 * kb][1]), Io16<T>::pack(w[2 * kb][2], w[2 * kb][3]),
                                Io16<T>::pack(w[2 * kb + 1][0], w[2 * kb + 1][1]),
                                Io16<T>::pack(w[2 * kb + 1][2], w[2 * kb + 1][3])};
 #pragma unroll
-        for (int d = 0; d < DP / 16; ++d) {
-            if (d >= steps) break;
-            uint32_t b[4];
-            ldm4t(b, (lb ^ (d << 5)) + kb * 16 * (DP * 2));
-            mma16816<T>(o[2 * d], a, b[0], b[1]);
-            mma16816<T>(o[2 * d + 1], a, b[2], b[3]);
+        for (int d0 = 0; d0 < DP / 16; d0 += GROUP) {
+            if (d0 >= steps) break;
+            uint32_t b[GROUP][4];
+#pragma unroll
+            for (int d = 0; d < GROUP; ++d) ldm4t(b[d], (lb ^ ((d0 + d) << 5)) + kb * 16 * (DP * 2));
+#pragma unroll
+            for (int d = 0; d < GROUP; ++d) {
+                mma16816<T>(o[2 * (d0 + d)], a, b[d][0], b[d][1]);
+                mma16816<T>(o[2 * (d0 + d) + 1], a, b[d][2], b[d][3]);
+            }
         }
     }
 }
 
 // Running softmax of 16 rows x NT * 8 keys: masks keys >= last[i] (relative to this tile) of row i of
-// the pair where `masked`, turns s into weights, and past the `first` tile moves the maximum and scales o
+// the pair, which are all >= `masked` (the same for the warp), turns s into weights, and past the `first` tile moves the maximum and scales o
 // and sum.
 template <int NT, int DT>
 __device__ __forceinline__ void softmax_step(float (&s)[NT][4], float (&o)[DT][4], float (&top)[2], float (&sum)[2],
-                                             const int (&last)[2], bool masked, bool first, float c2, int lane) {
-    if (masked) {
+                                             const int (&last)[2], int masked, bool first, float c2, int lane) {
+    if (masked < NT * 8) {
         const int col0 = (lane & 3) * 2;
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+        for (int n = 0; n < NT; ++n) {
+            if (n * 8 + 8 <= masked) continue;
 #pragma unroll
             for (int e = 0; e < 4; ++e)
                 if (col0 + n * 8 + (e & 1) >= last[e >> 1]) s[n][e] = -INFINITY;
+        }
     }
     float fade[2];
 #pragma unroll
@@ -235,7 +247,7 @@ __global__ void __launch_bounds__(kShortThreads, DP == 128 ? 4 : 5) eqlin_attn_f
     const int h = (blockIdx.x % n_hb) * U + unit;
     const Tile t = find_tile<M>(p.q_offsets, p.sequences, p.q_rows, blockIdx.x / n_hb);
     if (t.tile < 0) return;
-    const Rows kr = p.k_offsets == p.q_offsets && p.k_rows == p.q_rows ? t.own : sequence_rows(p.k_offsets, t.b, p.k_rows);
+    const Rows kr = other_rows(p, t, p.k_offsets, p.k_rows);
     const int r0 = t.tile * M, n = min(M, t.own.len - r0);
     const int seen = keys_seen(r0 + n - 1, t.own.len, kr.len, p.causal);
     const bool on = h < p.heads;                            // the last block may have fewer heads
@@ -275,7 +287,7 @@ __global__ void __launch_bounds__(kShortThreads, DP == 128 ? 4 : 5) eqlin_attn_f
                 const int lim = p.causal ? r0 + row + 8 * i + 1 + kr.len - t.own.len - k0 : kn;
                 last[i] = min(lim, kn);
             }
-            softmax_step<NT, DP / 8>(s, o, top, sum, last, p.causal || kn < M, k0 == 0, c2, lane);
+            softmax_step<NT, DP / 8>(s, o, top, sum, last, p.causal ? 0 : kn, k0 == 0, c2, lane);
         }
         cp_async_wait<0>();
         __syncthreads();
@@ -317,7 +329,7 @@ __global__ void __launch_bounds__(kShortThreads, DP == 128 ? 3 : 4) eqlin_attn_d
     const int h = (blockIdx.x % n_hb) * U + unit;
     const Tile t = find_tile<M>(p.q_offsets, p.sequences, p.q_rows, blockIdx.x / n_hb);
     if (t.tile < 0) return;
-    const Rows kr = p.k_offsets == p.q_offsets && p.k_rows == p.q_rows ? t.own : sequence_rows(p.k_offsets, t.b, p.k_rows);
+    const Rows kr = other_rows(p, t, p.k_offsets, p.k_rows);
     const int r0 = t.tile * M, n = min(M, t.own.len - r0);
     const int seen = keys_seen(r0 + n - 1, t.own.len, kr.len, p.causal);
     const bool on = h < p.heads;
@@ -418,7 +430,7 @@ __global__ void __launch_bounds__(kShortThreads, DP == 128 ? 2 : 4) eqlin_attn_d
     const int hk = (blockIdx.x % n_hb) * U + unit;
     const Tile t = find_tile<M>(p.k_offsets, p.sequences, p.k_rows, blockIdx.x / n_hb);
     if (t.tile < 0) return;
-    const Rows qr = p.k_offsets == p.q_offsets && p.k_rows == p.q_rows ? t.own : sequence_rows(p.q_offsets, t.b, p.q_rows);
+    const Rows qr = other_rows(p, t, p.q_offsets, p.q_rows);
     const int r0 = t.tile * M, n = min(M, t.own.len - r0);
     const bool on = hk < p.kv_heads;
     const uint32_t sk = ptx::smem_u32(smem) + unit * (4 * M * DP * 2), sv = sk + M * DP * 2, sq = sv + M * DP * 2,
@@ -532,7 +544,7 @@ __global__ void __launch_bounds__(Few<DP>::WARPS * 32)
     const int hk = rest % p.kv_heads;
     const Tile t = find_tile<16>(p.q_offsets, p.sequences, p.q_rows, rest / p.kv_heads, group);
     if (t.tile < 0) return;
-    const Rows kr = sequence_rows(p.k_offsets, t.b, p.k_rows);
+    const Rows kr = other_rows(p, t, p.k_offsets, p.k_rows);
     const int r0 = t.tile * 16;                             // packed row
     const int n = min(16, t.own.len * group - r0);
     const int seen = keys_seen((r0 + n - 1) / group, t.own.len, kr.len, p.causal);
@@ -576,6 +588,7 @@ __global__ void __launch_bounds__(Few<DP>::WARPS * 32)
     int lim[2];                                             // keys that each row sees
 #pragma unroll
     for (int i = 0; i < 2; ++i) lim[i] = keys_seen((r0 + row + 8 * i) / group, t.own.len, kr.len, p.causal);
+    const int seen_all = keys_seen(r0 / group, t.own.len, kr.len, p.causal);   // by every row
     for (int u = 0; first + warp + u * F::WARPS < end; ++u) {
         cp_async_wait<F::STAGES - 2>();
         __syncwarp();
@@ -584,7 +597,7 @@ __global__ void __launch_bounds__(Few<DP>::WARPS * 32)
         float s[F::KEYS / 8][4] = {};
         rows_by_rows<T, DP, F::KEYS / 8>(s, sq, kt, steps, la);
         const int last[2] = {min(lim[0], kr.len) - k0, min(lim[1], kr.len) - k0};
-        softmax_step<F::KEYS / 8, DP / 8>(s, o, top, sum, last, min(last[0], last[1]) < F::KEYS, u == 0, c2, lane);
+        softmax_step<F::KEYS / 8, DP / 8>(s, o, top, sum, last, min(seen_all - k0, F::KEYS), u == 0, c2, lane);
         weights_by_rows<T, DP, F::KEYS / 8>(o, s, kt + F::STAGE_BYTES / 2, steps, la);
         __syncwarp();
         fetch(u + F::STAGES - 1);

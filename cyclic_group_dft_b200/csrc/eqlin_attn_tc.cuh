@@ -286,6 +286,9 @@ __global__ void __launch_bounds__(Fwd<DP, NQ>::THREADS, NQ == 2 ? 1 : 2)
 
     const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;   // (uniform)
     if (threadIdx.x == 0) {
+        ptx::prefetch_tmap(&mq);
+        ptx::prefetch_tmap(&mk);
+        ptx::prefetch_tmap(&mv);
         ctl->abort = 0;
         for (int s = 0; s < ST; ++s) {
             ptx::mbar_init(full(s), 1);
@@ -314,7 +317,7 @@ __global__ void __launch_bounds__(Fwd<DP, NQ>::THREADS, NQ == 2 ? 1 : 2)
     const int n_slots = gridDim.x / p.heads;
     const int slot = p.causal ? n_slots - 1 - blockIdx.x / p.heads : blockIdx.x / p.heads;
     const Tile t = find_tile<NQ * kTile>(p.q_offsets, p.sequences, p.q_rows, slot);
-    const Rows kr = sequence_rows(p.k_offsets, t.b, p.k_rows);
+    const Rows kr = other_rows(p, t, p.k_offsets, p.k_rows);
     const int r0 = t.tile * NQ * kTile;
     int count[NQ], n = 0;     // key tiles of each query tile
 #pragma unroll
