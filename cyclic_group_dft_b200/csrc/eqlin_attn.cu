@@ -117,6 +117,15 @@ int tc_grid(int64_t rows, int64_t sequences, int m, int64_t heads, unsigned* gri
     return EQLIN_OK;
 }
 
+// The same for the kernels of short sequences.
+template <int M>
+int short_grid(int64_t rows, int64_t sequences, int64_t head_blocks, unsigned* grid) {
+    const int64_t n = attn::mma::short_blocks<M>(rows, sequences) * head_blocks;
+    if (n >= (int64_t(1) << 31)) return report(EQLIN_ERR_UNSUPPORTED, "too many rows, sequences and heads for one call");
+    *grid = static_cast<unsigned>(n);
+    return EQLIN_OK;
+}
+
 // Limits of the bounded waits; EQLIN_WAIT_TIMEOUT_MS and the test hook EQLIN_TEST_STOP_AFTER (the load
 // warp stops after that many tiles, so that the waits run out) are read on each call.
 unsigned long long wait_timeout_ns() {
@@ -209,7 +218,7 @@ template <class T, int DP, int M>
 int forward_short_m(const attn::Params& p, cudaStream_t st) {
     constexpr int U = 64 / M;
     unsigned grid = 0;
-    const int s = tc_grid(p.q_rows, p.sequences, M, (p.heads + U - 1) / U, &grid);
+    const int s = short_grid<M>(p.q_rows, p.sequences, (p.heads + U - 1) / U, &grid);
     if (s != EQLIN_OK) return s;
     return launch(attn::mma::eqlin_attn_fwd_short_kernel<T, DP, M>, dim3(grid), dim3(attn::mma::kShortThreads),
                   attn::mma::short_smem<DP>(), st, "attention launch", p);
@@ -330,8 +339,8 @@ int backward_short_m(const attn::Params& p, cudaStream_t st) {
     namespace mma = attn::mma;
     constexpr int U = 64 / M;
     unsigned grid_q = 0, grid_k = 0;
-    int s = tc_grid(p.q_rows, p.sequences, M, (p.heads + U - 1) / U, &grid_q);
-    if (s == EQLIN_OK) s = tc_grid(p.k_rows, p.sequences, M, (p.kv_heads + U - 1) / U, &grid_k);
+    int s = short_grid<M>(p.q_rows, p.sequences, (p.heads + U - 1) / U, &grid_q);
+    if (s == EQLIN_OK) s = short_grid<M>(p.k_rows, p.sequences, (p.kv_heads + U - 1) / U, &grid_k);
     if (s == EQLIN_OK && p.q_rows > 0)
         s = launch(mma::eqlin_attn_dq_short_kernel<T, DP, M>, dim3(grid_q), dim3(mma::kShortThreads),
                    mma::short_bwd_smem<DP>(), st, "attention gradient launch", p);

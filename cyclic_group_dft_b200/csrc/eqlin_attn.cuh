@@ -61,7 +61,8 @@ struct Tile {
     int tile;    // tile within the sequence, or -1: none
     Rows own;    // the sequence's rows on this side
 };
-template <int M>
+// LATER: the slots of tiles 1, 2, .. alone (see for_short_tiles).
+template <int M, bool LATER = false>
 __device__ __forceinline__ Tile find_tile(const int32_t* offsets, int sequences, int rows, int slot, int mult = 1) {
     Tile t;
     if (!offsets) {
@@ -72,10 +73,10 @@ __device__ __forceinline__ Tile find_tile(const int32_t* offsets, int sequences,
     }
     auto offset = [&](int b) { return min(max(offsets[b], 0), rows); };
     auto first_slot = [&](int off, int b) {   // mult is 1, or the product with it is small (a few packed rows)
-        return static_cast<long long>(static_cast<unsigned long long>(off) * mult / M) + b;
+        return static_cast<long long>(static_cast<unsigned long long>(off) * mult / M) + (LATER ? 1 : b);
     };
     const int lane = threadIdx.x & 31;
-    const float slots = static_cast<float>(rows) * mult * (1.f / M) + sequences;
+    const float slots = static_cast<float>(rows) * mult * (1.f / M) + (LATER ? 1 : sequences);
     const int guess = static_cast<int>(__fdividef(static_cast<float>(slot) * sequences, slots));
     const int base = max(0, min(guess - 15, sequences - 31));
     const int probe = base + lane;
@@ -105,8 +106,8 @@ __device__ __forceinline__ Tile find_tile(const int32_t* offsets, int sequences,
         end = max(start, offset(lo + 1));
     }
     t.own = {start, end - start};
-    const long long tile = slot - first_slot(start, t.b);
-    t.tile = tile >= 0 && tile * M < static_cast<long long>(t.own.len) * mult ? static_cast<int>(tile) : -1;
+    const long long tile = slot - first_slot(start, t.b) + (LATER ? 1 : 0);
+    t.tile = tile >= (LATER ? 1 : 0) && tile * M < static_cast<long long>(t.own.len) * mult ? static_cast<int>(tile) : -1;
     return t;
 }
 

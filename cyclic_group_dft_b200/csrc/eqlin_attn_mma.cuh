@@ -181,6 +181,34 @@ __device__ __forceinline__ void softmax_step(float (&s)[NT][4], float (&o)[DT][4
 // a tile of 32 or 16 rows, so that short sequences fill the warps.  Each warp owns 16 query rows.  Keys
 // come in tiles of M.
 constexpr int kShortThreads = 128;
+
+// Most of these sequences have one tile, so the first tiles need no search: block b of the first `sequences` takes
+// tile 0 of sequence b.  The later tiles of longer sequences have slots by their rows: tile t of sequence b is
+// slot off[b] / M + t, one of rows / M that overlap nothing, and the blocks after the first ones look through
+// kLaterSlots of them each.
+constexpr int kLaterSlots = 8;
+template <int M>
+__host__ __device__ constexpr long long short_blocks(long long rows, long long sequences) {
+    return sequences + (rows / M + kLaterSlots - 1) / kLaterSlots;
+}
+template <int M, class F>
+__device__ __forceinline__ void for_short_tiles(const int32_t* offsets, int sequences, int rows, int block, F&& f) {
+    if (block < sequences) {
+        Tile t;
+        t.b = block;
+        t.own = sequence_rows(offsets, block, rows);
+        t.tile = 0;
+        if (t.own.len > 0) f(t);
+        return;
+    }
+    const int first = (block - sequences) * kLaterSlots + 1;
+    for (int slot = first; slot < first + kLaterSlots && slot <= rows / M; ++slot) {
+        const Tile t = find_tile<M, true>(offsets, sequences, rows, slot);
+        if (t.tile < 0) continue;
+        f(t);
+        __syncthreads();   // the next tile takes the same shared memory
+    }
+}
 template <int DP>
 constexpr size_t short_smem() {
     return size_t(3) * 64 * DP * 2;
@@ -236,17 +264,11 @@ __device__ __forceinline__ void store_rows(const float (&acc)[DP / 8][4], const 
 }
 
 template <class T, int DP, int M>
-__global__ void __launch_bounds__(kShortThreads, DP == 128 ? 4 : 5) eqlin_attn_fwd_short_kernel(const Params p) {
+__device__ __forceinline__ void fwd_short_tile(const Params& p, uint8_t* smem, int head_block, const Tile& t) {
     constexpr int U = 64 / M, WU = 4 / U, NT = M / 8;      // heads of a block, warps of a head
-    extern __shared__ __align__(1024) uint8_t smem[];
-    ptx::grid_launch_dependents();
-    ptx::grid_dependency_wait();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int n_hb = (p.heads + U - 1) / U;
     const int unit = warp / WU, rw = warp % WU;
-    const int h = (blockIdx.x % n_hb) * U + unit;
-    const Tile t = find_tile<M>(p.q_offsets, p.sequences, p.q_rows, blockIdx.x / n_hb);
-    if (t.tile < 0) return;
+    const int h = (head_block) * U + unit;
     const Rows kr = other_rows(p, t, p.k_offsets, p.k_rows);
     const int r0 = t.tile * M, n = min(M, t.own.len - r0);
     const int seen = keys_seen(r0 + n - 1, t.own.len, kr.len, p.causal);
@@ -309,6 +331,16 @@ __global__ void __launch_bounds__(kShortThreads, DP == 128 ? 4 : 5) eqlin_attn_f
                       static_cast<T*>(p.out) + (static_cast<long long>(t.own.start) + r0) * p.o_stride +
                           static_cast<long long>(h) * p.D, p.o_stride, lane);
 }
+template <class T, int DP, int M>
+__global__ void __launch_bounds__(kShortThreads, DP == 128 ? 4 : 5) eqlin_attn_fwd_short_kernel(const Params p) {
+    extern __shared__ __align__(1024) uint8_t smem[];
+    ptx::grid_launch_dependents();
+    ptx::grid_dependency_wait();
+    constexpr int U = 64 / M;
+    const int n_hb = (p.heads + U - 1) / U;
+    for_short_tiles<M>(p.q_offsets, p.sequences, p.q_rows, blockIdx.x / n_hb,
+                       [&](const Tile& t) { fwd_short_tile<T, DP, M>(p, smem, blockIdx.x % n_hb, t); });
+}
 
 // Gradients of short sequences: the forward's tiles, with four of them (Q, dO, K, V) in shared memory.
 template <int DP>
@@ -318,17 +350,11 @@ constexpr size_t short_bwd_smem() {
 
 // dq, and delta = do . o of its rows, which the kernel for dk and dv (launched next) reads.
 template <class T, int DP, int M>
-__global__ void __launch_bounds__(kShortThreads, DP == 128 ? 3 : 4) eqlin_attn_dq_short_kernel(const Params p) {
+__device__ __forceinline__ void dq_short_tile(const Params& p, uint8_t* smem, int head_block, const Tile& t) {
     constexpr int U = 64 / M, WU = 4 / U, NT = M / 8;
-    extern __shared__ __align__(1024) uint8_t smem[];
-    ptx::grid_launch_dependents();
-    ptx::grid_dependency_wait();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int n_hb = (p.heads + U - 1) / U;
     const int unit = warp / WU, rw = warp % WU;
-    const int h = (blockIdx.x % n_hb) * U + unit;
-    const Tile t = find_tile<M>(p.q_offsets, p.sequences, p.q_rows, blockIdx.x / n_hb);
-    if (t.tile < 0) return;
+    const int h = (head_block) * U + unit;
     const Rows kr = other_rows(p, t, p.k_offsets, p.k_rows);
     const int r0 = t.tile * M, n = min(M, t.own.len - r0);
     const int seen = keys_seen(r0 + n - 1, t.own.len, kr.len, p.causal);
@@ -416,20 +442,25 @@ __global__ void __launch_bounds__(kShortThreads, DP == 128 ? 3 : 4) eqlin_attn_d
     store_rows<T, DP>(dq, mul, sq, rw * 16, n, p.D,
                       static_cast<T*>(p.dq) + first_row * p.dq_stride + static_cast<long long>(h) * p.D, p.dq_stride, lane);
 }
-
-// dk and dv: a warp owns 16 keys; the query rows that see the tile pass by, for each head of the group.
 template <class T, int DP, int M>
-__global__ void __launch_bounds__(kShortThreads, DP == 128 ? 2 : 4) eqlin_attn_dkv_short_kernel(const Params p) {
-    constexpr int U = 64 / M, WU = 4 / U, NT = (M < 32 ? M : 32) / 8;   // queries in steps of 32 (or M) columns
+__global__ void __launch_bounds__(kShortThreads, DP == 128 ? 3 : 4) eqlin_attn_dq_short_kernel(const Params p) {
     extern __shared__ __align__(1024) uint8_t smem[];
     ptx::grid_launch_dependents();
     ptx::grid_dependency_wait();
+    constexpr int U = 64 / M;
+    const int n_hb = (p.heads + U - 1) / U;
+    for_short_tiles<M>(p.q_offsets, p.sequences, p.q_rows, blockIdx.x / n_hb,
+                       [&](const Tile& t) { dq_short_tile<T, DP, M>(p, smem, blockIdx.x % n_hb, t); });
+}
+
+// dk and dv: a warp owns 16 keys; the query rows that see the tile pass by, for each head of the group.
+template <class T, int DP, int M>
+__device__ __forceinline__ void dkv_short_tile(const Params& p, uint8_t* smem, int head_block, const Tile& t) {
+    constexpr int U = 64 / M, WU = 4 / U, NT = (M < 32 ? M : 32) / 8;   // queries in steps of 32 (or M) columns
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int n_hb = (p.kv_heads + U - 1) / U, group = p.heads / p.kv_heads;
+    const int group = p.heads / p.kv_heads;
     const int unit = warp / WU, rw = warp % WU;
-    const int hk = (blockIdx.x % n_hb) * U + unit;
-    const Tile t = find_tile<M>(p.k_offsets, p.sequences, p.k_rows, blockIdx.x / n_hb);
-    if (t.tile < 0) return;
+    const int hk = (head_block) * U + unit;
     const Rows qr = other_rows(p, t, p.q_offsets, p.q_rows);
     const int r0 = t.tile * M, n = min(M, t.own.len - r0);
     const bool on = hk < p.kv_heads;
@@ -507,6 +538,16 @@ __global__ void __launch_bounds__(kShortThreads, DP == 128 ? 2 : 4) eqlin_attn_d
     const long long col = static_cast<long long>(hk) * p.D;
     store_rows<T, DP>(dk, mul, sk, rw * 16, n, p.D, static_cast<T*>(p.dk) + first_row * p.dk_stride + col, p.dk_stride, lane);
     store_rows<T, DP>(dv, one, sv, rw * 16, n, p.D, static_cast<T*>(p.dv) + first_row * p.dv_stride + col, p.dv_stride, lane);
+}
+template <class T, int DP, int M>
+__global__ void __launch_bounds__(kShortThreads, DP == 128 ? 2 : 4) eqlin_attn_dkv_short_kernel(const Params p) {
+    extern __shared__ __align__(1024) uint8_t smem[];
+    ptx::grid_launch_dependents();
+    ptx::grid_dependency_wait();
+    constexpr int U = 64 / M;
+    const int n_hb = (p.kv_heads + U - 1) / U;
+    for_short_tiles<M>(p.k_offsets, p.sequences, p.k_rows, blockIdx.x / n_hb,
+                       [&](const Tile& t) { dkv_short_tile<T, DP, M>(p, smem, blockIdx.x % n_hb, t); });
 }
 
 // ------------------------------------------------------------------- few queries over many keys
