@@ -1,15 +1,17 @@
 """ctypes binding of the handle-free operators of libeqlin.so (C ABI in include/eqlin.h):
 attention over packed sequences, residual addition with root-mean-square norm, and rotary
 positions.  Argument marshalling only, as in ``_capi``: torch supplies memory and streams.
+Every function of tensors takes the keyword ``stream`` as well (see ``_in_stream``).
 """
 from __future__ import annotations
 
 import ctypes
+import functools
 
 import torch
 
 from . import _capi
-from ._capi import _TORCH_TO_EQLIN, _check, _lib, _stream_ptr
+from ._capi import _TORCH_TO_EQLIN, _check, _lib
 
 _vp, _i64, _int, _f32, _sz = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
 
@@ -18,6 +20,9 @@ class _AttentionShape(ctypes.Structure):
     _fields_ = [("q_rows", _i64), ("k_rows", _i64), ("sequences", _i64), ("heads", _i64), ("kv_heads", _i64),
                 ("head_dim", _i64), ("q_offsets", _vp), ("k_offsets", _vp), ("q_stride", _i64), ("k_stride", _i64),
                 ("v_stride", _i64), ("o_stride", _i64), ("io_dtype", _int), ("causal", _int), ("scale", _f32)]
+
+
+_Sections = ctypes.c_int32 * 4   # pairs of each rotary axis
 
 
 class _GradStrides(ctypes.Structure):
@@ -46,16 +51,36 @@ _current_device = torch._C._cuda_getDevice
 _current_stream = torch._C._cuda_getCurrentRawStream
 
 
-def _run(name: str, device: int, stream, *args) -> None:
-    """Calls library function `name` with `args` and the stream, with device number `device` current."""
+def _run(name: str, device: int, *args) -> None:
+    """Calls library function `name` with `args` and the current stream, with device number `device` current."""
     f = getattr(_lib, name)
     if _current_device() == device:
-        status = f(*args, _current_stream(device) if stream is None else _stream_ptr(stream))
+        status = f(*args, _current_stream(device))
     else:
         with torch.cuda.device(device):
-            status = f(*args, _stream_ptr(stream))
+            status = f(*args, _current_stream(device))
     if status:
         _check(status, name)
+
+
+def _in_stream(f):
+    """Gives a function its keyword `stream` (a torch Stream or a cudaStream_t as a number; default: the current
+    stream): the whole call, its allocations among it, is made with that stream current.  What it allocates
+    then belongs to that stream, and a workspace that is given up on return is not reused before the kernels
+    are done with it."""
+
+    @functools.wraps(f)
+    def call(*args, stream=None, **kwargs):
+        if stream is None:
+            return f(*args, **kwargs)
+        if not isinstance(stream, torch.cuda.Stream):
+            device = (args[0] if args else next(iter(kwargs.values()))).device
+            stream = torch.cuda.ExternalStream(int(stream), device=device) if int(stream) else \
+                torch.cuda.default_stream(device)
+        with torch.cuda.stream(stream):
+            return f(*args, **kwargs)
+
+    return call
 
 
 # These checks run on every call, whose kernels may take a few microseconds: each asks a tensor for as little as
@@ -116,9 +141,9 @@ def _w_code(weight: torch.Tensor | None) -> int:
     return _capi.EQLIN_F32 if weight is None else _TORCH_TO_EQLIN[weight.dtype]
 
 
+@_in_stream
 def eqlin_add_rmsnorm(x: torch.Tensor, residual: torch.Tensor | None = None, weight: torch.Tensor | None = None,
-                      eps: float = 1e-6, y: torch.Tensor | None = None, sum_out: torch.Tensor | None = None,
-                      stream=None) -> tuple[torch.Tensor, torch.Tensor]:
+                      eps: float = 1e-6, y: torch.Tensor | None = None, sum_out: torch.Tensor | None = None) -> tuple[torch.Tensor, torch.Tensor]:
     """(y, r) with r = x + residual and y = r * weight[c] / sqrt(mean(r^2) + eps) over the
     channels and group elements of a token; x, residual, y and r are [N, C, G], weight [C] or
     None (ones).  Without a residual r is x itself, unless sum_out is given.  y and sum_out may
@@ -133,15 +158,15 @@ def eqlin_add_rmsnorm(x: torch.Tensor, residual: torch.Tensor | None = None, wei
         sum_out = torch.empty_like(x)
     if sum_out is not None and N > 0 and sum_out.data_ptr() == y.data_ptr():
         raise ValueError("y and sum_out must not be the same tensor")
-    _run("eqlin_add_rmsnorm", device, stream, x.data_ptr(), _ptr(residual), _ptr(weight), y.data_ptr(), _ptr(sum_out),
+    _run("eqlin_add_rmsnorm", device, x.data_ptr(), _ptr(residual), _ptr(weight), y.data_ptr(), _ptr(sum_out),
          N, C, G, eps, _w_code(weight), _TORCH_TO_EQLIN[dtype])
     return y, (x if sum_out is None else sum_out)
 
 
+@_in_stream
 def eqlin_add_rmsnorm_fp8(x: torch.Tensor, residual: torch.Tensor | None = None, weight: torch.Tensor | None = None,
                           eps: float = 1e-6, y: torch.Tensor | None = None, scale: torch.Tensor | None = None,
-                          sum_out: torch.Tensor | None = None,
-                          stream=None) -> tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+                          sum_out: torch.Tensor | None = None) -> tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
     """(y8, scale, r): eqlin_add_rmsnorm with y as float8_e4m3fn and one fp32 scale per token,
     y = y8 * scale[:, None, None], scale = max|y| / 448 (1 for a row of zeros)."""
     shape, dtype, device = _norm_args(x, residual, weight, sum_out)
@@ -156,7 +181,7 @@ def eqlin_add_rmsnorm_fp8(x: torch.Tensor, residual: torch.Tensor | None = None,
         _like(scale, "scale", (N,), torch.float32, device)
     if sum_out is None and residual is not None:
         sum_out = torch.empty_like(x)
-    _run("eqlin_add_rmsnorm_fp8", device, stream, x.data_ptr(), _ptr(residual), _ptr(weight), y.data_ptr(),
+    _run("eqlin_add_rmsnorm_fp8", device, x.data_ptr(), _ptr(residual), _ptr(weight), y.data_ptr(),
          scale.data_ptr(), _ptr(sum_out), N, C, G, eps, _w_code(weight), _TORCH_TO_EQLIN[dtype])
     return y, scale, (x if sum_out is None else sum_out)
 
@@ -168,11 +193,11 @@ def eqlin_rmsnorm_backward_workspace_size(N: int, C: int, G: int, io_dtype=torch
     return int(v.value)
 
 
+@_in_stream
 def eqlin_rmsnorm_backward(dy: torch.Tensor, r: torch.Tensor, weight: torch.Tensor | None = None,
                            dsum: torch.Tensor | None = None, eps: float = 1e-6, with_weight: bool = True,
                            dx: torch.Tensor | None = None, dweight: torch.Tensor | None = None,
-                           workspace: torch.Tensor | None = None,
-                           stream=None) -> tuple[torch.Tensor, torch.Tensor | None]:
+                           workspace: torch.Tensor | None = None) -> tuple[torch.Tensor, torch.Tensor | None]:
     """(dx [N, C, G], dweight [C] fp32 or None) from dy and the stored sum r of
     eqlin_add_rmsnorm; dx is the gradient of x and of the residual alike and includes dsum, the
     gradient that reaches r through the residual stream.  The workspace (a uint8 CUDA tensor) is
@@ -197,7 +222,7 @@ def eqlin_rmsnorm_backward(dy: torch.Tensor, r: torch.Tensor, weight: torch.Tens
     if dweight is not None and workspace is None:
         need = eqlin_rmsnorm_backward_workspace_size(N, C, G, dtype)
         workspace = torch.empty((max(need, 16),), dtype=torch.uint8, device=r.device)
-    _run("eqlin_rmsnorm_backward", device, stream, dy.data_ptr(), r.data_ptr(), _ptr(weight), _ptr(dsum), dx.data_ptr(),
+    _run("eqlin_rmsnorm_backward", device, dy.data_ptr(), r.data_ptr(), _ptr(weight), _ptr(dsum), dx.data_ptr(),
          _ptr(dweight), N, C, G, eps, _w_code(weight), _TORCH_TO_EQLIN[dtype], _ptr(workspace), _workspace(workspace, device))
     return dx, dweight
 
@@ -211,28 +236,28 @@ def _workspace(workspace: torch.Tensor | None, device: int) -> int:
     return workspace.numel()
 
 
+@_in_stream
 def eqlin_rope(x: torch.Tensor, positions: torch.Tensor, heads: int, sections, base: float = 10000.0,
-               inverse: bool = False, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+               inverse: bool = False, out: torch.Tensor | None = None) -> torch.Tensor:
     """Rotary positions with several axes on x [N, heads * Dh, G] (a channel slice of a wider
     tensor will do): channel pair (c, c + Dh/2) of each head turns by positions[n, axis] *
     base^(-j / sections[axis]).  positions is [N, axes] int32; the sections add up to Dh/2.
     inverse turns back, which is also the gradient.  out may be x (in place)."""
     shape, dtype, device = _features(x, "x"), x.dtype, x.get_device()
     N, C, G = shape
-    sections = [int(n) for n in sections]
+    axes = len(sections)
     if heads < 1 or C % heads:
         raise ValueError(f"{C} channels are not {heads} heads")
-    _like(positions, "positions", (N, len(sections)), torch.int32, device)
-    if any(n < 0 or n > C for n in sections):
-        raise ValueError("the sections must be counts that add up to half the channels of a head")
+    if not 1 <= axes <= 4 or min(sections) < 0 or 2 * heads * sum(sections) != C:
+        raise ValueError("the sections must be 1 to 4 counts that add up to half the channels of a head")
+    _like(positions, "positions", (N, axes), torch.int32, device)
     xs = _rows(x, "x", shape, dtype, device)
     if out is None:
         out, ys = torch.empty(shape, dtype=dtype, device=x.device), C * G
     else:
         ys = _rows(out, "out", shape, dtype, device)
-    table = (ctypes.c_int32 * max(len(sections), 1))(*sections)
-    _run("eqlin_rope", device, stream, x.data_ptr(), positions.data_ptr(), out.data_ptr(), N, heads, C // heads, G, table,
-         len(sections), base, xs, ys, int(bool(inverse)), _TORCH_TO_EQLIN[dtype])
+    _run("eqlin_rope", device, x.data_ptr(), positions.data_ptr(), out.data_ptr(), N, heads, C // heads, G,
+         _Sections(*sections), axes, base, xs, ys, int(bool(inverse)), _TORCH_TO_EQLIN[dtype])
     return out
 
 
@@ -275,12 +300,12 @@ def _attention_workspace(shape: _AttentionShape, backward: int, workspace, ref: 
     return workspace
 
 
+@_in_stream
 def eqlin_attention_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, heads: int,
                             kv_heads: int | None = None, q_offsets: torch.Tensor | None = None,
                             k_offsets: torch.Tensor | None = None, causal: bool = False, scale: float | None = None,
                             o: torch.Tensor | None = None, lse: torch.Tensor | None = None,
-                            workspace: torch.Tensor | None = None,
-                            stream=None) -> tuple[torch.Tensor, torch.Tensor]:
+                            workspace: torch.Tensor | None = None) -> tuple[torch.Tensor, torch.Tensor]:
     """(o [Nq, heads * Dh, G], lse [heads, Nq] fp32) of attention over packed sequences.
 
     q is [Nq, heads * Dh, G], k and v are [Nk, kv_heads * Dh, G] (channel slices of a joint
@@ -298,18 +323,18 @@ def eqlin_attention_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, h
     else:
         _like(lse, "lse", (heads, q_shape[0]), torch.float32, device)
     workspace = _attention_workspace(shape, 0, workspace, q)
-    _run("eqlin_attention_forward", device, stream, ctypes.byref(shape), q.data_ptr(), k.data_ptr(), v.data_ptr(),
+    _run("eqlin_attention_forward", device, ctypes.byref(shape), q.data_ptr(), k.data_ptr(), v.data_ptr(),
          o.data_ptr(), lse.data_ptr(), _ptr(workspace), _workspace(workspace, device))
     return o, lse
 
 
+@_in_stream
 def eqlin_attention_backward(do: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: torch.Tensor,
                              lse: torch.Tensor, heads: int, kv_heads: int | None = None,
                              q_offsets: torch.Tensor | None = None, k_offsets: torch.Tensor | None = None,
                              causal: bool = False, scale: float | None = None,
                              grads: tuple[torch.Tensor, torch.Tensor, torch.Tensor] | None = None,
-                             workspace: torch.Tensor | None = None,
-                             stream=None) -> tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+                             workspace: torch.Tensor | None = None) -> tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
     """(dq, dk, dv) from do = dL/do and the forward's inputs, o and lse.  grads gives the three
     outputs (channel slices of one joint gradient will do); they are allocated when not given."""
     shape, q_shape, k_shape, dtype, device = _attention_shape(q, k, v, heads, kv_heads, q_offsets, k_offsets, causal,
@@ -323,7 +348,7 @@ def eqlin_attention_backward(do: torch.Tensor, q: torch.Tensor, k: torch.Tensor,
     strides = _GradStrides(_rows(do, "do", q_shape, dtype, device), _rows(dq, "dq", q_shape, dtype, device),
                            _rows(dk, "dk", k_shape, dtype, device), _rows(dv, "dv", k_shape, dtype, device))
     workspace = _attention_workspace(shape, 1, workspace, q)
-    _run("eqlin_attention_backward", device, stream, ctypes.byref(shape), ctypes.byref(strides), do.data_ptr(),
+    _run("eqlin_attention_backward", device, ctypes.byref(shape), ctypes.byref(strides), do.data_ptr(),
          q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(), dq.data_ptr(), dk.data_ptr(),
          dv.data_ptr(), _ptr(workspace), _workspace(workspace, device))
     return dq, dk, dv

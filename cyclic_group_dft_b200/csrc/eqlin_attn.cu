@@ -21,7 +21,7 @@ using eqlin::report;
 namespace attn = eqlin::attn;
 
 constexpr int64_t kMaxRows = int64_t(1) << 31;
-constexpr int64_t kMaxStride = int64_t(1) << 40;
+constexpr int64_t kMaxStride = int64_t(1) << 38;   // (a TMA stride is below 2^40 bytes)
 
 int check_shape(const eqlin_attention_shape* a) {
     if (!a) return report(EQLIN_ERR_INVALID_ARG, "shape is NULL");

@@ -518,7 +518,7 @@ typedef struct {
  *   several query heads are the sums over them.
  *
  * 16-bit I/O multiplies on the tensor cores with fp32 accumulation; the weights exp(s - lse) and
- * ds are rounded to the I/O type before their products.  fp32 I/O: fp32 arithmetic.  Statistics
+ * ds are rounded to the I/O type before their products (fp16: a ds above 65504 becomes infinite).  fp32 I/O: fp32 arithmetic.  Statistics
  * are fp32.  No atomics: repeated calls give the same bits.
  * Rows that no sequence covers (behind the last one) are not read and not written.  A row holding
  * infinities or NaN affects its own sequence only.  Offsets are device data the host cannot

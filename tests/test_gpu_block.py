@@ -386,6 +386,33 @@ def test_streams_graphs_and_two_calls_at_once():
         assert all(torch.equal(u, v) for u, v in zip(o2, want_b))
 
 
+def test_calls_on_a_given_stream():
+    """stream=: a torch Stream or its number; allocations inside belong to it, and work that is queued on the
+    current stream neither delays nor disturbs the call."""
+    H, Dh, G = 4, 16, 4
+    lens = [1, 1, 2]
+    k_lens = [3000, 500, 1200]                      # split keys: a workspace that the call gives up on return
+    q = _randn(sum(lens), H * Dh, G, seed=1, dtype=torch.bfloat16).to(DEV)
+    k, v = (_randn(sum(k_lens), H * Dh, G, seed=i, dtype=torch.bfloat16).to(DEV) for i in (2, 3))
+    kw = dict(heads=H, q_offsets=ref.offsets(lens, DEV), k_offsets=ref.offsets(k_lens, DEV))
+    x = _randn(300, 96, 4, seed=4, dtype=torch.bfloat16).to(DEV)
+    pos = torch.ones(300, 1, dtype=torch.int32, device=DEV)
+    want = eq.eqlin_attention_forward(q, k, v, **kw) + eq.eqlin_rmsnorm_backward(x, x)
+    want += (eq.eqlin_rope(x, pos, 1, (48,)),)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for stream in (side, side.cuda_stream, 0):
+        noise = torch.randn(2048, 2048, device=DEV)
+        for _ in range(10):
+            noise = (noise @ noise).clamp_(-1, 1)   # keeps the current stream busy, and its allocator
+            got = eq.eqlin_attention_forward(q, k, v, stream=stream, **kw)
+            got += eq.eqlin_rmsnorm_backward(x, x, stream=stream)
+            got += (eq.eqlin_rope(x, pos, 1, (48,), stream=stream),)
+            torch.full((1 << 20,), 3.0, device=DEV)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 def test_transformer_block(dtype):
     """norm -> joint projection -> rotary positions -> attention -> projection -> add and norm, forward
