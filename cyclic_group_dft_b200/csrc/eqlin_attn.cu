@@ -172,6 +172,22 @@ Fwd forward_kind(const eqlin_attention_shape& a) {
 
 constexpr int kB200Sms = 148;   // the plan does not depend on the device, so that sizes need none
 
+// fp32: 16-row tiles on the CUDA cores, with split keys in the forward, where few tiles of 64 rows would be left
+// for the tensor cores.  Measured, 64 features, CUDA cores / tensor cores: 16 tiles (256 tokens, 4 heads) forward
+// 17 / 21 us, gradients 41 / 64; 32 tiles 31 / 37 and 89 / 117; 48 tiles 27 / 21 and 68 / 66; 64 tiles (1024
+// tokens, 4 heads) 91 / 70 and 290 / 232.
+int64_t f32_tiles(int64_t rows, int64_t sequences, int64_t heads) {
+    return std::max(sequences, (rows + 63) / 64) * heads;
+}
+bool f32_small(int64_t rows, int64_t sequences, int64_t heads) {
+    return f32_tiles(rows, sequences, heads) < kB200Sms / 4;
+}
+// Forward: few queries too, as long as splits help (1 query over 4096 keys, 8 heads, 16 sequences: 179 / 285 us;
+// 16 queries, 32 sequences: 344 / 294).
+bool f32_small_forward(int64_t rows, int64_t sequences, int64_t heads) {
+    return f32_tiles(rows, sequences, heads) < (rows <= 16 * sequences ? kB200Sms : kB200Sms / 4);
+}
+
 // Slices of the keys, where the tiles alone would leave SMs idle: as many as fill them once (fp32: two blocks
 // fit an SM; tiles of 16 rows), but no slice below 256 keys.
 int forward_splits(const eqlin_attention_shape& a) {
@@ -182,7 +198,7 @@ int forward_splits(const eqlin_attention_shape& a) {
         const int64_t rows = a.q_rows * (a.heads / a.kv_heads);
         units = std::max(a.sequences, (rows + 15) / 16) * a.kv_heads;
         room = kB200Sms;
-    } else if (a.io_dtype == EQLIN_F32) {
+    } else if (a.io_dtype == EQLIN_F32 && f32_small_forward(a.q_rows, a.sequences, a.heads)) {
         units = std::max(a.sequences, (a.q_rows + 15) / 16) * a.heads;
         room = 2 * kB200Sms;
     } else {
@@ -221,7 +237,7 @@ int forward_short_m(const attn::Params& p, cudaStream_t st) {
     const int s = short_grid<M>(p.q_rows, p.sequences, (p.heads + U - 1) / U, &grid);
     if (s != EQLIN_OK) return s;
     return launch(attn::mma::eqlin_attn_fwd_short_kernel<T, DP, M>, dim3(grid), dim3(attn::mma::kShortThreads),
-                  attn::mma::short_smem<DP>(), st, "attention launch", p);
+                  attn::mma::short_smem<T, DP>(), st, "attention launch", p);
 }
 template <class T, int DP>
 int forward_short(const attn::Params& p, cudaStream_t st) {
@@ -253,23 +269,26 @@ int forward_16(attn::Params& p, Fwd kind, int io, cudaStream_t st) {
 }
 
 // ------------------------------------------------------------------------------------ fp32 I/O
-// Rows per thread of the fp32 kernels: 1 (tiles of 16 rows) where tiles of 64 would not give every SM a block.
-bool f32_small(int64_t rows, int64_t sequences, int64_t heads) {
-    return std::max(sequences, (rows + 63) / 64) * heads < kB200Sms;
-}
-
-template <int DP, int R>
-int forward_f32_r(const attn::Params& p, cudaStream_t st) {
+template <int DP>
+int forward_f32_small(const attn::Params& p, cudaStream_t st) {
     using namespace attn::f32;
-    using S = Shape<DP, R>;
-    const int s = launch(eqlin_attn_fwd_f32_kernel<DP, R>, dim3(slots(p.q_rows, p.sequences, S::M), p.heads, p.splits),
+    using S = Shape<DP>;
+    const int s = launch(eqlin_attn_fwd_f32_kernel<DP>, dim3(slots(p.q_rows, p.sequences, S::M), p.heads, p.splits),
                          dim3(kThreads), S::FWD_BYTES, st, "attention launch", p);
     return s == EQLIN_OK && p.splits > 1 ? launch_join<float>(p, st) : s;
 }
+template <int DP>
+int forward_f32_tiles(const attn::Params& p, cudaStream_t st) {
+    unsigned grid = 0;
+    const int s = tc_grid(p.q_rows, p.sequences, 64, p.heads, &grid);
+    if (s != EQLIN_OK) return s;
+    return launch(attn::mma::eqlin_attn_fwd_f32_kernel<DP>, dim3(grid), dim3(attn::mma::kShortThreads),
+                  attn::mma::short_smem<float, DP>(), st, "attention launch", p);
+}
 int forward_f32(const attn::Params& p, cudaStream_t st) {
-    const bool small = f32_small(p.q_rows, p.sequences, p.heads);
-    if (p.D <= 64) return small ? forward_f32_r<64, 1>(p, st) : forward_f32_r<64, 4>(p, st);
-    return small ? forward_f32_r<128, 1>(p, st) : forward_f32_r<128, 4>(p, st);
+    if (f32_small_forward(p.q_rows, p.sequences, p.heads))
+        return p.D <= 64 ? forward_f32_small<64>(p, st) : forward_f32_small<128>(p, st);
+    return p.D <= 64 ? forward_f32_tiles<64>(p, st) : forward_f32_tiles<128>(p, st);
 }
 
 template <class T>
@@ -283,10 +302,10 @@ int launch_delta(const attn::Params& p, cudaStream_t st) {
                   "attention gradient launch", p, lanes);
 }
 
-template <int DP, int R>
-int backward_f32_r(const attn::Params& p, cudaStream_t st) {
+template <int DP>
+int backward_f32_small(const attn::Params& p, cudaStream_t st) {
     using namespace attn::f32;
-    using S = Shape<DP, R>;
+    using S = Shape<DP>;
     unsigned k_blocks = 0, q_blocks = 0;
     int s = EQLIN_OK;
     if (p.k_rows > 0) s = tc_grid(p.k_rows, p.sequences, S::M, p.kv_heads, &k_blocks);
@@ -295,13 +314,27 @@ int backward_f32_r(const attn::Params& p, cudaStream_t st) {
         s = report(EQLIN_ERR_UNSUPPORTED, "too many rows, sequences and heads for one call");
     if (s == EQLIN_OK && p.q_rows > 0) s = launch_delta<float>(p, st);
     if (s != EQLIN_OK) return s;
-    return launch(eqlin_attn_bwd_f32_kernel<DP, R>, dim3(k_blocks + q_blocks), dim3(kThreads),
+    return launch(eqlin_attn_bwd_f32_kernel<DP>, dim3(k_blocks + q_blocks), dim3(kThreads),
                   std::max(S::DKV_BYTES, S::DQ_BYTES), st, "attention gradient launch", p, k_blocks);
 }
+template <int DP>
+int backward_f32_tiles(const attn::Params& p, cudaStream_t st) {
+    namespace mma = attn::mma;
+    unsigned grid_q = 0, grid_k = 0;
+    int s = tc_grid(p.q_rows, p.sequences, 64, p.heads, &grid_q);
+    if (s == EQLIN_OK) s = tc_grid(p.k_rows, p.sequences, 64, p.kv_heads, &grid_k);
+    if (s == EQLIN_OK && p.q_rows > 0)
+        s = launch(mma::eqlin_attn_dq_f32_kernel<DP>, dim3(grid_q), dim3(mma::kShortThreads),
+                   mma::short_bwd_smem<float, DP>(), st, "attention gradient launch", p);
+    if (s == EQLIN_OK && p.k_rows > 0)
+        s = launch(mma::eqlin_attn_dkv_f32_kernel<DP>, dim3(grid_k), dim3(mma::kShortThreads),
+                   mma::short_bwd_smem<float, DP>(), st, "attention gradient launch", p);
+    return s;
+}
 int backward_f32(const attn::Params& p, cudaStream_t st) {
-    const bool small = f32_small(std::max(p.q_rows, p.k_rows), p.sequences, p.heads);
-    if (p.D <= 64) return small ? backward_f32_r<64, 1>(p, st) : backward_f32_r<64, 4>(p, st);
-    return small ? backward_f32_r<128, 1>(p, st) : backward_f32_r<128, 4>(p, st);
+    if (f32_small(std::max(p.q_rows, p.k_rows), p.sequences, p.heads))
+        return p.D <= 64 ? backward_f32_small<64>(p, st) : backward_f32_small<128>(p, st);
+    return p.D <= 64 ? backward_f32_tiles<64>(p, st) : backward_f32_tiles<128>(p, st);
 }
 
 template <class T, int DP>
@@ -343,10 +376,10 @@ int backward_short_m(const attn::Params& p, cudaStream_t st) {
     if (s == EQLIN_OK) s = short_grid<M>(p.k_rows, p.sequences, (p.kv_heads + U - 1) / U, &grid_k);
     if (s == EQLIN_OK && p.q_rows > 0)
         s = launch(mma::eqlin_attn_dq_short_kernel<T, DP, M>, dim3(grid_q), dim3(mma::kShortThreads),
-                   mma::short_bwd_smem<DP>(), st, "attention gradient launch", p);
+                   mma::short_bwd_smem<T, DP>(), st, "attention gradient launch", p);
     if (s == EQLIN_OK && p.k_rows > 0)
         s = launch(mma::eqlin_attn_dkv_short_kernel<T, DP, M>, dim3(grid_k), dim3(mma::kShortThreads),
-                   mma::short_bwd_smem<DP>(), st, "attention gradient launch", p);
+                   mma::short_bwd_smem<T, DP>(), st, "attention gradient launch", p);
     return s;
 }
 template <class T, int DP>

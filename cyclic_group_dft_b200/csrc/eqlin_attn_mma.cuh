@@ -1,7 +1,13 @@
-// eqlin_attn_mma.cuh -- 16-bit attention where a 128-row tensor-core tile would be mostly empty: short
-// sequences (windows of a few dozen tokens) and few queries over many keys.  Both are bound by memory,
-// not by the tensor cores, and use 16-row warp products (mma.sync m16n8k16) whose scores and outputs
-// stay in registers.
+// eqlin_attn_mma.cuh -- attention by 16-row warp products (mma.sync), whose scores and outputs stay in
+// registers:
+//   16-bit I/O where a 128-row tcgen05 tile would be mostly empty: short sequences (windows of a few dozen tokens)
+//   and few queries over many keys.  Both are bound by memory, not by the tensor cores.
+//   fp32 I/O of more than a few tiles, each product as three of tf32: with hi = tf32(v) (rounded to nearest) and
+//   lo = v - hi (exact, at most 2^-11 |v|), a b = hi hi + hi lo + lo hi but for lo lo and what the tensor core
+//   cuts off lo: 2.5 * 2^-21 |a b| at most.  Bound by the tensor cores' tf32 rate, a third of it, and by the
+//   splitting; against CUDA cores: 784 tokens, 8 sequences, 8 heads of 64 features forward 322 to 244 us,
+//   gradients 1056 to 784; 4096 tokens, 4 heads of 128 1060 to 731 and 3530 to 3333.  (Each small product
+//   behind the last on the same accumulator: 262 and 929, 916 and 4781.)
 //
 // Tiles in shared memory are rows of DP features; the 16-byte chunk c of row r lies at chunk
 // c ^ (r & 7), so that ldmatrix reads eight rows without bank conflicts.  Rows past a sequence's end
@@ -50,14 +56,51 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
             : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
             : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+__device__ __forceinline__ void mma1688(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// v = hi + lo, hi with the 11 significant bits of tf32
+struct Split {
+    uint32_t hi, lo;
+    __device__ __forceinline__ explicit Split(uint32_t v) {
+        asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(hi) : "f"(__uint_as_float(v)));
+        lo = __float_as_uint(__uint_as_float(v) - __uint_as_float(hi));
+    }
+};
+// d[i] += a b[i] in fp32 precision for N tiles of 8 columns: the small products first, and each of the three over
+// all tiles before the next, so that no product waits for the one before it.
+template <int N>
+__device__ __forceinline__ void mma_f32(float (*d)[4], const uint32_t (&ah)[4], const uint32_t (&al)[4],
+                                        const uint32_t (&b)[N][2]) {
+    uint32_t bh[N][2], bl[N][2];
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const Split v(b[i][e]);
+            bh[i][e] = v.hi;
+            bl[i][e] = v.lo;
+        }
+#pragma unroll
+    for (int i = 0; i < N; ++i) mma1688(d[i], al, bh[i][0], bh[i][1]);
+#pragma unroll
+    for (int i = 0; i < N; ++i) mma1688(d[i], ah, bl[i][0], bl[i][1]);
+#pragma unroll
+    for (int i = 0; i < N; ++i) mma1688(d[i], ah, bh[i][0], bh[i][1]);
+}
 __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-template <int DP>
+// RB: bytes of a row of a tile
+template <class T, int DP>
+constexpr int kRowBytes = DP * static_cast<int>(sizeof(T));
+template <int RB>
 __device__ __forceinline__ uint32_t at(uint32_t tile, int row, int chunk) {
-    return tile + row * (DP * 2) + ((chunk ^ (row & 7)) << 4);
+    return tile + row * RB + ((chunk ^ (row & 7)) << 4);
 }
 // the four lanes of a row pair
 __device__ __forceinline__ float quad_max(float v) {
@@ -69,71 +112,131 @@ __device__ __forceinline__ float quad_sum(float v) {
     return v + __shfl_xor_sync(0xFFFFFFFFu, v, 2);
 }
 
-// What a lane adds to a tile's address to read 16 x 16 pieces of it with ldmatrix.  Tiles are aligned to
-// their row bytes, rows r and r + 8 have the same chunk order, and the chunks of piece k differ from those of
-// piece 0 in address bits 5 to 7 alone: (base + lane part) ^ (k << 5) is the whole address computation.
-template <int DP>
+// What a lane adds to a tile's address to read pieces of 16 rows x 32 bytes with ldmatrix (16 features of 16 bits,
+// or 8 of fp32, whose fragments have the same places).  Tiles are aligned to their row bytes, rows r and r + 8
+// have the same chunk order, and the chunks of piece k differ from those of piece 0 in address bits from 5 on
+// alone: (base + lane part) ^ (k << 5) is the whole address computation.
+template <int RB>
 struct Lane {
     uint32_t a;   // rows 0-15 of the lower 16 bytes, then of the upper (operand A; B through a transpose)
     uint32_t b;   // rows 0-7 lower, rows 0-7 upper, rows 8-15 lower, rows 8-15 upper (operand B)
     __device__ __forceinline__ explicit Lane(int lane)
-        : a((lane & 15) * (DP * 2) + (((lane >> 4) ^ (lane & 7)) << 4)),
-          b(((lane & 7) + ((lane >> 4) << 3)) * (DP * 2) + ((((lane >> 3) & 1) ^ (lane & 7)) << 4)) {}
+        : a((lane & 15) * RB + (((lane >> 4) ^ (lane & 7)) << 4)),
+          b(((lane & 7) + ((lane >> 4) << 3)) * RB + ((((lane >> 3) & 1) ^ (lane & 7)) << 4)) {}
 };
 
-// acc[n8 tile] (16 rows of A x NT * 8 rows of B) += A B^T over the features, A and B row tiles.
+// acc[n8 tile] (16 rows of A x NT * 8 rows of B) += A B^T over the features, A and B row tiles; `steps` pieces of
+// 32 bytes.
 template <class T, int DP, int NT>
 __device__ __forceinline__ void rows_by_rows(float (&acc)[NT][4], uint32_t a_tile, uint32_t b_tile, int steps,
-                                             const Lane<DP>& at) {
+                                             const Lane<kRowBytes<T, DP>>& at) {
+    constexpr int RB = kRowBytes<T, DP>;
     const uint32_t la = a_tile + at.a, lb = b_tile + at.b;
-    // the pieces of the next 16 features are on their way while these are multiplied
-    uint32_t a[2][4], b[2][NT / 2][4];
-    auto fetch = [&](int ks) {
-        ldm4(a[ks & 1], la ^ (ks << 5));
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll 2
+        for (int ks = 0; ks < steps; ++ks) {
+            uint32_t a[4], ah[4], al[4], b[NT][2];
+            ldm4(a, la ^ (ks << 5));
 #pragma unroll
-        for (int n = 0; n < NT / 2; ++n) ldm4(b[ks & 1][n], (lb ^ (ks << 5)) + n * 16 * (DP * 2));
-    };
-    fetch(0);
+            for (int n = 0; n < NT; n += 2) {
+                uint32_t r[4];
+                ldm4(r, (lb ^ (ks << 5)) + n * 8 * RB);
+                b[n][0] = r[0];
+                b[n][1] = r[1];
+                b[n + 1][0] = r[2];
+                b[n + 1][1] = r[3];
+            }
 #pragma unroll
-    for (int ks = 0; ks < DP / 16; ++ks) {
-        if (ks >= steps) break;
-        if (ks + 1 < DP / 16) fetch(ks + 1);      // (past the head's features: zeros)
+            for (int e = 0; e < 4; ++e) {
+                const Split v(a[e]);
+                ah[e] = v.hi;
+                al[e] = v.lo;
+            }
+            mma_f32<NT>(acc, ah, al, b);
+        }
+    } else {
+        // the next pieces are on their way while these are multiplied
+        uint32_t a[2][4], b[2][NT / 2][4];
+        auto fetch = [&](int ks) {
+            ldm4(a[ks & 1], la ^ (ks << 5));
 #pragma unroll
-        for (int n = 0; n < NT / 2; ++n) {
-            mma16816<T>(acc[2 * n], a[ks & 1], b[ks & 1][n][0], b[ks & 1][n][1]);
-            mma16816<T>(acc[2 * n + 1], a[ks & 1], b[ks & 1][n][2], b[ks & 1][n][3]);
+            for (int n = 0; n < NT / 2; ++n) ldm4(b[ks & 1][n], (lb ^ (ks << 5)) + n * 16 * RB);
+        };
+        fetch(0);
+#pragma unroll
+        for (int ks = 0; ks < RB / 32; ++ks) {
+            if (ks >= steps) break;
+            if (ks + 1 < RB / 32) fetch(ks + 1);      // (past the head's features: zeros)
+#pragma unroll
+            for (int n = 0; n < NT / 2; ++n) {
+                mma16816<T>(acc[2 * n], a[ks & 1], b[ks & 1][n][0], b[ks & 1][n][1]);
+                mma16816<T>(acc[2 * n + 1], a[ks & 1], b[ks & 1][n][2], b[ks & 1][n][3]);
+            }
         }
     }
 }
-// o[feature tile] += P B: P = 16 rows x NT * 8 from accumulators rounded to T, B a row tile.
+// o[feature tile] += W B: W = 16 rows x NT * 8 weights from accumulators (rounded to T where T has 16 bits), B a row
+// tile.  fp32: the accumulator's columns 2 t and 2 t + 1 of 8 stand at k = t and t + 4, so rows 2 t and 2 t + 1 of B
+// are read there.
 template <class T, int DP, int NT>
 __device__ __forceinline__ void weights_by_rows(float (&o)[DP / 8][4], const float (&w)[NT][4], uint32_t b_tile, int steps,
-                                                const Lane<DP>& at) {
-    const uint32_t lb = b_tile + at.a;
-    constexpr int GROUP = 4;                      // pieces of 16 features in flight
+                                                const Lane<kRowBytes<T, DP>>& at, int lane) {
+    constexpr int RB = kRowBytes<T, DP>;
+    if constexpr (sizeof(T) == 4) {
+        // feature 8 d + lane / 4 of row 8 kb + 2 (lane & 3), and of the next row
+        const int t2 = (lane & 3) * 2, in = (lane >> 2) & 3, up = lane >> 4;
+        const uint32_t row0 = b_tile + t2 * RB + ((up ^ t2) << 4) + in * 4;
+        const uint32_t row1 = b_tile + (t2 + 1) * RB + ((up ^ (t2 + 1)) << 4) + in * 4;
 #pragma unroll
-    for (int kb = 0; kb < NT / 2; ++kb) {
-        const uint32_t a[4] = {Io16<T>::pack(w[2 * kb][0], w[2 * kb][1]), Io16<T>::pack(w[2 * kb][2], w[2 * kb][3]),
-                               Io16<T>::pack(w[2 * kb + 1][0], w[2 * kb + 1][1]),
-                               Io16<T>::pack(w[2 * kb + 1][2], w[2 * kb + 1][3])};
+        for (int kb = 0; kb < NT; ++kb) {
+            uint32_t ah[4], al[4];
 #pragma unroll
-        for (int d0 = 0; d0 < DP / 16; d0 += GROUP) {
-            if (d0 >= steps) break;
-            uint32_t b[GROUP][4];
+            for (int e = 0; e < 4; ++e) {
+                const Split v(__float_as_uint(w[kb][e == 1 ? 2 : e == 2 ? 1 : e]));
+                ah[e] = v.hi;
+                al[e] = v.lo;
+            }
+            constexpr int GROUP = 4;                  // tiles of 8 features at once
 #pragma unroll
-            for (int d = 0; d < GROUP; ++d) ldm4t(b[d], (lb ^ ((d0 + d) << 5)) + kb * 16 * (DP * 2));
+            for (int d0 = 0; d0 < DP / 8; d0 += GROUP) {
+                if (d0 >= steps) break;
+                uint32_t b[GROUP][2];
 #pragma unroll
-            for (int d = 0; d < GROUP; ++d) {
-                mma16816<T>(o[2 * (d0 + d)], a, b[d][0], b[d][1]);
-                mma16816<T>(o[2 * (d0 + d) + 1], a, b[d][2], b[d][3]);
+                for (int d = 0; d < GROUP; ++d) {
+                    const uint32_t at_d = (d0 + d) << 5;
+                    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(b[d][0]) : "r"((row0 ^ at_d) + kb * 8 * RB) : "memory");
+                    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(b[d][1]) : "r"((row1 ^ at_d) + kb * 8 * RB) : "memory");
+                }
+                mma_f32<GROUP>(o + d0, ah, al, b);
+            }
+        }
+    } else {
+        const uint32_t lb = b_tile + at.a;
+        constexpr int GROUP = 4;                      // pieces of 16 features in flight
+#pragma unroll
+        for (int kb = 0; kb < NT / 2; ++kb) {
+            const uint32_t a[4] = {Io16<T>::pack(w[2 * kb][0], w[2 * kb][1]), Io16<T>::pack(w[2 * kb][2], w[2 * kb][3]),
+                                   Io16<T>::pack(w[2 * kb + 1][0], w[2 * kb + 1][1]),
+                                   Io16<T>::pack(w[2 * kb + 1][2], w[2 * kb + 1][3])};
+#pragma unroll
+            for (int d0 = 0; d0 < DP / 16; d0 += GROUP) {
+                if (d0 >= steps) break;
+                uint32_t b[GROUP][4];
+#pragma unroll
+                for (int d = 0; d < GROUP; ++d) ldm4t(b[d], (lb ^ ((d0 + d) << 5)) + kb * 16 * RB);
+#pragma unroll
+                for (int d = 0; d < GROUP; ++d) {
+                    mma16816<T>(o[2 * (d0 + d)], a, b[d][0], b[d][1]);
+                    mma16816<T>(o[2 * (d0 + d) + 1], a, b[d][2], b[d][3]);
+                }
             }
         }
     }
 }
 
 // Running softmax of 16 rows x NT * 8 keys: masks keys >= last[i] (relative to this tile) of row i of
-// the pair, which are all >= `masked` (the same for the warp), turns s into weights, and past the `first` tile moves the maximum and scales o
-// and sum.
+// the pair, which are all >= `masked` (the same for the warp), turns s into weights, and past the `first` tile
+// moves the maximum and scales o and sum.
 template <int NT, int DT>
 __device__ __forceinline__ void softmax_step(float (&s)[NT][4], float (&o)[DT][4], float (&top)[2], float (&sum)[2],
                                              const int (&last)[2], int masked, bool first, float c2, int lane) {
@@ -209,63 +312,77 @@ __device__ __forceinline__ void for_short_tiles(const int32_t* offsets, int sequ
         __syncthreads();   // the next tile takes the same shared memory
     }
 }
-template <int DP>
+template <class T, int DP>
 constexpr size_t short_smem() {
-    return size_t(3) * 64 * DP * 2;
+    return size_t(3) * 64 * kRowBytes<T, DP>;
 }
 
 // Rows [0, M) of a tile (zeros past n and past D) by THREADS threads: a thread keeps its 16-byte column.
 template <class T, int DP, int M, int THREADS>
 __device__ __forceinline__ void copy_tile(uint32_t dst, const void* src, long long stride, long long row0, int n, int D,
                                           int head, int tid) {
-    constexpr int ROWS = THREADS / (DP / 8);                // rows of one step
-    const int c = tid % (DP / 8), r0 = tid / (DP / 8);
-    const T* g = static_cast<const T*>(src) + (row0 + r0) * stride + static_cast<long long>(head) * D + c * 8;
+    constexpr int RB = kRowBytes<T, DP>, CHUNKS = RB / 16, PER = 16 / sizeof(T);
+    constexpr int ROWS = THREADS / CHUNKS;                  // rows of one step
+    const int c = tid % CHUNKS, r0 = tid / CHUNKS;
+    const T* g = static_cast<const T*>(src) + (row0 + r0) * stride + static_cast<long long>(head) * D + c * PER;
     const long long step = ROWS * stride;
-    const int left = c * 8 < D ? n - r0 : 0;                // rows k * ROWS below this are copied
-    const uint32_t d0 = at<DP>(dst, r0, c);
+    const int left = c * PER < D ? n - r0 : 0;              // rows k * ROWS below this are copied
+    const uint32_t d0 = at<RB>(dst, r0, c);
 #pragma unroll
     for (int k = 0; k < M / ROWS; ++k) {
         const bool take = k * ROWS < left;
-        const uint32_t d = ROWS % 8 == 0 ? d0 + k * ROWS * (DP * 2) : at<DP>(dst, r0 + k * ROWS, c);
+        const uint32_t d = ROWS % 8 == 0 ? d0 + k * ROWS * RB : at<RB>(dst, r0 + k * ROWS, c);
         cp_async16(d, take ? g : static_cast<const T*>(src), take);
         g += step;
     }
 }
 
-// Output rows of a warp through its 16 rows of a tile in shared memory, then as whole 16-byte chunks: the
+// Output rows of a warp, 16 bits through its 16 rows of a tile in shared memory and then as whole 16-byte chunks: the
 // accumulators times mul[i] (row lane / 4 + 8 i), rows below n.
 template <class T, int DP>
 __device__ __forceinline__ void store_rows(const float (&acc)[DP / 8][4], const float (&mul)[2], uint32_t tile, int warp_row,
                                            int n, int D, T* out, long long stride, int lane) {
+    if constexpr (sizeof(T) == 4) {   // four lanes write 32 bytes of a row: whole sectors as it is
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const uint32_t base = at<DP>(tile, warp_row + (lane >> 2) + 8 * i, 0) + (lane & 3) * 4;
+        for (int i = 0; i < 2; ++i) {
+            const int r = warp_row + (lane >> 2) + 8 * i;
+            if (r >= n) continue;
+            float* row = out + r * stride + (lane & 3) * 2;
 #pragma unroll
-        for (int d = 0; d < DP / 8; ++d) {
-            const uint32_t w = Io16<T>::pack(acc[d][2 * i] * mul[i], acc[d][2 * i + 1] * mul[i]);
-            asm volatile("st.shared.b32 [%0], %1;" ::"r"(base ^ (d << 4)), "r"(w) : "memory");
+            for (int d = 0; d < DP / 8; ++d)
+                if (d * 8 < D) *reinterpret_cast<float2*>(row + d * 8) = make_float2(acc[d][2 * i] * mul[i], acc[d][2 * i + 1] * mul[i]);
         }
-    }
-    __syncwarp();
-    constexpr int ROWS = 32 / (DP / 8);                     // rows of one step
-    const int c = lane % (DP / 8);
+    } else {
+        constexpr int RB = kRowBytes<T, DP>;
 #pragma unroll
-    for (int k = 0; k < 16 / ROWS; ++k) {
-        const int r = warp_row + lane / (DP / 8) + k * ROWS;
-        if (r >= n || c * 8 >= D) continue;
-        uint4 v;
-        asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
-                     : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                     : "r"(at<DP>(tile, r, c))
-                     : "memory");
-        *reinterpret_cast<uint4*>(out + r * stride + c * 8) = v;
+        for (int i = 0; i < 2; ++i) {
+            const uint32_t base = at<RB>(tile, warp_row + (lane >> 2) + 8 * i, 0) + (lane & 3) * 4;
+#pragma unroll
+            for (int d = 0; d < DP / 8; ++d) {
+                const uint32_t w = Io16<T>::pack(acc[d][2 * i] * mul[i], acc[d][2 * i + 1] * mul[i]);
+                asm volatile("st.shared.b32 [%0], %1;" ::"r"(base ^ (d << 4)), "r"(w) : "memory");
+            }
+        }
+        __syncwarp();
+        constexpr int ROWS = 32 / (DP / 8);                     // rows of one step
+        const int c = lane % (DP / 8);
+#pragma unroll
+        for (int k = 0; k < 16 / ROWS; ++k) {
+            const int r = warp_row + lane / (DP / 8) + k * ROWS;
+            if (r >= n || c * 8 >= D) continue;
+            uint4 v;
+            asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                         : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                         : "r"(at<RB>(tile, r, c))
+                         : "memory");
+            *reinterpret_cast<uint4*>(out + r * stride + c * 8) = v;
+        }
     }
 }
 
 template <class T, int DP, int M>
 __device__ __forceinline__ void fwd_short_tile(const Params& p, uint8_t* smem, int head_block, const Tile& t) {
-    constexpr int U = 64 / M, WU = 4 / U, NT = M / 8;      // heads of a block, warps of a head
+    constexpr int RB = kRowBytes<T, DP>, U = 64 / M, WU = 4 / U, NT = M / 8;      // heads of a block, warps of a head
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int unit = warp / WU, rw = warp % WU;
     const int h = (head_block) * U + unit;
@@ -274,10 +391,10 @@ __device__ __forceinline__ void fwd_short_tile(const Params& p, uint8_t* smem, i
     const int seen = keys_seen(r0 + n - 1, t.own.len, kr.len, p.causal);
     const bool on = h < p.heads;                            // the last block may have fewer heads
     const int hk = h / (p.heads / p.kv_heads);
-    const uint32_t sq = ptx::smem_u32(smem) + unit * (3 * M * DP * 2), sk = sq + M * DP * 2, sv = sk + M * DP * 2;
+    const uint32_t sq = ptx::smem_u32(smem) + unit * (3 * M * RB), sk = sq + M * RB, sv = sk + M * RB;
     const int tid = threadIdx.x - unit * WU * 32;
-    const Lane<DP> la(lane);
-    const int steps = (p.D + 15) / 16;
+    const Lane<RB> la(lane);
+    const int steps = (p.D * static_cast<int>(sizeof(T)) + 31) / 32;
     const float c2 = p.scale * kLog2e;
     float o[DP / 8][4];
 #pragma unroll
@@ -302,7 +419,7 @@ __device__ __forceinline__ void fwd_short_tile(const Params& p, uint8_t* smem, i
         for (int i = 0; i < NT; ++i) s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.f;
         const bool work = on && rw * 16 < n;
         if (work) {
-            rows_by_rows<T, DP, NT>(s, sq + rw * 16 * (DP * 2), sk, steps, la);
+            rows_by_rows<T, DP, NT>(s, sq + rw * 16 * RB, sk, steps, la);
             int last[2];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
@@ -313,7 +430,7 @@ __device__ __forceinline__ void fwd_short_tile(const Params& p, uint8_t* smem, i
         }
         cp_async_wait<0>();
         __syncthreads();
-        if (work) weights_by_rows<T, DP, NT>(o, s, sv, steps, la);
+        if (work) weights_by_rows<T, DP, NT>(o, s, sv, steps, la, lane);
     }
     cp_async_wait<0>();
     __syncthreads();
@@ -343,15 +460,15 @@ __global__ void __launch_bounds__(kShortThreads, DP == 128 ? 4 : 5) eqlin_attn_f
 }
 
 // Gradients of short sequences: the forward's tiles, with four of them (Q, dO, K, V) in shared memory.
-template <int DP>
+template <class T, int DP>
 constexpr size_t short_bwd_smem() {
-    return size_t(4) * 64 * DP * 2 + 2 * 64 * sizeof(float);
+    return size_t(4) * 64 * kRowBytes<T, DP> + 2 * 64 * sizeof(float);
 }
 
 // dq, and delta = do . o of its rows, which the kernel for dk and dv (launched next) reads.
 template <class T, int DP, int M>
 __device__ __forceinline__ void dq_short_tile(const Params& p, uint8_t* smem, int head_block, const Tile& t) {
-    constexpr int U = 64 / M, WU = 4 / U, NT = M / 8;
+    constexpr int RB = kRowBytes<T, DP>, U = 64 / M, WU = 4 / U, NT = M / 8;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int unit = warp / WU, rw = warp % WU;
     const int h = (head_block) * U + unit;
@@ -360,11 +477,11 @@ __device__ __forceinline__ void dq_short_tile(const Params& p, uint8_t* smem, in
     const int seen = keys_seen(r0 + n - 1, t.own.len, kr.len, p.causal);
     const bool on = h < p.heads;
     const int hk = h / (p.heads / p.kv_heads);
-    const uint32_t sq = ptx::smem_u32(smem) + unit * (4 * M * DP * 2), sdo = sq + M * DP * 2, sk = sdo + M * DP * 2,
-                   sv = sk + M * DP * 2;
+    const uint32_t sq = ptx::smem_u32(smem) + unit * (4 * M * RB), sdo = sq + M * RB, sk = sdo + M * RB,
+                   sv = sk + M * RB;
     const int tid = threadIdx.x - unit * WU * 32;
-    const Lane<DP> la(lane);
-    const int steps = (p.D + 15) / 16;
+    const Lane<RB> la(lane);
+    const int steps = (p.D * static_cast<int>(sizeof(T)) + 31) / 32;
     const float c2 = p.scale * kLog2e;
     const int row = rw * 16 + (lane >> 2);
     const long long first_row = static_cast<long long>(t.own.start) + r0;
@@ -382,14 +499,15 @@ __device__ __forceinline__ void dq_short_tile(const Params& p, uint8_t* smem, in
             const T* po = static_cast<const T*>(p.o) + (first_row + r) * p.o_stride + static_cast<long long>(h) * p.D;
             const T* pd = static_cast<const T*>(p.dout) + (first_row + r) * p.do_stride + static_cast<long long>(h) * p.D;
 #pragma unroll
-            for (int c = 0; c < DP / 16; ++c) {
-                const int at8 = (2 * c + (lane & 1)) * 8;
-                if (at8 >= p.D) break;
-                float a[8], b[8];
-                Vec<T, 8>::unpack(Vec<T, 8>::load(po + at8), a);
-                Vec<T, 8>::unpack(Vec<T, 8>::load(pd + at8), b);
+            for (int c = 0; c < RB / 32; ++c) {
+                constexpr int PER = 16 / sizeof(T);
+                const int first = (2 * c + (lane & 1)) * PER;
+                if (first >= p.D) break;
+                float a[PER], b[PER];
+                Vec<T, PER>::unpack(Vec<T, PER>::load(po + first), a);
+                Vec<T, PER>::unpack(Vec<T, PER>::load(pd + first), b);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) sum = fmaf(a[e], b[e], sum);
+                for (int e = 0; e < PER; ++e) sum = fmaf(a[e], b[e], sum);
             }
         }
         sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 1);
@@ -420,8 +538,8 @@ __device__ __forceinline__ void dq_short_tile(const Params& p, uint8_t* smem, in
         for (int i = 0; i < NT; ++i)
 #pragma unroll
             for (int e = 0; e < 4; ++e) s[i][e] = dp[i][e] = 0.f;
-        rows_by_rows<T, DP, NT>(s, sq + rw * 16 * (DP * 2), sk, steps, la);
-        rows_by_rows<T, DP, NT>(dp, sdo + rw * 16 * (DP * 2), sv, steps, la);
+        rows_by_rows<T, DP, NT>(s, sq + rw * 16 * RB, sk, steps, la);
+        rows_by_rows<T, DP, NT>(dp, sdo + rw * 16 * RB, sv, steps, la);
         int last[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i) last[i] = min(kn, p.causal ? r0 + row + 8 * i + 1 + kr.len - t.own.len - k0 : kn);
@@ -432,7 +550,7 @@ __device__ __forceinline__ void dq_short_tile(const Params& p, uint8_t* smem, in
                 const bool vis = i * 8 + (lane & 3) * 2 + (e & 1) < last[e >> 1];
                 s[i][e] = vis ? ex2(fmaf(s[i][e], c2, off[e >> 1])) * (dp[i][e] - delta[e >> 1]) : 0.f;
             }
-        weights_by_rows<T, DP, NT>(dq, s, sk, steps, la);
+        weights_by_rows<T, DP, NT>(dq, s, sk, steps, la, lane);
     }
     cp_async_commit();
     cp_async_wait<0>();
@@ -456,7 +574,7 @@ __global__ void __launch_bounds__(kShortThreads, DP == 128 ? 3 : 4) eqlin_attn_d
 // dk and dv: a warp owns 16 keys; the query rows that see the tile pass by, for each head of the group.
 template <class T, int DP, int M>
 __device__ __forceinline__ void dkv_short_tile(const Params& p, uint8_t* smem, int head_block, const Tile& t) {
-    constexpr int U = 64 / M, WU = 4 / U, NT = (M < 32 ? M : 32) / 8;   // queries in steps of 32 (or M) columns
+    constexpr int RB = kRowBytes<T, DP>, U = 64 / M, WU = 4 / U, NT = (M < 32 ? M : 32) / 8;   // queries in steps of 32 (or M) columns
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int group = p.heads / p.kv_heads;
     const int unit = warp / WU, rw = warp % WU;
@@ -464,13 +582,13 @@ __device__ __forceinline__ void dkv_short_tile(const Params& p, uint8_t* smem, i
     const Rows qr = other_rows(p, t, p.q_offsets, p.q_rows);
     const int r0 = t.tile * M, n = min(M, t.own.len - r0);
     const bool on = hk < p.kv_heads;
-    const uint32_t sk = ptx::smem_u32(smem) + unit * (4 * M * DP * 2), sv = sk + M * DP * 2, sq = sv + M * DP * 2,
-                   sdo = sq + M * DP * 2;
-    float* slse = reinterpret_cast<float*>(smem + 4 * 64 * DP * 2) + unit * 2 * M;   // lse, then delta, of the tile's rows
+    const uint32_t sk = ptx::smem_u32(smem) + unit * (4 * M * RB), sv = sk + M * RB, sq = sv + M * RB,
+                   sdo = sq + M * RB;
+    float* slse = reinterpret_cast<float*>(smem + 4 * 64 * RB) + unit * 2 * M;   // lse, then delta, of the tile's rows
     float* sdelta = slse + M;
     const int tid = threadIdx.x - unit * WU * 32;
-    const Lane<DP> la(lane);
-    const int steps = (p.D + 15) / 16;
+    const Lane<RB> la(lane);
+    const int steps = (p.D * static_cast<int>(sizeof(T)) + 31) / 32;
     const float c2 = p.scale * kLog2e;
     const int key = r0 + rw * 16 + (lane >> 2);
     const long long first_row = static_cast<long long>(t.own.start) + r0;
@@ -510,8 +628,8 @@ __device__ __forceinline__ void dkv_short_tile(const Params& p, uint8_t* smem, i
                 for (int i = 0; i < NT; ++i)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) s[i][e] = dp[i][e] = 0.f;
-                rows_by_rows<T, DP, NT>(s, sk + rw * 16 * (DP * 2), sq + c0 * (DP * 2), steps, la);
-                rows_by_rows<T, DP, NT>(dp, sv + rw * 16 * (DP * 2), sdo + c0 * (DP * 2), steps, la);
+                rows_by_rows<T, DP, NT>(s, sk + rw * 16 * RB, sq + c0 * RB, steps, la);
+                rows_by_rows<T, DP, NT>(dp, sv + rw * 16 * RB, sdo + c0 * RB, steps, la);
 #pragma unroll
                 for (int i = 0; i < NT; ++i) {
                     const int c = c0 + i * 8 + (lane & 3) * 2;
@@ -525,8 +643,8 @@ __device__ __forceinline__ void dkv_short_tile(const Params& p, uint8_t* smem, i
                         dp[i][e] = w == 0.f ? 0.f : w * (dp[i][e] - (e & 1 ? dl.y : dl.x));
                     }
                 }
-                weights_by_rows<T, DP, NT>(dv, s, sdo + c0 * (DP * 2), steps, la);
-                weights_by_rows<T, DP, NT>(dk, dp, sq + c0 * (DP * 2), steps, la);
+                weights_by_rows<T, DP, NT>(dv, s, sdo + c0 * RB, steps, la, lane);
+                weights_by_rows<T, DP, NT>(dk, dp, sq + c0 * RB, steps, la, lane);
             }
         }
     }
@@ -548,6 +666,35 @@ __global__ void __launch_bounds__(kShortThreads, DP == 128 ? 2 : 4) eqlin_attn_d
     const int n_hb = (p.kv_heads + U - 1) / U;
     for_short_tiles<M>(p.k_offsets, p.sequences, p.k_rows, blockIdx.x / n_hb,
                        [&](const Tile& t) { dkv_short_tile<T, DP, M>(p, smem, blockIdx.x % n_hb, t); });
+}
+
+// fp32 of every length: a block for each tile of 64 rows and head.  The kernels are bound by the three tf32
+// products (503 multiply-adds a cycle and SM measured, so 168 of fp32; the FMA pipes have 124).
+template <int DP>
+__global__ void __launch_bounds__(kShortThreads) eqlin_attn_fwd_f32_kernel(const Params p) {
+    extern __shared__ __align__(1024) uint8_t smem[];
+    ptx::grid_launch_dependents();
+    ptx::grid_dependency_wait();
+    const int slot = p.causal ? gridDim.x / p.heads - 1 - blockIdx.x / p.heads : blockIdx.x / p.heads;   // long rows first
+    const Tile t = find_tile<64>(p.q_offsets, p.sequences, p.q_rows, slot);
+    if (t.tile >= 0) fwd_short_tile<float, DP, 64>(p, smem, blockIdx.x % p.heads, t);
+}
+template <int DP>
+__global__ void __launch_bounds__(kShortThreads) eqlin_attn_dq_f32_kernel(const Params p) {
+    extern __shared__ __align__(1024) uint8_t smem[];
+    ptx::grid_launch_dependents();
+    ptx::grid_dependency_wait();
+    const int slot = p.causal ? gridDim.x / p.heads - 1 - blockIdx.x / p.heads : blockIdx.x / p.heads;
+    const Tile t = find_tile<64>(p.q_offsets, p.sequences, p.q_rows, slot);
+    if (t.tile >= 0) dq_short_tile<float, DP, 64>(p, smem, blockIdx.x % p.heads, t);
+}
+template <int DP>
+__global__ void __launch_bounds__(kShortThreads) eqlin_attn_dkv_f32_kernel(const Params p) {
+    extern __shared__ __align__(1024) uint8_t smem[];
+    ptx::grid_launch_dependents();
+    ptx::grid_dependency_wait();
+    const Tile t = find_tile<64>(p.k_offsets, p.sequences, p.k_rows, blockIdx.x / p.kv_heads);
+    if (t.tile >= 0) dkv_short_tile<float, DP, 64>(p, smem, blockIdx.x % p.kv_heads, t);
 }
 
 // ------------------------------------------------------------------- few queries over many keys
@@ -595,12 +742,12 @@ __global__ void __launch_bounds__(Few<DP>::WARPS * 32)
     const int end = static_cast<int>(static_cast<long long>(blocks) * (split + 1) / splits);
     const uint32_t sq = ptx::smem_u32(smem), ring = sq + F::Q_BYTES + warp * (F::STAGES * F::STAGE_BYTES);
     const int chunks = p.D / 8, steps = (p.D + 15) / 16;
-    const Lane<DP> la(lane);
+    const Lane<kRowBytes<T, DP>> la(lane);
     for (int i = threadIdx.x; i < 16 * (DP / 8); i += F::WARPS * 32) {
         const int r = i / (DP / 8), c = i % (DP / 8);
         const int q = (r0 + r) / group, h = hk * group + (r0 + r) - q * group;
         const bool take = r < n && c < chunks;
-        cp_async16(at<DP>(sq, r, c),
+        cp_async16(at<kRowBytes<T, DP>>(sq, r, c),
                    static_cast<const T*>(p.q) + (take ? (static_cast<long long>(t.own.start) + q) * p.q_stride +
                                                             static_cast<long long>(h) * p.D + c * 8 : 0), take);
     }
@@ -639,7 +786,7 @@ __global__ void __launch_bounds__(Few<DP>::WARPS * 32)
         rows_by_rows<T, DP, F::KEYS / 8>(s, sq, kt, steps, la);
         const int last[2] = {min(lim[0], kr.len) - k0, min(lim[1], kr.len) - k0};
         softmax_step<F::KEYS / 8, DP / 8>(s, o, top, sum, last, min(seen_all - k0, F::KEYS), u == 0, c2, lane);
-        weights_by_rows<T, DP, F::KEYS / 8>(o, s, kt + F::STAGE_BYTES / 2, steps, la);
+        weights_by_rows<T, DP, F::KEYS / 8>(o, s, kt + F::STAGE_BYTES / 2, steps, la, lane);
         __syncwarp();
         fetch(u + F::STAGES - 1);
     }

@@ -7,6 +7,12 @@ the value itself:
   - an output rounded once from fp32: u |y|;
   - fp32 arithmetic: E = 2^-20 relative to the sum of the absolute values of the terms (sums of up to
     a few hundred products of 2^-24 each, approximate exponentials of 2^-22);
+  - attention's fp32 products may each be three products of tf32 (11 significant bits): a = h + l with h
+    rounded to nearest, |l| <= 2^-11 |a|; l, cut to 11 bits, loses less than 2^-10 |l| <= 2^-21 |a|.
+    a b - (h h' + h l' + l h') is l l' (2^-22 |a b|) and the two cuts (2^-21 |a b| each): 2.5 * 2^-21 |a b|;
+  - attention's 16-bit forward may take its weights from a polynomial for 2^x of relative error 2^-18.5 (a
+    fit of degree 4 to 2^f on [-1/2, 1/2]): the normaliser and the weights each move by that, which in o
+    adds up to twice as much per term and in lse, the normaliser's logarithm, to once as much;
   - attention weights and ds, rounded to T before their products: u per term, plus half of the
     smallest subnormal of T where T is fp16.
 """
@@ -59,6 +65,8 @@ def attention(q, k, v, do, q_lens, k_lens, heads, kv_heads, causal, scale=None, 
         p_round, ds_round = 0.0, 0.0          # fp32 keeps them unrounded
     else:
         p_round = ds_round = u
+    M = E + 2.5 * 2.0 ** -21 if T == torch.float32 else E      # products
+    X = 0.0 if T == torch.float32 else 2.0 ** -18.5            # the forward's weights
     H, Hk, G = heads, kv_heads, q.shape[2]
     D = q.shape[1] * G // H
     scale = 1 / math.sqrt(D) if scale is None else scale
@@ -74,22 +82,22 @@ def attention(q, k, v, do, q_lens, k_lens, heads, kv_heads, causal, scale=None, 
             g = h // (H // Hk)
             x, y, z, w = Q[q0:q0 + a, h], K[k0:k0 + b, g], V[k0:k0 + b, g], dO[q0:q0 + a, h]
             s = scale * (x @ y.T)
-            s_err = E * scale * (x.abs() @ y.abs().T) + E * s.abs()
+            s_err = M * scale * (x.abs() @ y.abs().T) + E * s.abs()
             s = s.masked_fill(hidden, -math.inf)
             lse = torch.logsumexp(s, 1) if b else torch.full((a,), -math.inf, dtype=torch.float64)
             p = torch.exp(s - torch.where(lse == -math.inf, torch.zeros_like(lse), lse)[:, None])
-            lse_err = (p * s_err).sum(1) + E * (1 + lse.abs())
+            lse_err = (p * s_err).sum(1) + E * (1 + lse.abs()) + X
             p_err = p * (s_err + torch.where(lse == -math.inf, torch.zeros_like(lse), lse_err)[:, None]
                          + E + p_round) + t0 * (p > 0)
             # a row whose weights underflow far below its largest keeps an absolute error only
             o = p @ z
             rows, keys = slice(q0, q0 + a), slice(k0, k0 + b)
             out["o"][rows, h], out["lse"][h, rows] = o, lse
-            bound["o"][rows, h] = p_err @ z.abs() + E * (p @ z.abs()) + u * o.abs() + t0
+            bound["o"][rows, h] = p_err @ z.abs() + (M + X) * (p @ z.abs()) + u * o.abs() + t0
             bound["lse"][h, rows] = lse_err
             ot = o.to(T).double()
             dp, delta = w @ z.T, (w * ot).sum(1)
-            dp_err = E * (w.abs() @ z.abs().T)
+            dp_err = M * (w.abs() @ z.abs().T)
             delta_err = E * (w.abs() * ot.abs()).sum(1)
             ds = p * (dp - delta[:, None])
             p32 = p_err - p * p_round - t0 * (p > 0)             # ds is formed from unrounded weights
@@ -104,9 +112,9 @@ def attention(q, k, v, do, q_lens, k_lens, heads, kv_heads, causal, scale=None, 
             out["dq"][rows, h] = dq
             out["dk"][keys, g] += dk
             out["dv"][keys, g] += dv
-            bound["dq"][rows, h] = scale * (ds_err @ y.abs() + E * ds.abs() @ y.abs()) + u * dq.abs() + t0
-            bound["dk"][keys, g] += scale * (ds_err.T @ x.abs() + E * ds.abs().T @ x.abs()) + t0
-            bound["dv"][keys, g] += p_err.T @ w.abs() + E * (p.T @ w.abs()) + t0
+            bound["dq"][rows, h] = scale * (ds_err @ y.abs() + M * ds.abs() @ y.abs()) + u * dq.abs() + t0
+            bound["dk"][keys, g] += scale * (ds_err.T @ x.abs() + M * ds.abs().T @ x.abs()) + t0
+            bound["dv"][keys, g] += p_err.T @ w.abs() + M * (p.T @ w.abs()) + t0
         q0, k0 = q0 + a, k0 + b
     for n in ("dk", "dv"):
         bound[n] += u * (out[n].abs() + bound[n])

@@ -217,6 +217,35 @@ def test_cross_attention(q_lens, k_lens, H, Hk, D, causal, dtype):
     _check_attention(*_attention(q_lens, k_lens, H, Hk, D, causal, dtype, seed=len(q_lens) + D))
 
 
+@pytest.mark.parametrize("q_lens,k_lens,H,Hk,D,causal", [
+    ([63, 65, 1, 0, 128, 129, 200], None, 6, 3, 64, True), ([49] * 5, None, 8, 8, 128, False),
+    ([385, 2, 640], None, 16, 4, 120, True), ([65], None, 40, 8, 8, False), ([257, 3], None, 20, 20, 72, True),
+    ([10, 0, 130, 3], [0, 20, 50, 400], 12, 6, 128, True), ([200], [70], 12, 4, 48, True),
+    ([5, 9], [0, 0], 20, 20, 64, True), ([0, 0], [5, 9], 20, 10, 64, False), ([20, 70], [130, 61], 38, 2, 40, False),
+])
+def test_fp32_attention_of_many_tiles(q_lens, k_lens, H, Hk, D, causal):
+    """Enough tiles of 64 rows that fp32 goes to the tensor cores."""
+    k_lens = q_lens if k_lens is None else k_lens
+    _check_attention(*_attention(q_lens, k_lens, H, Hk, D, causal, torch.float32, seed=D + H))
+
+
+def test_fp32_not_a_number_stays_in_its_sequence_of_many_tiles():
+    lens, H, D, G = [70, 5, 130], 16, 64, 4
+    n = sum(lens)
+    q, k, v, do = (_randn(n, H * D // G, G, seed=i, dtype=torch.float32) for i in range(4))
+    for t in (q, k, v, do):
+        t[70:75] = float("nan")
+    off = ref.offsets(lens, DEV)
+    kw = dict(heads=H, q_offsets=off, k_offsets=off)
+    q, k, v, do = (t.to(DEV) for t in (q, k, v, do))
+    o, lse = eq.eqlin_attention_forward(q, k, v, **kw)
+    grads = eq.eqlin_attention_backward(do, q, k, v, o, lse, **kw)
+    torch.cuda.synchronize()
+    for t in (o, lse.T, *grads):
+        assert t[70:75].isnan().any()
+        assert torch.isfinite(t[:70]).all() and torch.isfinite(t[75:]).all()
+
+
 @pytest.mark.parametrize("dtype", TYPES)
 def test_attention_with_one_weight_far_above_the_others(dtype):
     """Scores of several hundred: the running maximum moves far, most weights vanish."""
