@@ -298,10 +298,18 @@ __global__ void __launch_bounds__(Bwd<DP>::THREADS, Bwd<DP>::BLOCKS)
         const uint32_t ts = t_s + lanes + half * HB, tdp = t_dp + lanes + half * HB;
         const float c2 = p.scale * kLog2e;
         bool ok = true;
+        // a warp whose 32 keys all lie past the end only keeps the barriers' count
+        const bool idle = t.tile < 0 || r0 + (warp & 3) * 32 >= t.own.len;
+        for (int j = 0; idle && j < n; ++j) {
+            if (!(ok = wait_warp(s_full, j & 1, ctl, p.timeout_ns))) break;
+            arrive_warp(p_full, lane);
+            if (!(ok = wait_warp(dp_full, j & 1, ctl, p.timeout_ns))) break;
+            arrive_warp(ds_full, lane);
+        }
         WalkAt cw = {begin, 0, begin, begin + per_head};
         RingAt<ST> at;
         at.next();                                                 // dO_0
-        for (int j = 0; j < n; ++j) {
+        for (int j = 0; !idle && j < n; ++j) {
             const float* rj = rows + (j % B::ROW_BUFS) * 2 * BN;
             if (!(ok = wait_warp(full(at.s), at.ph, ctl, p.timeout_ns))) break;
             at.next();
@@ -549,7 +557,14 @@ __global__ void __launch_bounds__(Bwd<DP>::THREADS, Bwd<DP>::BLOCKS)
             delta = stat[kTile];
         }
         bool ok = true;
-        for (int j = 0; j < n; ++j) {
+        // a warp whose 32 queries all lie past the end only keeps the barriers' count
+        const bool idle = t.tile < 0 || r0 + (warp & 3) * 32 >= t.own.len;
+        for (int j = 0; idle && j < n; ++j) {
+            if (!(ok = wait_warp(s_full(j & 1), (j >> 1) & 1, ctl, p.timeout_ns))) break;
+            if (!(ok = wait_warp(dp_full, j & 1, ctl, p.timeout_ns))) break;
+            arrive_warp(ds_full, lane);
+        }
+        for (int j = 0; !idle && j < n; ++j) {
             const uint32_t ts = t_s(j) + lanes + half * HB, tdp = t_dp + lanes + half * HB;
             if (!(ok = wait_warp(s_full(j & 1), (j >> 1) & 1, ctl, p.timeout_ns))) break;
             ptx::tc_fence_after();

@@ -468,8 +468,19 @@ __global__ void __launch_bounds__(Fwd<DP, NQ>::THREADS, NQ == 2 ? 1 : 2)
         const float c2 = p.scale * kLog2e;
         float top = -INFINITY, sum = 0.f;
         bool ok = true;
+        // A warp whose 32 rows all lie past the sequence's end only keeps the barriers' count: what its lanes of P
+        // and O hold goes nowhere.
+        const bool idle = t.tile < 0 || r0 + i * kTile + (warp & 3) * 32 >= t.own.len;
         for (int j = 0; j < cnt; ++j) {
             if (!(ok = wait_warp(s_full(i), j & 1, ctl, p.timeout_ns))) break;
+            if (idle) {
+                // never a phase ahead of the other warps: the weights of the tile before have all arrived
+                if (j > 0 && !(ok = wait_warp(o_full(i), (j - 1) & 1, ctl, p.timeout_ns))) break;
+                if (F::OWN_P) arrive_warp(s_read(i), lane);
+                arrive_warp(p_half(i), lane);
+                arrive_warp(p_full(i), lane);
+                continue;
+            }
             ptx::tc_fence_after();
             uint32_t s[4][32];
 #pragma unroll
