@@ -175,6 +175,30 @@ __device__ __forceinline__ void rows_by_rows(float (&acc)[NT][4], uint32_t a_til
         }
     }
 }
+// o[feature tile] += W B for 16-bit weights: w[i] holds rows lane / 4 and lane / 4 + 8 of columns 8 i + 2 (lane & 3)
+// and the next.
+template <class T, int DP, int NT>
+__device__ __forceinline__ void packed_by_rows(float (&o)[DP / 8][4], const uint32_t (&w)[NT][2], uint32_t b_tile, int steps,
+                                               const Lane<kRowBytes<T, DP>>& at) {
+    constexpr int RB = kRowBytes<T, DP>, GROUP = 4;   // pieces of 16 features in flight
+    const uint32_t lb = b_tile + at.a;
+#pragma unroll
+    for (int kb = 0; kb < NT / 2; ++kb) {
+        const uint32_t a[4] = {w[2 * kb][0], w[2 * kb][1], w[2 * kb + 1][0], w[2 * kb + 1][1]};
+#pragma unroll
+        for (int d0 = 0; d0 < DP / 16; d0 += GROUP) {
+            if (d0 >= steps) break;
+            uint32_t b[GROUP][4];
+#pragma unroll
+            for (int d = 0; d < GROUP; ++d) ldm4t(b[d], (lb ^ ((d0 + d) << 5)) + kb * 16 * RB);
+#pragma unroll
+            for (int d = 0; d < GROUP; ++d) {
+                mma16816<T>(o[2 * (d0 + d)], a, b[d][0], b[d][1]);
+                mma16816<T>(o[2 * (d0 + d) + 1], a, b[d][2], b[d][3]);
+            }
+        }
+    }
+}
 // o[feature tile] += W B: W = 16 rows x NT * 8 weights from accumulators (rounded to T where T has 16 bits), B a row
 // tile.  fp32: the accumulator's columns 2 t and 2 t + 1 of 8 stand at k = t and t + 4, so rows 2 t and 2 t + 1 of B
 // are read there.
@@ -211,26 +235,13 @@ __device__ __forceinline__ void weights_by_rows(float (&o)[DP / 8][4], const flo
             }
         }
     } else {
-        const uint32_t lb = b_tile + at.a;
-        constexpr int GROUP = 4;                      // pieces of 16 features in flight
+        uint32_t a[NT][2];
 #pragma unroll
-        for (int kb = 0; kb < NT / 2; ++kb) {
-            const uint32_t a[4] = {Io16<T>::pack(w[2 * kb][0], w[2 * kb][1]), Io16<T>::pack(w[2 * kb][2], w[2 * kb][3]),
-                                   Io16<T>::pack(w[2 * kb + 1][0], w[2 * kb + 1][1]),
-                                   Io16<T>::pack(w[2 * kb + 1][2], w[2 * kb + 1][3])};
-#pragma unroll
-            for (int d0 = 0; d0 < DP / 16; d0 += GROUP) {
-                if (d0 >= steps) break;
-                uint32_t b[GROUP][4];
-#pragma unroll
-                for (int d = 0; d < GROUP; ++d) ldm4t(b[d], (lb ^ ((d0 + d) << 5)) + kb * 16 * RB);
-#pragma unroll
-                for (int d = 0; d < GROUP; ++d) {
-                    mma16816<T>(o[2 * (d0 + d)], a, b[d][0], b[d][1]);
-                    mma16816<T>(o[2 * (d0 + d) + 1], a, b[d][2], b[d][3]);
-                }
-            }
+        for (int i = 0; i < NT; ++i) {
+            a[i][0] = Io16<T>::pack(w[i][0], w[i][1]);
+            a[i][1] = Io16<T>::pack(w[i][2], w[i][3]);
         }
+        packed_by_rows<T, DP, NT>(o, a, b_tile, steps, at);
     }
 }
 
@@ -465,6 +476,43 @@ constexpr size_t short_bwd_smem() {
     return size_t(4) * 64 * kRowBytes<T, DP> + 2 * 64 * sizeof(float);
 }
 
+// Of the warp's 16 rows from `warp_row` on: off = -lse log2(e) and delta = do . o of rows lane / 4 and lane / 4 + 8.
+template <class T, int RB>
+__device__ __forceinline__ void row_stats(const Params& p, int h, long long first_row, int warp_row, int n, int lane,
+                                          float (&off)[2], float (&delta)[2]) {
+    // delta: two lanes a row, each half of its features
+    const int r = warp_row + (lane >> 1);
+    float sum = 0.f;
+    if (r < n) {
+        const T* po = static_cast<const T*>(p.o) + (first_row + r) * p.o_stride + static_cast<long long>(h) * p.D;
+        const T* pd = static_cast<const T*>(p.dout) + (first_row + r) * p.do_stride + static_cast<long long>(h) * p.D;
+#pragma unroll
+        for (int c = 0; c < RB / 32; ++c) {
+            constexpr int PER = 16 / sizeof(T);
+            const int first = (2 * c + (lane & 1)) * PER;
+            if (first >= p.D) break;
+            float a[PER], b[PER];
+            Vec<T, PER>::unpack(Vec<T, PER>::load(po + first), a);
+            Vec<T, PER>::unpack(Vec<T, PER>::load(pd + first), b);
+#pragma unroll
+            for (int e = 0; e < PER; ++e) sum = fmaf(a[e], b[e], sum);
+        }
+    }
+    sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 1);
+    const long long stat = static_cast<long long>(h) * p.q_rows + first_row;
+    if (r < n && !(lane & 1)) p.delta[stat + r] = sum;
+    const int row = warp_row + (lane >> 2);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        delta[i] = __shfl_sync(0xFFFFFFFFu, sum, (lane >> 2) * 2 + 16 * i);
+        off[i] = 0.f;
+        if (row + 8 * i < n) {
+            const float l = p.lse[stat + row + 8 * i];
+            off[i] = l == -INFINITY ? 0.f : -l * kLog2e;        // a row that sees no key: all of it is masked
+        }
+    }
+}
+
 // dq, and delta = do . o of its rows, which the kernel for dk and dv (launched next) reads.
 template <class T, int DP, int M>
 __device__ __forceinline__ void dq_short_tile(const Params& p, uint8_t* smem, int head_block, const Tile& t) {
@@ -492,35 +540,7 @@ __device__ __forceinline__ void dq_short_tile(const Params& p, uint8_t* smem, in
     if (on) {
         copy_tile<T, DP, M, WU * 32>(sq, p.q, p.q_stride, first_row, n, p.D, h, tid);
         copy_tile<T, DP, M, WU * 32>(sdo, p.dout, p.do_stride, first_row, n, p.D, h, tid);
-        // delta: two lanes a row, each half of its features
-        const int r = rw * 16 + (lane >> 1);
-        float sum = 0.f;
-        if (r < n) {
-            const T* po = static_cast<const T*>(p.o) + (first_row + r) * p.o_stride + static_cast<long long>(h) * p.D;
-            const T* pd = static_cast<const T*>(p.dout) + (first_row + r) * p.do_stride + static_cast<long long>(h) * p.D;
-#pragma unroll
-            for (int c = 0; c < RB / 32; ++c) {
-                constexpr int PER = 16 / sizeof(T);
-                const int first = (2 * c + (lane & 1)) * PER;
-                if (first >= p.D) break;
-                float a[PER], b[PER];
-                Vec<T, PER>::unpack(Vec<T, PER>::load(po + first), a);
-                Vec<T, PER>::unpack(Vec<T, PER>::load(pd + first), b);
-#pragma unroll
-                for (int e = 0; e < PER; ++e) sum = fmaf(a[e], b[e], sum);
-            }
-        }
-        sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 1);
-        const long long stat = static_cast<long long>(h) * p.q_rows + first_row;
-        if (r < n && !(lane & 1)) p.delta[stat + r] = sum;
-        delta[0] = __shfl_sync(0xFFFFFFFFu, sum, (lane >> 2) * 2);
-        delta[1] = __shfl_sync(0xFFFFFFFFu, sum, (lane >> 2) * 2 + 16);
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-            if (row + 8 * i < n) {
-                const float l = p.lse[stat + row + 8 * i];
-                off[i] = l == -INFINITY ? 0.f : -l * kLog2e;    // a row that sees no key: all of it is masked
-            }
+        row_stats<T, RB>(p, h, first_row, rw * 16, n, lane, off, delta);
     }
     for (int k0 = 0; k0 < seen; k0 += M) {
         const int kn = min(M, kr.len - k0);
@@ -560,6 +580,169 @@ __device__ __forceinline__ void dq_short_tile(const Params& p, uint8_t* smem, in
     store_rows<T, DP>(dq, mul, sq, rw * 16, n, p.D,
                       static_cast<T*>(p.dq) + first_row * p.dq_stride + static_cast<long long>(h) * p.D, p.dq_stride, lane);
 }
+// o[feature tile] += W^T B over the n rows of W (16-bit weights, one row of RB bytes each, columns rw * 16 on) and of
+// B (a row tile).
+template <class T, int DP, int M>
+__device__ __forceinline__ void columns_by_rows(float (&o)[DP / 8][4], uint32_t w_tile, int rw, uint32_t b_tile, int n,
+                                                int steps, const Lane<kRowBytes<T, DP>>& at) {
+    constexpr int RB = kRowBytes<T, DP>, GROUP = 4;
+    const uint32_t lw = (w_tile + at.b) ^ (rw << 5), lb = b_tile + at.a;
+#pragma unroll
+    for (int kb = 0; kb < M / 16; ++kb) {
+        if (kb * 16 >= n) break;
+        uint32_t a[4];
+        ldm4t(a, lw + kb * 16 * RB);
+#pragma unroll
+        for (int d0 = 0; d0 < DP / 16; d0 += GROUP) {
+            if (d0 >= steps) break;
+            uint32_t b[GROUP][4];
+#pragma unroll
+            for (int d = 0; d < GROUP; ++d) ldm4t(b[d], (lb ^ ((d0 + d) << 5)) + kb * 16 * RB);
+#pragma unroll
+            for (int d = 0; d < GROUP; ++d) {
+                mma16816<T>(o[2 * (d0 + d)], a, b[d][0], b[d][1]);
+                mma16816<T>(o[2 * (d0 + d) + 1], a, b[d][2], b[d][3]);
+            }
+        }
+    }
+}
+
+// Whether a sequence's gradients are all computed from one tile: one head of keys for each of queries, and no more
+// than M rows on either side.
+template <int M>
+__device__ __forceinline__ bool one_tile(const Params& p, int queries, int keys) {
+    return p.heads == p.kv_heads && queries > 0 && queries <= M && keys > 0 && keys <= M;
+}
+
+// All gradients of one head of a sequence of one tile: the scores and the weights are computed once, by warps that
+// own 16 queries; the weights and ds go to shared memory (over V and K, which are then done with), for warps
+// that own 16 keys.
+template <class T, int DP, int M>
+__device__ __forceinline__ void bwd_one_tile(const Params& p, uint8_t* smem, int head_block, const Tile& t, const Rows& kr) {
+    constexpr int RB = kRowBytes<T, DP>, U = 64 / M, WU = 4 / U, NT = M / 8;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int unit = warp / WU, rw = warp % WU;
+    const int h = head_block * U + unit;
+    const int n = t.own.len, kn = kr.len;
+    const bool on = h < p.heads, work = on && rw * 16 < n, key_work = on && rw * 16 < kn;
+    const uint32_t sq = ptx::smem_u32(smem) + unit * (4 * M * RB), sdo = sq + M * RB, sk = sdo + M * RB,
+                   sv = sk + M * RB;
+    const int tid = threadIdx.x - unit * WU * 32;
+    const Lane<RB> la(lane);
+    const int steps = (p.D * static_cast<int>(sizeof(T)) + 31) / 32;
+    const float c2 = p.scale * kLog2e;
+    const int row = rw * 16 + (lane >> 2);
+    const long long first_row = t.own.start, first_key = kr.start, col = static_cast<long long>(h) * p.D;
+    // two lanes a row for delta: their half of the row of O is on its way while the scores are computed
+    const int dr = rw * 16 + (lane >> 1);
+    uint4 o[RB / 32];
+    float off[2] = {0.f, 0.f};
+    if (on) {
+        copy_tile<T, DP, M, WU * 32>(sq, p.q, p.q_stride, first_row, n, p.D, h, tid);
+        copy_tile<T, DP, M, WU * 32>(sk, p.k, p.k_stride, first_key, kn, p.D, h, tid);
+    }
+    cp_async_commit();
+    if (on) {
+        copy_tile<T, DP, M, WU * 32>(sdo, p.dout, p.do_stride, first_row, n, p.D, h, tid);
+        copy_tile<T, DP, M, WU * 32>(sv, p.v, p.v_stride, first_key, kn, p.D, h, tid);
+    }
+    cp_async_commit();
+    const T* po = static_cast<const T*>(p.o) + (first_row + dr) * p.o_stride + col;
+#pragma unroll
+    for (int c = 0; c < RB / 32; ++c) {
+        const int first = (2 * c + (lane & 1)) * 8;
+        o[c] = on && dr < n && first < p.D ? __ldg(reinterpret_cast<const uint4*>(po + first)) : make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        if (on && row + 8 * i < n) {
+            const float l = p.lse[static_cast<long long>(h) * p.q_rows + first_row + row + 8 * i];
+            off[i] = l == -INFINITY ? 0.f : -l * kLog2e;        // a row that sees no key: all of it is masked
+        }
+    float s[NT][4], dp[NT][4];
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[i][e] = dp[i][e] = 0.f;
+    cp_async_wait<1>();
+    __syncthreads();
+    if (work) rows_by_rows<T, DP, NT>(s, sq + rw * 16 * RB, sk, steps, la);
+    cp_async_wait<0>();
+    __syncthreads();
+    float dq[DP / 8][4], acc[DP / 8][4];
+    uint32_t w[NT][2], ds[NT][2];
+    if (work) {
+        float sum = 0.f, delta[2];
+#pragma unroll
+        for (int c = 0; c < RB / 32; ++c) {
+            uint4 d;
+            asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                         : "=r"(d.x), "=r"(d.y), "=r"(d.z), "=r"(d.w)
+                         : "r"(at<RB>(sdo, dr, 2 * c + (lane & 1)))
+                         : "memory");
+            float a[8], b[8];
+            Vec<T, 8>::unpack(o[c], a);
+            Vec<T, 8>::unpack(d, b);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) sum = fmaf(a[e], b[e], sum);
+        }
+        sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 1);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) delta[i] = __shfl_sync(0xFFFFFFFFu, sum, (lane >> 2) * 2 + 16 * i);
+        rows_by_rows<T, DP, NT>(dp, sdo + rw * 16 * RB, sv, steps, la);
+        int last[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) last[i] = min(kn, p.causal ? row + 8 * i + 1 + kn - n : kn);
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const bool vis = i * 8 + (lane & 3) * 2 + (e & 1) < last[e >> 1];
+                s[i][e] = vis ? ex2(fmaf(s[i][e], c2, off[e >> 1])) : 0.f;
+                dp[i][e] = vis ? s[i][e] * (dp[i][e] - delta[e >> 1]) : 0.f;
+            }
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                w[i][e] = Io16<T>::pack(s[i][2 * e], s[i][2 * e + 1]);
+                ds[i][e] = Io16<T>::pack(dp[i][2 * e], dp[i][2 * e + 1]);
+            }
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < NT; ++i) w[i][0] = w[i][1] = ds[i][0] = ds[i][1] = 0;
+    }
+#pragma unroll
+    for (int d = 0; d < DP / 8; ++d) dq[d][0] = dq[d][1] = dq[d][2] = dq[d][3] = 0.f;
+    if (work) packed_by_rows<T, DP, NT>(dq, ds, sk, steps, la);
+    __syncthreads();
+    if (work) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const uint32_t pw = at<RB>(sv, row + 8 * e, 0) + (lane & 3) * 4, pds = at<RB>(sk, row + 8 * e, 0) + (lane & 3) * 4;
+#pragma unroll
+            for (int i = 0; i < NT; ++i) {
+                asm volatile("st.shared.b32 [%0], %1;" ::"r"(pw ^ (i << 4)), "r"(w[i][e]) : "memory");
+                asm volatile("st.shared.b32 [%0], %1;" ::"r"(pds ^ (i << 4)), "r"(ds[i][e]) : "memory");
+            }
+        }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int d = 0; d < DP / 8; ++d) acc[d][0] = acc[d][1] = acc[d][2] = acc[d][3] = 0.f;
+    if (key_work) columns_by_rows<T, DP, M>(acc, sv, rw, sdo, n, steps, la);
+    __syncthreads();
+    const float mul[2] = {p.scale, p.scale}, one[2] = {1.f, 1.f};
+    // over the weights and dO, which all warps are done with; each warp in its own rows
+    if (work) store_rows<T, DP>(dq, mul, sv, rw * 16, n, p.D, static_cast<T*>(p.dq) + first_row * p.dq_stride + col, p.dq_stride, lane);
+    if (key_work) {
+        store_rows<T, DP>(acc, one, sdo, rw * 16, kn, p.D, static_cast<T*>(p.dv) + first_key * p.dv_stride + col, p.dv_stride, lane);
+#pragma unroll
+        for (int d = 0; d < DP / 8; ++d) acc[d][0] = acc[d][1] = acc[d][2] = acc[d][3] = 0.f;
+        columns_by_rows<T, DP, M>(acc, sk, rw, sq, n, steps, la);
+        __syncwarp();
+        store_rows<T, DP>(acc, mul, sdo, rw * 16, kn, p.D, static_cast<T*>(p.dk) + first_key * p.dk_stride + col, p.dk_stride, lane);
+    }
+}
 template <class T, int DP, int M>
 __global__ void __launch_bounds__(kShortThreads, DP == 128 ? 3 : 4) eqlin_attn_dq_short_kernel(const Params p) {
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -567,8 +750,11 @@ __global__ void __launch_bounds__(kShortThreads, DP == 128 ? 3 : 4) eqlin_attn_d
     ptx::grid_dependency_wait();
     constexpr int U = 64 / M;
     const int n_hb = (p.heads + U - 1) / U;
-    for_short_tiles<M>(p.q_offsets, p.sequences, p.q_rows, blockIdx.x / n_hb,
-                       [&](const Tile& t) { dq_short_tile<T, DP, M>(p, smem, blockIdx.x % n_hb, t); });
+    for_short_tiles<M>(p.q_offsets, p.sequences, p.q_rows, blockIdx.x / n_hb, [&](const Tile& t) {
+        const Rows kr = other_rows(p, t, p.k_offsets, p.k_rows);
+        if (one_tile<M>(p, t.own.len, kr.len)) bwd_one_tile<T, DP, M>(p, smem, blockIdx.x % n_hb, t, kr);
+        else dq_short_tile<T, DP, M>(p, smem, blockIdx.x % n_hb, t);
+    });
 }
 
 // dk and dv: a warp owns 16 keys; the query rows that see the tile pass by, for each head of the group.
@@ -664,8 +850,10 @@ __global__ void __launch_bounds__(kShortThreads, DP == 128 ? 2 : 4) eqlin_attn_d
     ptx::grid_dependency_wait();
     constexpr int U = 64 / M;
     const int n_hb = (p.kv_heads + U - 1) / U;
-    for_short_tiles<M>(p.k_offsets, p.sequences, p.k_rows, blockIdx.x / n_hb,
-                       [&](const Tile& t) { dkv_short_tile<T, DP, M>(p, smem, blockIdx.x % n_hb, t); });
+    for_short_tiles<M>(p.k_offsets, p.sequences, p.k_rows, blockIdx.x / n_hb, [&](const Tile& t) {
+        const Rows qr = other_rows(p, t, p.q_offsets, p.q_rows);
+        if (!one_tile<M>(p, qr.len, t.own.len)) dkv_short_tile<T, DP, M>(p, smem, blockIdx.x % n_hb, t);
+    });
 }
 
 // fp32 of every length: a block for each tile of 64 rows and head.  The kernels are bound by the three tf32
