@@ -119,8 +119,8 @@ int tc_grid(int64_t rows, int64_t sequences, int m, int64_t heads, unsigned* gri
 
 // The same for the kernels of short sequences.
 template <int M>
-int short_grid(int64_t rows, int64_t sequences, int64_t head_blocks, unsigned* grid) {
-    const int64_t n = attn::mma::short_blocks<M>(rows, sequences) * head_blocks;
+int short_grid(int64_t rows, int64_t sequences, int64_t head_blocks, unsigned* grid, int64_t per = 1) {
+    const int64_t n = attn::mma::short_blocks<M>(rows, sequences, per) * head_blocks;
     if (n >= (int64_t(1) << 31)) return report(EQLIN_ERR_UNSUPPORTED, "too many rows, sequences and heads for one call");
     *grid = static_cast<unsigned>(n);
     return EQLIN_OK;
@@ -373,13 +373,17 @@ int backward_short_m(const attn::Params& p, cudaStream_t st) {
     constexpr int U = 64 / M;
     unsigned grid_q = 0, grid_k = 0;
     int s = short_grid<M>(p.q_rows, p.sequences, (p.heads + U - 1) / U, &grid_q);
-    if (s == EQLIN_OK) s = short_grid<M>(p.k_rows, p.sequences, (p.kv_heads + U - 1) / U, &grid_k);
+    // sequences to a block of the second launch, which skips those of one tile: as many as leave the SMs several
+    // blocks each
+    const int64_t hb = (p.kv_heads + U - 1) / U;
+    const int per = p.heads != p.kv_heads ? 1 : static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(32, p.sequences * hb / (4 * kB200Sms))));
+    if (s == EQLIN_OK) s = short_grid<M>(p.k_rows, p.sequences, hb, &grid_k, per);
     if (s == EQLIN_OK && p.q_rows > 0)
         s = launch(mma::eqlin_attn_dq_short_kernel<T, DP, M>, dim3(grid_q), dim3(mma::kShortThreads),
                    mma::short_bwd_smem<T, DP>(), st, "attention gradient launch", p);
     if (s == EQLIN_OK && p.k_rows > 0)
         s = launch(mma::eqlin_attn_dkv_short_kernel<T, DP, M>, dim3(grid_k), dim3(mma::kShortThreads),
-                   mma::short_bwd_smem<T, DP>(), st, "attention gradient launch", p);
+                   mma::short_bwd_smem<T, DP>(), st, "attention gradient launch", p, per);
     return s;
 }
 template <class T, int DP>

@@ -302,8 +302,18 @@ constexpr int kShortThreads = 128;
 // kLaterSlots of them each.
 constexpr int kLaterSlots = 8;
 template <int M>
-__host__ __device__ constexpr long long short_blocks(long long rows, long long sequences) {
-    return sequences + (rows / M + kLaterSlots - 1) / kLaterSlots;
+__host__ __device__ constexpr long long short_blocks(long long rows, long long sequences, long long per = 1) {
+    return (sequences + per - 1) / per + (rows / M + kLaterSlots - 1) / kLaterSlots;
+}
+template <int M, class F>
+__device__ __forceinline__ void later_tiles(const int32_t* offsets, int sequences, int rows, int block, F&& f) {
+    const int first = block * kLaterSlots + 1;
+    for (int slot = first; slot < first + kLaterSlots && slot <= rows / M; ++slot) {
+        const Tile t = find_tile<M, true>(offsets, sequences, rows, slot);
+        if (t.tile < 0) continue;
+        f(t);
+        __syncthreads();   // the next tile takes the same shared memory
+    }
 }
 template <int M, class F>
 __device__ __forceinline__ void for_short_tiles(const int32_t* offsets, int sequences, int rows, int block, F&& f) {
@@ -315,13 +325,7 @@ __device__ __forceinline__ void for_short_tiles(const int32_t* offsets, int sequ
         if (t.own.len > 0) f(t);
         return;
     }
-    const int first = (block - sequences) * kLaterSlots + 1;
-    for (int slot = first; slot < first + kLaterSlots && slot <= rows / M; ++slot) {
-        const Tile t = find_tile<M, true>(offsets, sequences, rows, slot);
-        if (t.tile < 0) continue;
-        f(t);
-        __syncthreads();   // the next tile takes the same shared memory
-    }
+    later_tiles<M>(offsets, sequences, rows, block - sequences, f);
 }
 template <class T, int DP>
 constexpr size_t short_smem() {
@@ -843,17 +847,36 @@ __device__ __forceinline__ void dkv_short_tile(const Params& p, uint8_t* smem, i
     store_rows<T, DP>(dk, mul, sk, rw * 16, n, p.D, static_cast<T*>(p.dk) + first_row * p.dk_stride + col, p.dk_stride, lane);
     store_rows<T, DP>(dv, one, sv, rw * 16, n, p.D, static_cast<T*>(p.dv) + first_row * p.dv_stride + col, p.dv_stride, lane);
 }
+// `per` (at most 32) sequences' first tiles to a block: most have been done by bwd_one_tile, and a block of this kernel
+// that finds nothing to do costs as much as its launch (windows of 49, 4096 sequences, 3 heads of 128: 41 us in
+// 13.5 thousand blocks).
 template <class T, int DP, int M>
-__global__ void __launch_bounds__(kShortThreads, DP == 128 ? 2 : 4) eqlin_attn_dkv_short_kernel(const Params p) {
+__global__ void __launch_bounds__(kShortThreads, DP == 128 ? 2 : 4) eqlin_attn_dkv_short_kernel(const Params p, int per) {
     extern __shared__ __align__(1024) uint8_t smem[];
     ptx::grid_launch_dependents();
     ptx::grid_dependency_wait();
     constexpr int U = 64 / M;
-    const int n_hb = (p.kv_heads + U - 1) / U;
-    for_short_tiles<M>(p.k_offsets, p.sequences, p.k_rows, blockIdx.x / n_hb, [&](const Tile& t) {
-        const Rows qr = other_rows(p, t, p.q_offsets, p.q_rows);
-        if (!one_tile<M>(p, qr.len, t.own.len)) dkv_short_tile<T, DP, M>(p, smem, blockIdx.x % n_hb, t);
-    });
+    const int n_hb = (p.kv_heads + U - 1) / U, block = blockIdx.x / n_hb, hb = blockIdx.x % n_hb;
+    const int first_blocks = (p.sequences + per - 1) / per;
+    if (block < first_blocks) {
+        const int lane = threadIdx.x & 31, b = block * per + lane;
+        bool todo = lane < per && b < p.sequences;
+        if (todo) {
+            const Rows kr = sequence_rows(p.k_offsets, b, p.k_rows), qr = sequence_rows(p.q_offsets, b, p.q_rows);
+            todo = kr.len > 0 && !one_tile<M>(p, qr.len, kr.len);
+        }
+        for (unsigned left = __ballot_sync(0xFFFFFFFFu, todo); left; left &= left - 1) {
+            Tile t;
+            t.b = block * per + __ffs(left) - 1;
+            t.own = sequence_rows(p.k_offsets, t.b, p.k_rows);
+            t.tile = 0;
+            dkv_short_tile<T, DP, M>(p, smem, hb, t);
+            __syncthreads();   // the next tile takes the same shared memory
+        }
+        return;
+    }
+    later_tiles<M>(p.k_offsets, p.sequences, p.k_rows, block - first_blocks,
+                   [&](const Tile& t) { dkv_short_tile<T, DP, M>(p, smem, hb, t); });
 }
 
 // fp32 of every length: a block for each tile of 64 rows and head.  The kernels are bound by the three tf32

@@ -229,6 +229,23 @@ def test_fp32_attention_of_many_tiles(q_lens, k_lens, H, Hk, D, causal):
     _check_attention(*_attention(q_lens, k_lens, H, Hk, D, causal, torch.float32, seed=D + H))
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("n,most,H,Hk,D,causal,other", [
+    (700, 64, 2, 2, 64, False, False), (650, 49, 2, 2, 128, True, True), (3000, 16, 1, 1, 8, False, True),
+    (1300, 30, 2, 2, 24, True, False), (700, 60, 4, 2, 16, False, True),
+])
+def test_many_short_sequences(n, most, H, Hk, D, causal, other, dtype):
+    """Mostly one tile each, with empty and longer ones between them; keys of other lengths than the queries'."""
+    g = torch.Generator().manual_seed(n + D)
+    lens = lambda: torch.randint(0, most + 1, (n,), generator=g).tolist()
+    q_lens = lens()
+    k_lens = lens() if other else list(q_lens)
+    for i in (3, n // 2, n - 1):                      # each longer than a tile on one side or both
+        q_lens[i] = 70 if i != 3 or not other else 5
+        k_lens[i] = 131 if other else q_lens[i]
+    _check_attention(*_attention(q_lens, k_lens, H, Hk, D, causal, dtype, seed=n))
+
+
 def test_fp32_not_a_number_stays_in_its_sequence_of_many_tiles():
     lens, H, D, G = [70, 5, 130], 16, 64, 4
     n = sum(lens)
