@@ -156,21 +156,40 @@ int forward_tc(attn::tc::FwdParams fp, int io, cudaStream_t st) {
 // ------------------------------------------------------------------------ choice of the forward
 enum class Fwd { kTiles, kShort, kFew };
 
+constexpr int kB200Sms = 148;   // the plans do not depend on the device, so that sizes need none
+
 // By the average lengths, which the host knows (the single ones are device data); every kernel is right
-// for every length.
-//   few    at most 16 packed rows (queries times heads of a key head) a sequence and keys enough to
-//          split: the keys are read once for all heads of the group, by all SMs.
-//   short  at most 64 rows a sequence on both sides.
-//   tiles  the rest.
+// for every length.  Measured in bf16, us, 8 heads unless said otherwise.
+//   few    tiles of 16 packed rows (queries times heads of a key head), keys split over the SMs.  Taken
+//          - where its tiles do not fill the SMs and the keys can be split: 32 queries over 4096 keys, 8 sequences,
+//            64 features: 21, tiles 39, short 83; 512 keys: 8.6, 11, 15;
+//          - where packing reads the keys several times less often: 8 queries, 2 key heads, 512 keys, 64
+//            sequences: 12.7, short 17, tiles 19; 2048 keys: 24, 54, 46.  Below 512 keys its join costs more: 128
+//            keys, 256 sequences, 8 queries 29, short 19, but 1 query 15, 19;
+//          - for up to 16 packed rows over long keys: 1 query, 2048 keys, 64 sequences, 128 features 95, short 95,
+//            tiles 118.
+//   short  tiles of 64 rows without a pipeline over the keys, several blocks to an SM.  Up to 64 rows on both sides
+//          (49, 4096 sequences, 3 heads of 128 features: 143, tiles 539); with blocks enough also up to 128 (128,
+//          1024 sequences, 3 heads of 128: 138, tiles 175; 192: 195, 177; but 16 sequences of 4 heads: 21, 6.6), or
+//          512 keys for 64 queries (512 keys, 64 sequences, 64 queries: 25, tiles 27; 2048: 93, 68).
+//   tiles  the rest: tcgen05.
 Fwd forward_kind(const eqlin_attention_shape& a) {
-    const int64_t group = a.heads / a.kv_heads;
     if (a.io_dtype == EQLIN_F32) return Fwd::kTiles;
-    if (a.q_rows * group <= 16 * a.sequences && a.k_rows >= 128 * a.sequences) return Fwd::kFew;
-    if (a.q_rows <= 64 * a.sequences && a.k_rows <= 64 * a.sequences) return Fwd::kShort;
+    const int64_t n = a.sequences, packed = a.q_rows * (a.heads / a.kv_heads);
+    const int64_t few_tiles = std::max(n, (packed + 15) / 16) * a.kv_heads;     // blocks without splits
+    const int64_t short_tiles = std::max(n, (a.q_rows + 63) / 64) * a.heads;
+    if (a.k_rows >= 128 * n) {
+        const bool longer = a.k_rows >= 512 * n;
+        if (few_tiles <= kB200Sms && (packed <= 16 * n || (packed <= 128 * n && longer))) return Fwd::kFew;
+        if (few_tiles * (longer ? 2 : 4) <= short_tiles) return Fwd::kFew;
+        if (packed <= 16 * n && a.k_rows >= 1024 * n) return Fwd::kFew;
+    }
+    if (a.q_rows <= 64 * n && a.k_rows <= 64 * n) return Fwd::kShort;
+    if (short_tiles >= 3 * kB200Sms &&
+        ((a.q_rows <= 128 * n && a.k_rows <= 128 * n) || (a.q_rows <= 64 * n && a.k_rows <= 512 * n)))
+        return Fwd::kShort;
     return Fwd::kTiles;
 }
-
-constexpr int kB200Sms = 148;   // the plan does not depend on the device, so that sizes need none
 
 // fp32: 16-row tiles on the CUDA cores, with split keys in the forward, where few tiles of 64 rows would be left
 // for the tensor cores.  Measured, 64 features, CUDA cores / tensor cores: 16 tiles (256 tokens, 4 heads) forward
@@ -207,13 +226,19 @@ int forward_splits(const eqlin_attention_shape& a) {
     return static_cast<int>(std::max<int64_t>(1, std::min({room / std::max<int64_t>(units, 1), keys / 256, int64_t(64)})));
 }
 
-// The gradients of sequences of up to 64 rows on average use 16-row products.
-bool backward_short_rows(int64_t q_rows, int64_t k_rows, int64_t sequences) {
-    return std::max(q_rows, k_rows) <= 64 * sequences;
+// 16-bit gradients by 16-row products: up to 64 rows on both sides (49, 4096 sequences, 3 heads of 128 features: 326
+// us, tcgen05 tiles 1241; 96: 846, 796).  With blocks enough, also few queries over more keys, which leave the tiles of
+// 128 empty: up to 64 over 128 keys (64 queries, 256 sequences, 8 heads of 64: 107 us, tiles 136), and up to
+// 32 where key heads are not shared (1 query, 2048 keys, 64 sequences, 8 heads of 64: 230, 280; of 2 key heads:
+// 177, 146; 8 sequences of 4096 keys: 171, 101).
+bool backward_short_rows(int64_t q_rows, int64_t k_rows, int64_t n, int64_t heads, int64_t kv_heads) {
+    if (std::max(q_rows, k_rows) <= 64 * n) return true;
+    return n * heads >= 3 * kB200Sms && q_rows <= 64 * n &&
+           (k_rows <= 128 * n || (heads == kv_heads && q_rows <= 32 * n));
 }
 
 size_t backward_workspace(const eqlin_attention_shape& a) {
-    if (a.io_dtype == EQLIN_F32 || backward_short_rows(a.q_rows, a.k_rows, a.sequences))
+    if (a.io_dtype == EQLIN_F32 || backward_short_rows(a.q_rows, a.k_rows, a.sequences, a.heads, a.kv_heads))
         return size_t(a.q_rows) * size_t(a.heads) * sizeof(float);
     return size_t(a.q_rows / attn::tc::kTile + a.sequences) * size_t(a.heads) * 2 * attn::tc::kTile * sizeof(float);
 }
@@ -396,7 +421,7 @@ int backward_short(const attn::Params& p, cudaStream_t st) {
 
 template <class T>
 int backward_16(attn::Params& p, int io, cudaStream_t st) {
-    if (backward_short_rows(p.q_rows, p.k_rows, p.sequences))
+    if (backward_short_rows(p.q_rows, p.k_rows, p.sequences, p.heads, p.kv_heads))
         return p.D <= 64 ? backward_short<T, 64>(p, st) : backward_short<T, 128>(p, st);
     p.timeout_ns = wait_timeout_ns();
     const attn::tc::BwdParams bp = {p, stop_after()};

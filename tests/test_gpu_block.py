@@ -246,6 +246,20 @@ def test_many_short_sequences(n, most, H, Hk, D, causal, other, dtype):
     _check_attention(*_attention(q_lens, k_lens, H, Hk, D, causal, dtype, seed=n))
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("n,q_most,k_most,H,Hk,D,causal", [
+    (60, 140, 0, 8, 8, 64, True), (57, 120, 0, 8, 2, 128, False),      # self-attention over about one and two tiles
+    (60, 33, 500, 8, 8, 40, True), (60, 60, 400, 8, 4, 128, False),    # few tiles of queries over several of keys
+    (70, 1, 900, 16, 2, 64, False), (64, 16, 700, 8, 8, 128, True),    # packed heads; one and a few queries
+    (3, 40, 1500, 6, 2, 72, True), (2, 100, 1200, 4, 4, 64, False),    # split keys for more than 16 packed rows
+])
+def test_attention_of_many_tiles(n, q_most, k_most, H, Hk, D, causal, dtype):
+    g = torch.Generator().manual_seed(n + D)
+    q_lens = torch.randint(0, q_most + 1, (n,), generator=g).tolist() if q_most > 1 else [1] * n
+    k_lens = torch.randint(k_most // 2, k_most + 1, (n,), generator=g).tolist() if k_most else q_lens
+    _check_attention(*_attention(q_lens, k_lens, H, Hk, D, causal, dtype, seed=n))
+
+
 def test_fp32_not_a_number_stays_in_its_sequence_of_many_tiles():
     lens, H, D, G = [70, 5, 130], 16, 64, 4
     n = sum(lens)
