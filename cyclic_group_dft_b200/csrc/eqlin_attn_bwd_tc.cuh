@@ -10,6 +10,10 @@
 // atomics or the fp32 copy of dq that one kernel needs.
 // Warps: two warpgroups of 128 threads for the elementwise work (thread = TMEM lane; each warpgroup
 // takes half of the columns, and its words of the A operand lie at the start of them), one warp of loads, one of MMAs.
+//
+// Bound by the chain of each tile (scores, weights, products), which the other tiles in flight overlap in part.  8192
+// tokens: 6 heads of 128 features 584 us (880 TFLOP/s counting 5 products), 8 heads of 64 542 us (633); 784 tokens, 32
+// sequences, 8 heads of 64: 240 us, tensor cores busy 36 to 38 %, instructions issued in 40 to 42 % of the cycles.
 #pragma once
 
 #include "eqlin_attn_tc.cuh"
@@ -20,7 +24,7 @@ namespace tc {
 
 // BN: rows of a tile of the side that is walked.  For heads of up to 64 features it is 64: then a block needs
 // half of the TMEM, and the chain of products and elementwise work of one block on an SM fills the gaps of the
-// other's.
+// other's (784 tokens, 32 sequences, 8 heads: 239 us; one block of four warpgroups with BN = 128: 342).
 template <int DP>
 struct Bwd {
     static constexpr int BN = DP;

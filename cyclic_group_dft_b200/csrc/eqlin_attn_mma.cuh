@@ -5,8 +5,8 @@
 //   fp32 I/O of more than a few tiles, each product as three of tf32: with hi = tf32(v) (rounded to nearest) and
 //   lo = v - hi (exact, at most 2^-11 |v|), a b = hi hi + hi lo + lo hi but for lo lo and what the tensor core
 //   cuts off lo: 2.5 * 2^-21 |a b| at most.  Bound by the tensor cores' tf32 rate, a third of it, and by the
-//   splitting; against CUDA cores: 784 tokens, 8 sequences, 8 heads of 64 features forward 322 to 244 us,
-//   gradients 1056 to 784; 4096 tokens, 4 heads of 128 1060 to 731 and 3530 to 3333.  (Each small product
+//   splitting; against CUDA cores: 784 tokens, 8 sequences, 8 heads of 64 features forward 322 to 228 us,
+//   gradients 1056 to 783; 4096 tokens, 4 heads of 128 1060 to 741 and 3530 to 2995.  (Each small product
 //   behind the last on the same accumulator: 262 and 929, 916 and 4781.)
 //
 // Tiles in shared memory are rows of DP features; the 16-byte chunk c of row r lies at chunk
@@ -69,6 +69,10 @@ struct Split {
         lo = __float_as_uint(__uint_as_float(v) - __uint_as_float(hi));
     }
 };
+// The tensor cores cut the low bits of an accumulator at each product, always towards zero, which adds up: over 8192
+// keys to 1.5e-5 of o.  So sums of kExact pieces of 8 start from zero and are then added in fp32: o is within 6e-7,
+// where a plain fp32 computation has 1.6e-6 (pieces of 64: 1.0e-6, and with more registers 843 for 783 us of gradients).
+constexpr int kExact = 4;
 // d[i] += a b[i] in fp32 precision for N tiles of 8 columns: the small products first, and each of the three over
 // all tiles before the next, so that no product waits for the one before it.
 template <int N>
@@ -133,26 +137,36 @@ __device__ __forceinline__ void rows_by_rows(float (&acc)[NT][4], uint32_t a_til
     constexpr int RB = kRowBytes<T, DP>;
     const uint32_t la = a_tile + at.a, lb = b_tile + at.b;
     if constexpr (sizeof(T) == 4) {
-#pragma unroll 2
-        for (int ks = 0; ks < steps; ++ks) {
-            uint32_t a[4], ah[4], al[4], b[NT][2];
-            ldm4(a, la ^ (ks << 5));
+#pragma unroll 1
+        for (int k0 = 0; k0 < steps; k0 += kExact) {
+            float part[NT][4];
 #pragma unroll
-            for (int n = 0; n < NT; n += 2) {
-                uint32_t r[4];
-                ldm4(r, (lb ^ (ks << 5)) + n * 8 * RB);
-                b[n][0] = r[0];
-                b[n][1] = r[1];
-                b[n + 1][0] = r[2];
-                b[n + 1][1] = r[3];
+            for (int n = 0; n < NT; ++n) part[n][0] = part[n][1] = part[n][2] = part[n][3] = 0.f;
+#pragma unroll
+            for (int ks = k0; ks < k0 + kExact; ++ks) {      // (past the head's features: zeros)
+                uint32_t a[4], ah[4], al[4], b[NT][2];
+                ldm4(a, la ^ (ks << 5));
+#pragma unroll
+                for (int n = 0; n < NT; n += 2) {
+                    uint32_t r[4];
+                    ldm4(r, (lb ^ (ks << 5)) + n * 8 * RB);
+                    b[n][0] = r[0];
+                    b[n][1] = r[1];
+                    b[n + 1][0] = r[2];
+                    b[n + 1][1] = r[3];
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const Split v(a[e]);
+                    ah[e] = v.hi;
+                    al[e] = v.lo;
+                }
+                mma_f32<NT>(part, ah, al, b);
             }
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const Split v(a[e]);
-                ah[e] = v.hi;
-                al[e] = v.lo;
-            }
-            mma_f32<NT>(acc, ah, al, b);
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[n][e] += part[n][e];
         }
     } else {
         // the next pieces are on their way while these are multiplied
@@ -211,27 +225,37 @@ __device__ __forceinline__ void weights_by_rows(float (&o)[DP / 8][4], const flo
         const int t2 = (lane & 3) * 2, in = (lane >> 2) & 3, up = lane >> 4;
         const uint32_t row0 = b_tile + t2 * RB + ((up ^ t2) << 4) + in * 4;
         const uint32_t row1 = b_tile + (t2 + 1) * RB + ((up ^ (t2 + 1)) << 4) + in * 4;
+        constexpr int GROUP = 4;                      // tiles of 8 features at once
 #pragma unroll
-        for (int kb = 0; kb < NT; ++kb) {
-            uint32_t ah[4], al[4];
+        for (int d0 = 0; d0 < DP / 8; d0 += GROUP) {
+            if (d0 >= steps) break;
+            float part[GROUP][4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const Split v(__float_as_uint(w[kb][e == 1 ? 2 : e == 2 ? 1 : e]));
-                ah[e] = v.hi;
-                al[e] = v.lo;
-            }
-            constexpr int GROUP = 4;                  // tiles of 8 features at once
+            for (int kb = 0; kb < NT; ++kb) {
+                if (kb % kExact == 0) {
 #pragma unroll
-            for (int d0 = 0; d0 < DP / 8; d0 += GROUP) {
-                if (d0 >= steps) break;
-                uint32_t b[GROUP][2];
+                    for (int d = 0; d < GROUP; ++d) part[d][0] = part[d][1] = part[d][2] = part[d][3] = 0.f;
+                }
+                uint32_t ah[4], al[4], b[GROUP][2];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const Split v(__float_as_uint(w[kb][e == 1 ? 2 : e == 2 ? 1 : e]));
+                    ah[e] = v.hi;
+                    al[e] = v.lo;
+                }
 #pragma unroll
                 for (int d = 0; d < GROUP; ++d) {
                     const uint32_t at_d = (d0 + d) << 5;
                     asm volatile("ld.shared.b32 %0, [%1];" : "=r"(b[d][0]) : "r"((row0 ^ at_d) + kb * 8 * RB) : "memory");
                     asm volatile("ld.shared.b32 %0, [%1];" : "=r"(b[d][1]) : "r"((row1 ^ at_d) + kb * 8 * RB) : "memory");
                 }
-                mma_f32<GROUP>(o + d0, ah, al, b);
+                mma_f32<GROUP>(part, ah, al, b);
+                if (kb % kExact == kExact - 1 || kb == NT - 1) {
+#pragma unroll
+                    for (int d = 0; d < GROUP; ++d)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) o[d0 + d][e] += part[d][e];
+                }
             }
         }
     } else {
@@ -268,8 +292,10 @@ __device__ __forceinline__ void softmax_step(float (&s)[NT][4], float (&o)[DT][4
 #pragma unroll
         for (int n = 0; n < NT; ++n) m = fmaxf(m, fmaxf(s[n][2 * i], s[n][2 * i + 1]));
         m = fmaxf(top[i], quad_max(m));
-        const float ref = m == -INFINITY ? 0.f : m * c2;
-        fade[i] = ex2(fmaf(top[i], c2, -ref));                 // 0 while top is -infinity
+        // Two rounded products, so that fade is exactly 1 while the maximum stays: what one fused operation would
+        // leave of their rounding, always the same way, is a drift over many tiles.
+        const float ref = m == -INFINITY ? 0.f : __fmul_rn(m, c2);
+        fade[i] = ex2(__fsub_rn(__fmul_rn(top[i], c2), ref));  // 0 while top is -infinity
         top[i] = m;
         float part = 0.f;
 #pragma unroll
@@ -293,7 +319,11 @@ __device__ __forceinline__ void softmax_step(float (&s)[NT][4], float (&o)[DT][4
 //
 // A block of four warps takes 64 rows in all: one tile of M = 64 rows of one head, or two or four heads of
 // a tile of 32 or 16 rows, so that short sequences fill the warps.  Each warp owns 16 query rows.  Keys
-// come in tiles of M.
+// come in tiles of M.  A block's copies, products and stores follow one another, and the three to five blocks of an SM
+// overlap: bound by that latency more than by memory.  Windows of 49 tokens, 4096 of them, 3 heads of 128 features:
+// forward 143 us (4.3 TB/s; instructions issued in 51 % of the cycles), gradients 326 us (3.8 TB/s counting each
+// tensor once), against 1450 us of a kernel for all lengths on the CUDA cores.  Several windows to a block, one after
+// the other, gained nothing (143 to 147 us for 2 to 3).
 constexpr int kShortThreads = 128;
 
 // Most of these sequences have one tile, so the first tiles need no search: block b of the first `sequences` takes
@@ -620,7 +650,9 @@ __device__ __forceinline__ bool one_tile(const Params& p, int queries, int keys)
 
 // All gradients of one head of a sequence of one tile: the scores and the weights are computed once, by warps that
 // own 16 queries; the weights and ds go to shared memory (over V and K, which are then done with), for warps
-// that own 16 keys.
+// that own 16 keys.  Five products and each tensor read once, for seven and twice with dq and dk, dv apart (windows
+// of 49, 3 heads of 128: 326 us for 587).  Q and K are waited for first; dO, V and the rows of O for delta arrive
+// while the scores are computed (all at once: 485 us).
 template <class T, int DP, int M>
 __device__ __forceinline__ void bwd_one_tile(const Params& p, uint8_t* smem, int head_block, const Tile& t, const Rows& kr) {
     constexpr int RB = kRowBytes<T, DP>, U = 64 / M, WU = 4 / U, NT = M / 8;
@@ -916,7 +948,9 @@ __global__ void __launch_bounds__(kShortThreads) eqlin_attn_dkv_f32_kernel(const
 // joined in shared memory.  With several slices the block writes o and lse in fp32 to the workspace
 // ([split][head][row]) and eqlin_attn_join_kernel joins them.
 //
-// Bound by memory: each key and value is read once.  Per SM about 128 KB of copies are in flight.
+// Bound by memory: each key and value is read once.  Per SM about 128 KB of copies are in flight.  One query, 8
+// sequences of 16384 keys, 8 heads on 2 key heads of 64 features: 17 us with the join for 67 MB (3.9 TB/s; a launch,
+// the offsets' reads and the join are 6 of them).
 template <int DP>
 struct Few {
     static constexpr int WARPS = 8;

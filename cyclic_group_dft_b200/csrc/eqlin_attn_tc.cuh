@@ -162,7 +162,7 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
 // where a head has 64 features).  x = n + f, n the nearest integer: adding 1.5 * 2^23 leaves n in the low
 // bits, 2^f is a polynomial, 2^n is built from its bits (Cody and Waite's reduction; the coefficients are a
 // Remez fit of the relative error on [-1/2, 1/2]: 2.7e-6 = 2^-18.5 with the fp32 evaluation, far below the
-// 2^-9 of the weights' rounding).  x <= 100; x <= -127, -infinity among it, gives exactly 0; NaN stays NaN.
+// 2^-8 (bf16) or 2^-11 (fp16) of the weights' rounding).  x <= 100; x <= -127, -infinity among it, gives exactly 0; NaN stays NaN.
 __device__ __forceinline__ float2 ex2_fma(float2 x) {
     asm("max.NaN.f32 %0, %0, %1;" : "+f"(x.x) : "f"(-127.f));
     asm("max.NaN.f32 %0, %0, %1;" : "+f"(x.y) : "f"(-127.f));
@@ -234,7 +234,16 @@ __device__ __forceinline__ void zero_tail(uint8_t* tile, int boxes, int valid, i
 //   O_i += P V                         (A from TMEM)
 // The maximum that P refers to moves only when the true one has grown by more than 2^8: until then
 // P stays below 2^8, and the rescaling of O (a round trip through registers) is rarely needed.
-// With two query tiles the tensor cores work on one while the other's softmax runs.
+//
+// D > 64: two query tiles in a block, so that the tensor cores work on one while the other's softmax runs.  Bound by
+// the tensor cores: 1430 TFLOP/s over long keys with all SMs filled; a causal call of few long sequences by its
+// longest one (12 sequences of up to 4096: 85 us, of which about 60 are the steps of one block).
+// D <= 64: one query tile and two blocks on an SM.  The products of a tile of 128 x 128 take 512 cycles, its
+// exponentials 1024 in the exponential unit alone, and the steps of a tile (scores out of TMEM, maximum, exponentials,
+// weights into TMEM) follow one another; two blocks overlap them to 1480 cycles.  784 tokens, 32 sequences, 8 heads:
+// 98 us (413 TFLOP/s; tensor cores busy 27 %, instructions issued in 42 % of the cycles); 8192 tokens, 8 heads: 198 us
+// (694).  Measured instead, for these two: tiles of 64 keys with 2, 3, 4 blocks on an SM 114, 102, 95 and 258, 282,
+// 228 us; two threads a row with their maxima exchanged through shared memory 103 and 217.
 template <int DP, int NQ>
 struct Fwd {
     static constexpr int BOXES = DP / 64;

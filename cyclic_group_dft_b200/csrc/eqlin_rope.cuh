@@ -15,6 +15,7 @@
 //
 // Bound by memory: one read and one write of the features.  A block takes a few tokens,
 // computes their cos and sin once into shared memory for all heads, and rotates whole vectors.
+// bf16, 200704 tokens, 6 heads of 32 channels, G = 4: 105 us for 618 MB (5.9 TB/s).
 #pragma once
 
 #include "eqlin_vec.cuh"

@@ -9,7 +9,8 @@ the value itself:
     a few hundred products of 2^-24 each, approximate exponentials of 2^-22);
   - attention's fp32 products may each be three products of tf32 (11 significant bits): a = h + l with h
     rounded to nearest, |l| <= 2^-11 |a|; l, cut to 11 bits, loses less than 2^-10 |l| <= 2^-21 |a|.
-    a b - (h h' + h l' + l h') is l l' (2^-22 |a b|) and the two cuts (2^-21 |a b| each): 2.5 * 2^-21 |a b|;
+    a b - (h h' + h l' + l h') is l l' (2^-22 |a b|) and the two cuts (2^-21 |a b| each): 2.5 * 2^-21 |a b|.  Their sums start from zero every
+    32 terms, as the tensor cores' additions are cut and not rounded;
   - attention's 16-bit forward may take its weights from a polynomial for 2^x of relative error 2^-18.5 (a
     fit of degree 4 to 2^f on [-1/2, 1/2]): the normaliser and the weights each move by that, which in o
     adds up to twice as much per term and in lse, the normaliser's logarithm, to once as much;

@@ -260,6 +260,20 @@ def test_attention_of_many_tiles(n, q_most, k_most, H, Hk, D, causal, dtype):
     _check_attention(*_attention(q_lens, k_lens, H, Hk, D, causal, dtype, seed=n))
 
 
+@pytest.mark.parametrize("q_len,k_len", [(30, 8192), (8192, 30)])
+def test_fp32_attention_sums_do_not_drift(q_len, k_len):
+    """Thousands of terms of one sign: roundings that all go one way would add up in o, or in dv."""
+    H, D, G = 40, 16, 4
+    q, k = _randn(q_len, H * D // G, G, seed=1, dtype=torch.float32), _randn(k_len, H * D // G, G, seed=2, dtype=torch.float32)
+    v = 1 + _randn(k_len, H * D // G, G, seed=3, dtype=torch.float32).abs()
+    do = 1 + _randn(q_len, H * D // G, G, seed=4, dtype=torch.float32).abs()
+    want, bound = ref.attention(q, k, v, do, [q_len], [k_len], H, H, False)
+    q, k, v, do = (t.to(DEV) for t in (q, k, v, do))
+    o, lse = eq.eqlin_attention_forward(q, k, v, heads=H)
+    dq, dk, dv = eq.eqlin_attention_backward(do, q, k, v, want["o"].float().to(DEV), want["lse"].float().to(DEV), heads=H)
+    _check_attention({"o": o, "lse": lse, "dq": dq, "dk": dk, "dv": dv}, want, bound)
+
+
 def test_fp32_not_a_number_stays_in_its_sequence_of_many_tiles():
     lens, H, D, G = [70, 5, 130], 16, 64, 4
     n = sum(lens)
