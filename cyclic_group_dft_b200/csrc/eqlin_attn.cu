@@ -178,7 +178,7 @@ Fwd forward_kind(const eqlin_attention_shape& a) {
     const int64_t n = a.sequences, packed = a.q_rows * (a.heads / a.kv_heads);
     const int64_t few_tiles = std::max(n, (packed + 15) / 16) * a.kv_heads;     // blocks without splits
     const int64_t short_tiles = std::max(n, (a.q_rows + 63) / 64) * a.heads;
-    if (a.k_rows >= 128 * n) {
+    if (a.k_rows >= 128 * n && packed < (int64_t(1) << 31)) {   // (packed rows are counted in 32 bits)
         const bool longer = a.k_rows >= 512 * n;
         if (few_tiles <= kB200Sms && (packed <= 16 * n || (packed <= 128 * n && longer))) return Fwd::kFew;
         if (few_tiles * (longer ? 2 : 4) <= short_tiles) return Fwd::kFew;
