@@ -48,7 +48,8 @@ int plan_norm(int64_t N, int64_t C, int64_t G, int io, int sms, bool backward, N
     pl->wide = pl->tpr > 32;
     const int64_t groups = pl->wide ? 1 : norm::kThreads / pl->tpr;
     const int64_t rows = (N + groups - 1) / groups;
-    const int per_sm = backward ? norm::bwd_blocks(pl->vpt, pl->wide) : norm::fwd_blocks(pl->vpt, pl->wide);
+    const int fit = pl->wide ? norm::kMaxWide / pl->tpr : 1;   // the wide form's counts are for its largest block
+    const int per_sm = fit * (backward ? norm::bwd_blocks(pl->vpt, pl->wide) : norm::fwd_blocks(pl->vpt, pl->wide));
     pl->blocks = static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>(rows, int64_t(sms) * per_sm)));
     return EQLIN_OK;
 }
@@ -89,16 +90,19 @@ int launch_norm_fwd(const NormPlan& pl, const norm::Params& p, cudaStream_t st) 
     });
 }
 
+template <class T>
 size_t bwd_smem(const NormPlan& pl) {
     const int groups = pl.wide ? 1 : norm::kThreads / pl.tpr;
-    return size_t(groups) * pl.tpr * pl.vpt * pl.vec * sizeof(float);
+    const size_t weights = size_t(pl.tpr) * pl.vpt * pl.vec * sizeof(float), sums = groups * weights;
+    const size_t ring = norm::bwd_ring<T>(pl.vec, pl.wide) ? size_t(2) * 3 * pl.vpt * norm::kThreads * 16 : 0;
+    return weights + std::max(sums, ring);
 }
 
 template <class T, int VEC>
 int launch_norm_bwd(const NormPlan& pl, const norm::Params& p, cudaStream_t st) {
     return with_vpt<T, VEC>(pl, [&](auto vpt, auto wide) {
         return launch(norm::eqlin_rmsnorm_bwd_kernel<T, VEC, decltype(vpt)::value, decltype(wide)::value>,
-                      dim3(pl.blocks), dim3(pl.wide ? pl.tpr : norm::kThreads), bwd_smem(pl), st,
+                      dim3(pl.blocks), dim3(pl.wide ? pl.tpr : norm::kThreads), bwd_smem<T>(pl), st,
                       "norm gradient launch", p);
     });
 }

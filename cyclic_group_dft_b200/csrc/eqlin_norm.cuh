@@ -35,6 +35,15 @@ constexpr float kE4m3Max = 448.f;
 constexpr int fwd_blocks(int vpt, bool wide) { return wide ? (vpt <= 2 ? 2 : 1) : vpt == 1 ? 6 : vpt == 2 ? 4 : 3; }
 constexpr int bwd_blocks(int vpt, bool wide) { return wide ? (vpt <= 2 ? 2 : 1) : vpt == 1 ? 4 : vpt == 2 ? 3 : 2; }
 
+// Whether the gradients' vectors come through the ring.
+template <class T>
+constexpr bool bwd_ring(int vec, bool wide) {
+    return !wide && vec * sizeof(T) == 16;
+}
+__device__ __forceinline__ void cp_async16(uint4* dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(ptx::smem_u32(dst)), "l"(src) : "memory");
+}
+
 struct Params {
     const void* x;          // fwd: x;  bwd: dy
     const void* residual;   // fwd: residual or NULL;  bwd: the stored sum r
@@ -208,13 +217,17 @@ __global__ void __launch_bounds__(WIDE ? kMaxWide : kThreads, fwd_blocks(VPT, WI
 }
 
 // The gradients: dx (of x and of the residual alike) and, per block, the sums of dw.
-// Dynamic shared memory: groups * tpr * VPT * VEC floats for the sums of dw; before that, at its start, the
-// weights of tpr * VPT * VEC columns (registers would cost a block per SM).
+// Dynamic shared memory: the weights of tpr * VPT * VEC columns (registers would cost a block per SM); behind them
+// first the ring of the next row's vectors, then groups * tpr * VPT * VEC floats for the sums of dw.
+// Ring (narrow form, vectors of 16 bytes): a thread copies its vectors of the group's next row asynchronously while
+// it works on this one, and reads back its own alone, so that no barrier is needed.
 template <class T, int VEC, int VPT, bool WIDE>
 __global__ void __launch_bounds__(WIDE ? kMaxWide : kThreads, bwd_blocks(VPT, WIDE)) eqlin_rmsnorm_bwd_kernel(const Params p) {
     using V = Vec<T, VEC>;
+    constexpr bool RING = bwd_ring<T>(VEC, WIDE);
     __shared__ float red[32];
-    extern __shared__ float acc_smem[];
+    extern __shared__ __align__(16) float w_smem[];
+    float* acc_smem = w_smem + p.tpr * VPT * VEC;
     const int groups = WIDE ? 1 : kThreads / p.tpr;
     const int lane = WIDE ? threadIdx.x : threadIdx.x & (p.tpr - 1);
     const int group = WIDE ? 0 : threadIdx.x / p.tpr;
@@ -227,10 +240,10 @@ __global__ void __launch_bounds__(WIDE ? kMaxWide : kThreads, bwd_blocks(VPT, WI
 #pragma unroll
         for (int e = 0; e < VEC; ++e) dw[j][e] = 0.f;
     for (int i = threadIdx.x; i < p.tpr * VPT * VEC; i += blockDim.x)
-        acc_smem[i] = p.weight && i < p.L ? load_param(p.weight, p.w_dtype, i >> p.lg_g) : 1.f;
+        w_smem[i] = p.weight && i < p.L ? load_param(p.weight, p.w_dtype, i >> p.lg_g) : 1.f;
     __syncthreads();
     auto weights = [&](int j, float (&w)[VEC]) {
-        const float* s = acc_smem + (lane + j * p.tpr) * VEC;
+        const float* s = w_smem + (lane + j * p.tpr) * VEC;
         if constexpr (VEC % 4 == 0) {
 #pragma unroll
             for (int e = 0; e < VEC; e += 4) {
@@ -246,20 +259,47 @@ __global__ void __launch_bounds__(WIDE ? kMaxWide : kThreads, bwd_blocks(VPT, WI
         }
     };
     const float inv_l = 1.f / static_cast<float>(p.L);
-    for (long long base = static_cast<long long>(blockIdx.x) * groups; base < p.N;
-         base += static_cast<long long>(gridDim.x) * groups) {
+    const long long step = static_cast<long long>(gridDim.x) * groups;
+    uint4* ring = reinterpret_cast<uint4*>(acc_smem) + threadIdx.x;
+    auto slot = [&](int stage, int tensor, int j) { return ring + ((stage * 3 + tensor) * VPT + j) * kThreads; };
+    auto fetch = [&](long long row, int stage) {
+        if constexpr (RING) {
+#pragma unroll
+            for (int j = 0; j < VPT; ++j) {
+                const int v = lane + j * p.tpr;
+                if (row >= p.N || v >= nv) continue;
+                const long long at = row * p.L + v * VEC;
+                cp_async16(slot(stage, 0, j), static_cast<const T*>(p.x) + at);
+                cp_async16(slot(stage, 1, j), static_cast<const T*>(p.residual) + at);
+                if (p.sum) cp_async16(slot(stage, 2, j), static_cast<const T*>(p.sum) + at);
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        }
+    };
+    int stage = 0;
+    fetch(static_cast<long long>(blockIdx.x) * groups + group, 0);
+    for (long long base = static_cast<long long>(blockIdx.x) * groups; base < p.N; base += step, stage ^= 1) {
         const long long row = base + group;
         const bool live = row < p.N;
         typename V::Raw rdy[VPT], rs[VPT], rd[VPT];
+        if constexpr (RING) {
+            fetch(row + step, stage ^ 1);
+            asm volatile("cp.async.wait_group 1;" ::: "memory");
+        }
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
             const int v = lane + j * p.tpr;
             rdy[j] = rs[j] = rd[j] = typename V::Raw{};
             if (live && v < nv) {
-                const long long at = row * p.L + v * VEC;
-                rdy[j] = V::load(static_cast<const T*>(p.x) + at);
-                rs[j] = V::load(static_cast<const T*>(p.residual) + at);
-                if (p.sum) rd[j] = V::load(static_cast<const T*>(p.sum) + at);
+                if constexpr (RING) {
+                    rdy[j] = *slot(stage, 0, j);
+                    rs[j] = *slot(stage, 1, j);
+                } else {
+                    const long long at = row * p.L + v * VEC;
+                    rdy[j] = V::load(static_cast<const T*>(p.x) + at);
+                    rs[j] = V::load(static_cast<const T*>(p.residual) + at);
+                    if (p.sum) rd[j] = V::load(static_cast<const T*>(p.sum) + at);
+                }
             }
         }
         float s[2] = {0.f, 0.f};   // sum r^2 and sum w dy r
@@ -283,6 +323,8 @@ __global__ void __launch_bounds__(WIDE ? kMaxWide : kThreads, bwd_blocks(VPT, WI
         for (int j = 0; j < VPT; ++j) {
             const int v = lane + j * p.tpr;
             float dy[VEC], r[VEC], d[VEC], w[VEC];
+            if constexpr (RING)
+                if (p.sum && live && v < nv) rd[j] = *slot(stage, 2, j);
             V::unpack(rdy[j], dy);
             V::unpack(rs[j], r);
             V::unpack(rd[j], d);
@@ -296,7 +338,8 @@ __global__ void __launch_bounds__(WIDE ? kMaxWide : kThreads, bwd_blocks(VPT, WI
         }
     }
     if (!p.partial) return;
-    __syncthreads();   // the weights are read
+    if constexpr (RING) asm volatile("cp.async.wait_group 0;" ::: "memory");
+    __syncthreads();   // the ring is read
     const int row_pad = p.tpr * VPT * VEC;
 #pragma unroll
     for (int j = 0; j < VPT; ++j)
