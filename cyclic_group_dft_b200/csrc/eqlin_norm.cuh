@@ -364,7 +364,7 @@ __global__ void __launch_bounds__(512) eqlin_rmsnorm_dw_kernel(const float* part
     const int c = blockIdx.x * 32 + threadIdx.x;
     double s = 0.0;
     if (c < C) {
-#pragma unroll 4
+#pragma unroll 16   // reads in flight: the launch is short, and bound by their latency
         for (int b = threadIdx.y; b < blocks; b += 16) s += partial[static_cast<long long>(b) * C + c];
     }
     part[threadIdx.y][threadIdx.x] = s;
