@@ -90,20 +90,23 @@ int launch_norm_fwd(const NormPlan& pl, const norm::Params& p, cudaStream_t st) 
     });
 }
 
-template <class T>
-size_t bwd_smem(const NormPlan& pl) {
+size_t bwd_smem(const NormPlan& pl, bool ring) {
     const int groups = pl.wide ? 1 : norm::kThreads / pl.tpr;
     const size_t weights = size_t(pl.tpr) * pl.vpt * pl.vec * sizeof(float), sums = groups * weights;
-    const size_t ring = norm::bwd_ring<T>(pl.vec, pl.wide) ? size_t(2) * 3 * pl.vpt * norm::kThreads * 16 : 0;
-    return weights + std::max(sums, ring);
+    return weights + std::max(sums, ring ? size_t(2) * 2 * pl.vpt * norm::kThreads * 16 : 0);
 }
 
 template <class T, int VEC>
 int launch_norm_bwd(const NormPlan& pl, const norm::Params& p, cudaStream_t st) {
     return with_vpt<T, VEC>(pl, [&](auto vpt, auto wide) {
-        return launch(norm::eqlin_rmsnorm_bwd_kernel<T, VEC, decltype(vpt)::value, decltype(wide)::value>,
-                      dim3(pl.blocks), dim3(pl.wide ? pl.tpr : norm::kThreads), bwd_smem<T>(pl), st,
-                      "norm gradient launch", p);
+        constexpr int VPT = decltype(vpt)::value;
+        constexpr bool WIDE = decltype(wide)::value, CAN = !WIDE && VEC * sizeof(T) == 16;
+        auto go = [&](auto ring) {
+            constexpr bool RING = decltype(ring)::value;
+            return launch(norm::eqlin_rmsnorm_bwd_kernel<T, VEC, VPT, WIDE, RING>, dim3(pl.blocks),
+                          dim3(pl.wide ? pl.tpr : norm::kThreads), bwd_smem(pl, RING), st, "norm gradient launch", p);
+        };
+        return CAN && !p.sum ? go(std::bool_constant<CAN>()) : go(std::false_type());
     });
 }
 

@@ -15,7 +15,8 @@
 // the group axis, written per block, and reduced over blocks in a fixed order in float64.
 //
 // bf16, 200704 tokens of 96 channels, G = 4 (154 MB a tensor): forward 110 us for four tensors (5.6 TB/s), gradients
-// 99 us for three (4.7 TB/s; 128 registers a thread leave two blocks of 256 on an SM).  8-bit output, 25088 tokens of 64 channels, G = 8: 18.7 us (4.8 TB/s).
+// 82 us for three (5.6 TB/s), with dsum 110 us for four.  8-bit output, 25088 tokens of 64 channels, G = 8: 18.7 us (4.8
+// TB/s).  Wide rows, 12544 of 4096 features: forward 68 us for 411 MB (6.1 TB/s), gradients 85.
 #pragma once
 
 #include <cuda_fp8.h>
@@ -35,11 +36,6 @@ constexpr float kE4m3Max = 448.f;
 constexpr int fwd_blocks(int vpt, bool wide) { return wide ? (vpt <= 2 ? 2 : 1) : vpt == 1 ? 6 : vpt == 2 ? 4 : 3; }
 constexpr int bwd_blocks(int vpt, bool wide) { return wide ? (vpt <= 2 ? 2 : 1) : vpt == 1 ? 4 : vpt == 2 ? 3 : 2; }
 
-// Whether the gradients' vectors come through the ring.
-template <class T>
-constexpr bool bwd_ring(int vec, bool wide) {
-    return !wide && vec * sizeof(T) == 16;
-}
 __device__ __forceinline__ void cp_async16(uint4* dst, const void* src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(ptx::smem_u32(dst)), "l"(src) : "memory");
 }
@@ -219,12 +215,13 @@ __global__ void __launch_bounds__(WIDE ? kMaxWide : kThreads, fwd_blocks(VPT, WI
 // The gradients: dx (of x and of the residual alike) and, per block, the sums of dw.
 // Dynamic shared memory: the weights of tpr * VPT * VEC columns (registers would cost a block per SM); behind them
 // first the ring of the next row's vectors, then groups * tpr * VPT * VEC floats for the sums of dw.
-// Ring (narrow form, vectors of 16 bytes): a thread copies its vectors of the group's next row asynchronously while
-// it works on this one, and reads back its own alone, so that no barrier is needed.
-template <class T, int VEC, int VPT, bool WIDE>
+// RING (narrow form, vectors of 16 bytes, no dsum): a thread copies its vectors of the group's next row asynchronously
+// while it works on this one, and reads back its own alone, so that no barrier is needed.  200704 tokens of 96
+// channels, G = 4: 82 us for 98.  With dsum three tensors in flight are enough without it, and the ring was slower
+// (forward and gradients 220 us for 210).
+template <class T, int VEC, int VPT, bool WIDE, bool RING>
 __global__ void __launch_bounds__(WIDE ? kMaxWide : kThreads, bwd_blocks(VPT, WIDE)) eqlin_rmsnorm_bwd_kernel(const Params p) {
     using V = Vec<T, VEC>;
-    constexpr bool RING = bwd_ring<T>(VEC, WIDE);
     __shared__ float red[32];
     extern __shared__ __align__(16) float w_smem[];
     float* acc_smem = w_smem + p.tpr * VPT * VEC;
@@ -261,7 +258,7 @@ __global__ void __launch_bounds__(WIDE ? kMaxWide : kThreads, bwd_blocks(VPT, WI
     const float inv_l = 1.f / static_cast<float>(p.L);
     const long long step = static_cast<long long>(gridDim.x) * groups;
     uint4* ring = reinterpret_cast<uint4*>(acc_smem) + threadIdx.x;
-    auto slot = [&](int stage, int tensor, int j) { return ring + ((stage * 3 + tensor) * VPT + j) * kThreads; };
+    auto slot = [&](int stage, int tensor, int j) { return ring + ((stage * 2 + tensor) * VPT + j) * kThreads; };
     auto fetch = [&](long long row, int stage) {
         if constexpr (RING) {
 #pragma unroll
@@ -271,7 +268,6 @@ __global__ void __launch_bounds__(WIDE ? kMaxWide : kThreads, bwd_blocks(VPT, WI
                 const long long at = row * p.L + v * VEC;
                 cp_async16(slot(stage, 0, j), static_cast<const T*>(p.x) + at);
                 cp_async16(slot(stage, 1, j), static_cast<const T*>(p.residual) + at);
-                if (p.sum) cp_async16(slot(stage, 2, j), static_cast<const T*>(p.sum) + at);
             }
             asm volatile("cp.async.commit_group;" ::: "memory");
         }
@@ -323,8 +319,6 @@ __global__ void __launch_bounds__(WIDE ? kMaxWide : kThreads, bwd_blocks(VPT, WI
         for (int j = 0; j < VPT; ++j) {
             const int v = lane + j * p.tpr;
             float dy[VEC], r[VEC], d[VEC], w[VEC];
-            if constexpr (RING)
-                if (p.sum && live && v < nv) rd[j] = *slot(stage, 2, j);
             V::unpack(rdy[j], dy);
             V::unpack(rs[j], r);
             V::unpack(rd[j], d);
