@@ -312,7 +312,8 @@ __global__ void __launch_bounds__(WIDE ? kMaxWide : kThreads, bwd_blocks(VPT, WI
             }
         }
         group_sum<WIDE, 2>(s, p.tpr, red);
-        const float rstd = 1.f / sqrtf(fmaf(s[0], inv_l, p.eps));
+        // places past the last row hold zeros and must add none to dw: with eps = 0 they would have an infinite rstd
+        const float rstd = live ? 1.f / sqrtf(fmaf(s[0], inv_l, p.eps)) : 0.f;
         const float inner = s[1] * inv_l * rstd * rstd;   // mean(w dy u) * rstd, for u = r * rstd
         T* out = static_cast<T*>(p.y) + row * p.L;
 #pragma unroll

@@ -94,6 +94,20 @@ def test_norm_in_place_and_large_values():
     assert (y.float() - 1).abs().max() <= 2.0 ** -11
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("C,G", [(96, 4), (8, 1), (512, 8)])      # 16 rows of a block at once, 64 (fp32) and more, one
+@pytest.mark.parametrize("N", [1, 17, 50])
+def test_norm_gradient_without_eps(N, C, G, dtype):
+    """eps = 0 and rows that do not fill the blocks: places past the last row add nothing to dweight."""
+    x, w = _randn(N, C, G, seed=N, dtype=dtype), _randn(C, seed=C, dtype=torch.float32)
+    dy, dsum = _randn(N, C, G, seed=1, dtype=dtype), _randn(N, C, G, seed=2, dtype=dtype)
+    for ds in (None, dsum):                                        # with the ring of copies and without
+        dx64, dw64, dx_b, dw_b = ref.rmsnorm_backward(dy, x, w, ds, 0.0)
+        dx, dw = eq.eqlin_rmsnorm_backward(dy.to(DEV), x.to(DEV), w.to(DEV), None if ds is None else ds.to(DEV), eps=0.0)
+        within(dx, dx64, dx_b, "dx")
+        within(dw, dw64, dw_b, "dweight")
+
+
 def test_norm_gradient_against_differences():
     N, C, G, eps = 5, 24, 4, 1e-3
     x = _randn(N, C, G, seed=1, dtype=torch.float64)
