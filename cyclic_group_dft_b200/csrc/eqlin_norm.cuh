@@ -19,6 +19,8 @@
 // TB/s).  Wide rows, 12544 of 4096 features: forward 68 us for 411 MB (6.1 TB/s), gradients 85.
 #pragma once
 
+#include <cfloat>
+
 #include <cuda_fp8.h>
 
 #include "eqlin_vec.cuh"
@@ -174,11 +176,21 @@ __global__ void __launch_bounds__(WIDE ? kMaxWide : kThreads, fwd_blocks(VPT, WI
             }
         if constexpr (OUT8) {
             top = group_max<WIDE>(top, p.tpr, red);
-            const float scale = top > 0.f ? top / kE4m3Max : 1.f;
+            float scale = top > 0.f ? top / kE4m3Max : 1.f, up = 1.f;
+            if (scale < FLT_MIN) {
+                // Its reciprocal would be infinite: scale and row times 2^64 instead.  Rounded up, so that it is
+                // not 0 and y / scale not above 448.
+                scale = __fdiv_ru(top, kE4m3Max);
+                up = 18446744073709551616.f;
+#pragma unroll
+                for (int j = 0; j < VPT; ++j)
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) r[j][e] *= up;
+            }
             if (!live) continue;
             // one reciprocal for the row: within 2 units in the last place of y / scale, far below half of an
-            // e4m3 step
-            const float inv = 1.f / scale;
+            // e4m3 step (quotients instead: 25088 rows of 512 features 17 to 22 us, 200704 of 384 85 to 105)
+            const float inv = 1.f / (scale * up);
             if (lane == 0) p.scale[row] = scale;
             uint8_t* out = static_cast<uint8_t*>(p.y) + row * p.L;
 #pragma unroll

@@ -428,8 +428,8 @@ EQLIN_API int eqlin_mlp_query(int64_t Cin, int64_t H, int64_t Cout, int64_t G, i
  * of 8 and at most 16384, for fp32 at most 8192 (2048 when C*G is not a multiple of 4).
  *
  * eqlin_add_rmsnorm_fp8 -- the same with y in 8 bits: per row scale[n] = max |y[n]| / 448 (1 for
- * a row of zeros), y8 = e4m3(y / scale[n]), round to nearest even.  y8: device, [N, C, G] bytes,
- * 16-byte aligned, overlapping nothing; scale: device, [N] fp32.
+ * a row of zeros; rounded up where it is subnormal), y8 = e4m3(y / scale[n]), round to nearest
+ * even.  y8: device, [N, C, G] bytes, 16-byte aligned, overlapping nothing; scale: device, [N] fp32.
  *
  * eqlin_rmsnorm_backward -- the gradients, from the stored sum r:
  *   dx = dsum + rstd * (w dy - u * mean(w dy u)),  u = r * rstd,   of x and of residual alike;

@@ -61,6 +61,31 @@ def test_norm(N, C, G, dtype):
         within(dw, dw64, dw_b, "dweight")
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("C,G", [(96, 4), (512, 8), (3, 1)])
+@pytest.mark.parametrize("size", [1e-34, 1e-36, 1e-38, 1e-40, 1e-42, 1e-44])
+def test_norm_fp8_of_tiny_rows(C, G, size, dtype):
+    """Rows whose scale is a subnormal number, zeros among them: still y8 * scale within half a step of y."""
+    if dtype != torch.float32 and C * G % 8:
+        pytest.skip("16-byte rows only")
+    N = 5
+    x = _randn(N, C, G, seed=1, dtype=dtype)
+    x[:, ::3] = 0
+    x[0] = 0
+    w = torch.full((C,), size)
+    y64, _, _ = ref.add_rmsnorm(x, None, w, 1e-6)
+    y8, scale, _ = eq.eqlin_add_rmsnorm_fp8(x.to(DEV), None, w.to(DEV))
+    top = y64.abs().amax((1, 2))
+    # fp32 below 2^-126 has steps of 2^-149: y is off by half of one beside its relative error, the scale by one step
+    step = 2.0 ** -149
+    want = torch.where(top > step / 2, top / 448, torch.ones_like(top))
+    within(scale, want, ref.E * want + 1.01 * step, "scale")
+    s = scale.cpu().double()[:, None, None]
+    # e4m3: half a step is 2^-4 of the value, at least 2^-10 of the scale
+    within(y8.float().cpu().double() * s, y64, (2.0 ** -4 + 4 * ref.E) * y64.abs() + (2.0 ** -10 + ref.E) * s + 2 * step,
+           "y8 * scale")
+
+
 def test_norm_zero_rows_and_empty_batches():
     x = torch.zeros(3, 16, 4, dtype=torch.bfloat16, device=DEV)
     y8, scale, r = eq.eqlin_add_rmsnorm_fp8(x, x)
