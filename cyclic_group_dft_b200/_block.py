@@ -146,15 +146,15 @@ def eqlin_add_rmsnorm(x: torch.Tensor, residual: torch.Tensor | None = None, wei
                       eps: float = 1e-6, y: torch.Tensor | None = None, sum_out: torch.Tensor | None = None) -> tuple[torch.Tensor, torch.Tensor]:
     """(y, r) with r = x + residual and y = r * weight[c] / sqrt(mean(r^2) + eps) over the
     channels and group elements of a token; x, residual, y and r are [N, C, G], weight [C] or
-    None (ones).  Without a residual r is x itself, unless sum_out is given.  y and sum_out may
-    be x or residual (in place)."""
+    None (ones).  Without a residual r is x itself, unless sum_out is given or y is written over x: then r
+    has memory of its own.  y and sum_out may be x or residual (in place)."""
     shape, dtype, device = _norm_args(x, residual, weight, sum_out)
     N, C, G = shape
     if y is None:
         y = torch.empty_like(x)
     else:
         _like(y, "y", shape, dtype, device)
-    if sum_out is None and residual is not None:
+    if sum_out is None and (residual is not None or y.data_ptr() == x.data_ptr()):
         sum_out = torch.empty_like(x)
     if sum_out is not None and N > 0 and sum_out.data_ptr() == y.data_ptr():
         raise ValueError("y and sum_out must not be the same tensor")

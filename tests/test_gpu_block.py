@@ -120,6 +120,19 @@ def test_norm_in_place_and_large_values():
 
 
 @pytest.mark.parametrize("dtype", TYPES)
+def test_norm_in_place_without_a_residual_keeps_the_sum(dtype):
+    """y over x and no residual: r is the sum that the gradients need, not what y left there."""
+    x, w = _randn(50, 96, 4, seed=1, dtype=dtype).to(DEV), _randn(96, seed=2, dtype=torch.float32).to(DEV)
+    y, r = eq.eqlin_add_rmsnorm(x, None, w)
+    assert r.data_ptr() == x.data_ptr()                            # the sum is x itself
+    x2 = x.clone()
+    y2, r2 = eq.eqlin_add_rmsnorm(x2, None, w, y=x2)
+    assert y2.data_ptr() == x2.data_ptr() and torch.equal(y2, y) and torch.equal(r2, x)
+    e = x[:0]
+    assert eq.eqlin_add_rmsnorm(e, None, w, y=e)[1].shape == e.shape
+
+
+@pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("C,G", [(96, 4), (8, 1), (512, 8)])      # 16 rows of a block at once, 64 (fp32) and more, one
 @pytest.mark.parametrize("N", [1, 17, 50])
 def test_norm_gradient_without_eps(N, C, G, dtype):
