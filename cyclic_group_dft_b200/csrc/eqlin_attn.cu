@@ -240,7 +240,10 @@ bool backward_short_rows(int64_t q_rows, int64_t k_rows, int64_t n, int64_t head
 size_t backward_workspace(const eqlin_attention_shape& a) {
     if (a.io_dtype == EQLIN_F32 || backward_short_rows(a.q_rows, a.k_rows, a.sequences, a.heads, a.kv_heads))
         return size_t(a.q_rows) * size_t(a.heads) * sizeof(float);
-    return size_t(a.q_rows / attn::tc::kTile + a.sequences) * size_t(a.heads) * 2 * attn::tc::kTile * sizeof(float);
+    const size_t q_tiles = size_t(a.q_rows / attn::tc::kTile + a.sequences) * size_t(a.heads);
+    const size_t k_tiles = size_t(a.k_rows / attn::tc::kTile + a.sequences) * size_t(a.kv_heads);
+    const size_t floats = q_tiles * 2 * attn::tc::kTile;     // lse and delta
+    return (a.io_dtype == EQLIN_F16 ? floats + q_tiles * 16 + k_tiles * 4 : floats) * sizeof(float);
 }
 
 size_t forward_workspace(const eqlin_attention_shape& a) {
@@ -363,10 +366,10 @@ int backward_f32(const attn::Params& p, cudaStream_t st) {
 }
 
 template <class T, int DP>
-int backward_tc(const attn::tc::BwdParams& bp, int io, cudaStream_t st) {
+int backward_tc(attn::tc::BwdParams bp, int io, cudaStream_t st) {
     namespace tc = attn::tc;
     using B = tc::Bwd<DP>;
-    const attn::Params& p = bp.p;
+    attn::Params& p = bp.p;
     unsigned grid_k = 0, grid_q = 0;
     int s = tc_grid(p.k_rows, p.sequences, tc::kTile, p.kv_heads, &grid_k);
     if (s == EQLIN_OK) s = tc_grid(p.q_rows, p.sequences, tc::kTile, p.heads, &grid_q);
@@ -382,6 +385,8 @@ int backward_tc(const attn::tc::BwdParams& bp, int io, cudaStream_t st) {
     if (s != EQLIN_OK) return s;
     if (p.q_rows == 0) mq = mdo = mk;   // the side without rows is never read
     if (p.k_rows == 0) mk = mv = mq;
+    p.do_most = p.delta + size_t(grid_q) * 2 * tc::kTile;   // in the order of backward_workspace
+    p.v_most = p.do_most + size_t(grid_q) * 16;
     if (p.q_rows > 0)
         s = launch(tc::eqlin_attn_stats_kernel<T>, dim3(grid_q), dim3(256), 0, st, "attention gradient launch", p);
     if (s == EQLIN_OK && p.k_rows > 0)

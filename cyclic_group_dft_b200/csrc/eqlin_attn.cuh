@@ -14,6 +14,7 @@
 #pragma once
 
 #include <cstdint>
+#include <type_traits>
 
 #include "eqlin_vec.cuh"
 #include "sm100_ptx.cuh"
@@ -26,6 +27,7 @@ struct Params {
     void *out, *dq, *dk, *dv;      // out: the forward's o
     float* lse;                    // [heads][q_rows], or NULL
     float* delta;                  // gradients: delta [heads][q_rows], or the tensor-core kernels' statistics
+    float *do_most, *v_most;       // and, for fp16, what bounds ds (see eqlin_attn_stats_kernel)
     const int32_t *q_offsets, *k_offsets;   // [sequences + 1], or NULL: one sequence of all rows
     long long q_stride, k_stride, v_stride, o_stride, do_stride, dq_stride, dk_stride, dv_stride;
     int q_rows, k_rows, sequences, heads, kv_heads, D;
@@ -128,6 +130,24 @@ __device__ __forceinline__ int first_query(int first, int q_len, int k_len, int 
     const long long i = static_cast<long long>(first) + q_len - k_len;
     return static_cast<int>(i < 0 ? 0 : i);
 }
+
+// The gradients round p and ds to the I/O type before their products.  fp16 loses what is below 2^-14 there and has
+// nothing above 65504, so both are lifted by powers of two, which the outputs take back exactly: p <= 1 by 2^15, ds by
+// what its largest value, or a bound of it, allows (row by row, see the kernels).  Without it, 784 tokens with dO of
+// 2^-14 and v of 2^-6 lost dq whole.  What it costs, against no lift: 4096 windows of 49, 3 heads of 128 features 323 to
+// 333 us; 784 tokens, 32 sequences, 8 heads of 64 238 to 255; 8192 tokens 571 to 592; 100 tokens, 300 sequences 165 to
+// 184; 64 queries, 128 keys, 64 sequences, 8 heads on 2 71 to 79.
+template <class T>
+constexpr bool kLifted = std::is_same<T, __half>::value;
+template <class T>
+constexpr float kLiftP = kLifted<T> ? 15.f : 0.f;
+constexpr int kLiftMost = 94;
+// The exponent e for values of up to `most`: most * 2^e < 2^15.  Infinite and vanishing ones get a finite e.
+__device__ __forceinline__ int lift_of(float most) {
+    const int e = static_cast<int>((__float_as_uint(most) >> 23) & 255u) - 127;
+    return 14 - max(14 - kLiftMost, min(e, 80));
+}
+__device__ __forceinline__ float power_of_two(int e) { return __uint_as_float(static_cast<uint32_t>(max(e, -126) + 127) << 23); }
 
 // delta[h][i] = do_i . o_i in fp32: one warp per (row, 32 / lanes heads), reading both tensors
 // once.  A head takes `lanes` = the power of two >= D / VEC lanes.

@@ -96,13 +96,17 @@ __device__ __forceinline__ void store_accumulator(uint32_t taddr, bool filled, b
     }
 }
 
-// What the kernels below read of each query row: lse in units of log2 and delta = do . o, as
+// What the kernels below read of each query row: lse in units of log2 (less the lift of p) and delta = do . o, as
 // [head][slot][lse 128, delta 128] with the slots of find_tile<128>, so that a tile's values are one aligned piece.
 // A row that sees no key, or is past its sequence's end, gets lse = +infinity: weights of zero.  Both tensors are
 // read once; bound by memory.
+// fp16 (kLifted): for p <= 1, |ds_ij| <= |do_i| |v_j| + |delta_i|, by which ds can be lifted.  So each warp also leaves
+// the largest |do_i| and |delta_i| of its rows ([head][slot][8][2]); the kernel for dk and dv adds those of |v_j| for
+// the one for dq ([key head][slot][4]).  Infinite ones are left out: no exponent helps their products.
 template <class T>
 __global__ void __launch_bounds__(256) eqlin_attn_stats_kernel(const Params p) {
     using V = Vec<T, 8>;
+    constexpr bool LIFT = kLifted<T>;
     ptx::grid_launch_dependents();
     ptx::grid_dependency_wait();
     const int h = blockIdx.x % p.heads, slot = blockIdx.x / p.heads, n_slots = gridDim.x / p.heads;
@@ -111,28 +115,65 @@ __global__ void __launch_bounds__(256) eqlin_attn_stats_kernel(const Params p) {
     const int r0 = t.tile * kTile, n = min(kTile, t.own.len - r0);
     const int lanes = p.D <= 64 ? 8 : 16;                // threads of a row
     const int lane = threadIdx.x & (lanes - 1), rows = 256 / lanes;
-    const long long first = static_cast<long long>(t.own.start) + r0;
-    float* out = p.delta + (static_cast<long long>(h) * n_slots + slot) * 2 * kTile;
+    const long long first = static_cast<long long>(t.own.start) + r0, tile = static_cast<long long>(h) * n_slots + slot;
+    float* out = p.delta + tile * 2 * kTile;
     const bool in = lane * 8 < p.D;
     const T* a = static_cast<const T*>(p.dout) + first * p.do_stride + static_cast<long long>(h) * p.D + lane * 8;
     const T* b = static_cast<const T*>(p.o) + first * p.o_stride + static_cast<long long>(h) * p.D + lane * 8;
+    float most = 0.f;                                    // of |delta| in the first thread of a row, of |do|^2 in another
 #pragma unroll 4
     for (int r = threadIdx.x / lanes; r < kTile; r += rows) {
-        float sum = 0.f;
+        float sum = 0.f, norm = 0.f;
         if (in && r < n) {
             float x[8], y[8];
             V::unpack(V::load(a + r * p.do_stride), x);
             V::unpack(V::load(b + r * p.o_stride), y);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) sum = fmaf(x[e], y[e], sum);
+            for (int e = 0; e < 8; ++e) {
+                sum = fmaf(x[e], y[e], sum);
+                if (LIFT) norm = fmaf(x[e], x[e], norm);
+            }
         }
-        for (int o = lanes >> 1; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+        if (LIFT) {   // half of the row's threads go on with one of the sums, half with the other
+            const bool upper = lane & (lanes >> 1);
+            const float other = __shfl_xor_sync(0xFFFFFFFFu, upper ? sum : norm, lanes >> 1);
+            sum = (upper ? norm : sum) + other;
+        }
+        for (int o = LIFT ? lanes >> 2 : lanes >> 1; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+        if (LIFT && fabsf(sum) < INFINITY) most = fmaxf(most, fabsf(sum));
         if (lane == 0) {
             const float l = r < n ? p.lse[static_cast<long long>(h) * p.q_rows + first + r] : -INFINITY;
-            out[r] = l == -INFINITY ? INFINITY : l * kLog2e;
+            out[r] = l == -INFINITY ? INFINITY : fmaf(l, kLog2e, -kLiftP<T>);
             out[kTile + r] = sum;
         }
     }
+    if (LIFT) {
+        for (int o = lanes; o < 32; o <<= 1) most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, o));
+        float* to = p.do_most + (tile * 8 + (threadIdx.x >> 5)) * 2;
+        if ((threadIdx.x & 31) == 0) to[1] = most;
+        if ((threadIdx.x & 31) == lanes >> 1) to[0] = sqrtf(most);
+    }
+}
+
+// |x| of a row of a tile of fp16 in shared memory (features past the head's end are zeros), 0 where it is not finite.
+template <int DP>
+__device__ __forceinline__ float row_norm(const uint8_t* tile, int row) {
+    float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+    for (int c = 0; c < DP / 8; ++c) {
+        const uint4 v = *reinterpret_cast<const uint4*>(tile + (c >> 3) * kBoxBytes + row * 128 + (((c ^ row) & 7) << 4));
+        for (const uint32_t w : {v.x, v.y, v.z, v.w}) {
+            s0 = fmaf(Io16<__half>::lo(w), Io16<__half>::lo(w), s0);
+            s1 = fmaf(Io16<__half>::hi(w), Io16<__half>::hi(w), s1);
+        }
+    }
+    s0 = sqrtf(s0 + s1);
+    return s0 < INFINITY ? s0 : 0.f;
+}
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
+    return v;
 }
 
 // ------------------------------------------------------------------------------- dk and dv
@@ -304,7 +345,30 @@ __global__ void __launch_bounds__(Bwd<DP>::THREADS, Bwd<DP>::BLOCKS)
         bool ok = true;
         // a warp whose 32 keys all lie past the end only keeps the barriers' count
         const bool idle = t.tile < 0 || r0 + (warp & 3) * 32 >= t.own.len;
-        for (int j = 0; idle && j < n; ++j) {
+        // fp16: ds of this key lifted by its own |v| and the largest of the rows that the block walks
+        int lift = 0;
+        float own_v = 0.f;
+        if constexpr (kLifted<T>) {
+            if (!idle && n > 0) {
+                const int first = begin * BN / kTile, values = ((qr.len + kTile - 1) / kTile - first) * 8;
+                float a = 0.f, d = 0.f;
+                for (int g = 0; g < group; ++g) {
+                    const float2* most = reinterpret_cast<const float2*>(p.do_most) +
+                                         ((static_cast<long long>(hk) * group + g) * q_slots + q_slot + first) * 8;
+                    for (int i = lane; i < values; i += 32) {
+                        const float2 m = most[i];
+                        a = fmaxf(a, m.x);
+                        d = fmaxf(d, m.y);
+                    }
+                }
+                a = warp_max(a);
+                d = warp_max(d);
+                ok = wait_warp(fixed_full, 0, ctl, p.timeout_ns);
+                if (ok && live) own_v = row_norm<DP>(v_tile, tid & 127);
+                lift = lift_of(fmaf(a, own_v, d));
+            }
+        }
+        for (int j = 0; ok && idle && j < n; ++j) {
             if (!(ok = wait_warp(s_full, j & 1, ctl, p.timeout_ns))) break;
             arrive_warp(p_full, lane);
             if (!(ok = wait_warp(dp_full, j & 1, ctl, p.timeout_ns))) break;
@@ -313,7 +377,8 @@ __global__ void __launch_bounds__(Bwd<DP>::THREADS, Bwd<DP>::BLOCKS)
         WalkAt cw = {begin, 0, begin, begin + per_head};
         RingAt<ST> at;
         at.next();                                                 // dO_0
-        for (int j = 0; !idle && j < n; ++j) {
+        const float up = power_of_two(lift - 15);                  // p is lifted already
+        for (int j = 0; ok && !idle && j < n; ++j) {
             const float* rj = rows + (j % B::ROW_BUFS) * 2 * BN;
             if (!(ok = wait_warp(full(at.s), at.ph, ctl, p.timeout_ns))) break;
             at.next();
@@ -349,7 +414,7 @@ __global__ void __launch_bounds__(Bwd<DP>::THREADS, Bwd<DP>::BLOCKS)
                                           make_float2(c2, c2), make_float2(-l.z, -l.w));
                     const float v[4] = {ex2(a.x), ex2(a.y), ex2(b.x), ex2(b.y)};
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) s[c][e + k] = __float_as_uint(v[k]);
+                    for (int k = 0; k < 4; ++k) s[c][e + k] = __float_as_uint(kLifted<T> ? v[k] * up : v[k]);
                     w[e >> 1] = Io16<T>::pack(v[0], v[1]);
                     w[(e >> 1) + 1] = Io16<T>::pack(v[2], v[3]);
                 }
@@ -385,12 +450,18 @@ __global__ void __launch_bounds__(Bwd<DP>::THREADS, Bwd<DP>::BLOCKS)
             ptx::tc_fence_before();
             arrive_warp(ds_full, lane);
         }
+        if (kLifted<T> && half == 0 && n > 0) {   // the warps' largest |v|, for dq
+            own_v = warp_max(own_v);
+            if (lane == 0) p.v_most[(static_cast<long long>(hk) * (gridDim.x / p.kv_heads) + slot) * 4 + warp] = own_v;
+        }
         if (ok && n > 0) ok = wait_warp(done, 0, ctl, p.timeout_ns);
         if (ok && t.tile >= 0) {
             ptx::tc_fence_after();
             const long long at = static_cast<long long>(t.own.start) + row, col = static_cast<long long>(hk) * p.D;
-            if (half) store_accumulator<T>(t_dk + lanes, n > 0, live, static_cast<T*>(p.dk) + at * p.dk_stride + col, p.D, p.scale);
-            else store_accumulator<T>(t_dv + lanes, n > 0, live, static_cast<T*>(p.dv) + at * p.dv_stride + col, p.D, 1.f);
+            if (half) store_accumulator<T>(t_dk + lanes, n > 0, live, static_cast<T*>(p.dk) + at * p.dk_stride + col, p.D,
+                                           kLifted<T> ? p.scale * power_of_two(-lift) : p.scale);
+            else store_accumulator<T>(t_dv + lanes, n > 0, live, static_cast<T*>(p.dv) + at * p.dv_stride + col, p.D,
+                                      kLifted<T> ? power_of_two(-15) : 1.f);
         }
         ptx::tc_fence_before();
     }
@@ -563,12 +634,27 @@ __global__ void __launch_bounds__(Bwd<DP>::THREADS, Bwd<DP>::BLOCKS)
         bool ok = true;
         // a warp whose 32 queries all lie past the end only keeps the barriers' count
         const bool idle = t.tile < 0 || r0 + (warp & 3) * 32 >= t.own.len;
-        for (int j = 0; idle && j < n; ++j) {
+        // fp16: ds of this query lifted by its own |do| and delta and the largest |v| of the keys that the block walks
+        int lift = 0;
+        if constexpr (kLifted<T>) {
+            if (!idle && n > 0) {
+                const long long k_slots = p.k_rows / kTile + p.sequences;
+                const float* most = p.v_most + (hk * k_slots + (p.k_offsets ? kr.start / kTile + t.b : 0)) * 4;
+                const int values = (n * BN + kTile - 1) / kTile * 4;
+                float v = 0.f;
+                for (int i = lane; i < values; i += 32) v = fmaxf(v, most[i]);
+                v = warp_max(v);
+                ok = wait_warp(fixed_full, 0, ctl, p.timeout_ns);
+                if (ok) lift = lift_of(fmaf(row_norm<DP>(do_tile, threadIdx.x & 127), v, fabsf(delta)));
+            }
+        }
+        const float up = power_of_two(lift - 15), down = -delta * up;   // p is lifted already
+        for (int j = 0; ok && idle && j < n; ++j) {
             if (!(ok = wait_warp(s_full(j & 1), (j >> 1) & 1, ctl, p.timeout_ns))) break;
             if (!(ok = wait_warp(dp_full, j & 1, ctl, p.timeout_ns))) break;
             arrive_warp(ds_full, lane);
         }
-        for (int j = 0; !idle && j < n; ++j) {
+        for (int j = 0; ok && !idle && j < n; ++j) {
             const uint32_t ts = t_s(j) + lanes + half * HB, tdp = t_dp + lanes + half * HB;
             if (!(ok = wait_warp(s_full(j & 1), (j >> 1) & 1, ctl, p.timeout_ns))) break;
             ptx::tc_fence_after();
@@ -611,9 +697,10 @@ __global__ void __launch_bounds__(Bwd<DP>::THREADS, Bwd<DP>::BLOCKS)
                 }
 #pragma unroll
                 for (int e = 0; e < 32; e += 2) {
+                    const float2 dp = make_float2(__uint_as_float(d[e]), __uint_as_float(d[e + 1]));
                     const float2 a = mul2(make_float2(__uint_as_float(s[c][e]), __uint_as_float(s[c][e + 1])),
-                                          add2(make_float2(__uint_as_float(d[e]), __uint_as_float(d[e + 1])),
-                                               make_float2(-delta, -delta)));
+                                          kLifted<T> ? fma2(dp, make_float2(up, up), make_float2(down, down))
+                                                     : add2(dp, make_float2(-delta, -delta)));
                     w[e >> 1] = Io16<T>::pack(a.x, a.y);
                 }
                 tmem_st16(ts + c * 16, w);
@@ -626,7 +713,8 @@ __global__ void __launch_bounds__(Bwd<DP>::THREADS, Bwd<DP>::BLOCKS)
         if (ok && t.tile >= 0 && half == 0) {
             ptx::tc_fence_after();
             store_accumulator<T>(t_dq + lanes, n > 0, live,
-                                 static_cast<T*>(p.dq) + at * p.dq_stride + static_cast<long long>(h) * p.D, p.D, p.scale);
+                                 static_cast<T*>(p.dq) + at * p.dq_stride + static_cast<long long>(h) * p.D, p.D,
+                                 kLifted<T> ? p.scale * power_of_two(-lift) : p.scale);
         }
         ptx::tc_fence_before();
     }

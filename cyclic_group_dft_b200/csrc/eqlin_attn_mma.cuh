@@ -510,6 +510,38 @@ constexpr size_t short_bwd_smem() {
     return size_t(4) * 64 * kRowBytes<T, DP> + 2 * 64 * sizeof(float);
 }
 
+// fp16 (kLifted): ds of two rows, lifted so that the rows' largest values use the type's range.  The rows keep the
+// exponents `lift`; where a tile has values of 2^15 and more with them, the sums `acc` (zeros while `fresh`) move to a
+// smaller one, with three bits left so that this is rare.  Every lane of the warp must call it.
+template <int NT, int DT>
+__device__ __forceinline__ void lift_rows(float (&ds)[NT][4], float (&acc)[DT][4], int (&lift)[2], bool fresh) {
+    float m[2] = {0.f, 0.f};
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) m[i] = fmaxf(m[i], fmaxf(fabsf(ds[n][2 * i]), fabsf(ds[n][2 * i + 1])));
+    if (fresh || __any_sync(0xFFFFFFFFu, m[0] >= power_of_two(15 - lift[0]) || m[1] >= power_of_two(15 - lift[1]))) {
+        float fade[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int e = min(lift[i], lift_of(quad_max(m[i])) - 3);
+            fade[i] = power_of_two(e - lift[i]);
+            lift[i] = e;
+        }
+        if (!fresh) {
+#pragma unroll
+            for (int d = 0; d < DT; ++d)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[d][e] *= fade[e >> 1];
+        }
+    }
+    const float up[2] = {power_of_two(lift[0]), power_of_two(lift[1])};
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) ds[n][e] *= up[e >> 1];
+}
+
 // Of the warp's 16 rows from `warp_row` on: off = -lse log2(e) and delta = do . o of rows lane / 4 and lane / 4 + 8.
 template <class T, int RB>
 __device__ __forceinline__ void row_stats(const Params& p, int h, long long first_row, int warp_row, int n, int lane,
@@ -571,6 +603,7 @@ __device__ __forceinline__ void dq_short_tile(const Params& p, uint8_t* smem, in
 #pragma unroll
     for (int d = 0; d < DP / 8; ++d) dq[d][0] = dq[d][1] = dq[d][2] = dq[d][3] = 0.f;
     float off[2] = {0.f, 0.f}, delta[2];
+    int lift[2] = {kLiftMost, kLiftMost};
     if (on) {
         copy_tile<T, DP, M, WU * 32>(sq, p.q, p.q_stride, first_row, n, p.D, h, tid);
         copy_tile<T, DP, M, WU * 32>(sdo, p.dout, p.do_stride, first_row, n, p.D, h, tid);
@@ -604,13 +637,18 @@ __device__ __forceinline__ void dq_short_tile(const Params& p, uint8_t* smem, in
                 const bool vis = i * 8 + (lane & 3) * 2 + (e & 1) < last[e >> 1];
                 s[i][e] = vis ? ex2(fmaf(s[i][e], c2, off[e >> 1])) * (dp[i][e] - delta[e >> 1]) : 0.f;
             }
+        if constexpr (kLifted<T>) lift_rows<NT, DP / 8>(s, dq, lift, k0 == 0);
         weights_by_rows<T, DP, NT>(dq, s, sk, steps, la, lane);
     }
     cp_async_commit();
     cp_async_wait<0>();
     __syncthreads();
     if (!on) return;
-    const float mul[2] = {p.scale, p.scale};
+    float mul[2] = {p.scale, p.scale};
+    if constexpr (kLifted<T>) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) mul[i] *= power_of_two(-lift[i]);
+    }
     store_rows<T, DP>(dq, mul, sq, rw * 16, n, p.D,
                       static_cast<T*>(p.dq) + first_row * p.dq_stride + static_cast<long long>(h) * p.D, p.dq_stride, lane);
 }
@@ -693,7 +731,8 @@ __device__ __forceinline__ void bwd_one_tile(const Params& p, uint8_t* smem, int
     for (int i = 0; i < 2; ++i)
         if (on && row + 8 * i < n) {
             const float l = p.lse[static_cast<long long>(h) * p.q_rows + first_row + row + 8 * i];
-            off[i] = l == -INFINITY ? 0.f : -l * kLog2e;        // a row that sees no key: all of it is masked
+            // a row that sees no key: all of it is masked
+            off[i] = l == -INFINITY ? 0.f : fmaf(-l, kLog2e, kLiftP<T>);
         }
     float s[NT][4], dp[NT][4];
 #pragma unroll
@@ -707,6 +746,10 @@ __device__ __forceinline__ void bwd_one_tile(const Params& p, uint8_t* smem, int
     __syncthreads();
     float dq[DP / 8][4], acc[DP / 8][4];
     uint32_t w[NT][2], ds[NT][2];
+#pragma unroll
+    for (int d = 0; d < DP / 8; ++d) dq[d][0] = dq[d][1] = dq[d][2] = dq[d][3] = 0.f;
+    int lift[2] = {kLiftMost, kLiftMost};                   // fp16: of the rows for dq, and one of the head for dk
+    int* least = reinterpret_cast<int*>(smem + 4 * 64 * RB);      // the warps' smallest exponents
     if (work) {
         float sum = 0.f, delta[2];
 #pragma unroll
@@ -740,17 +783,46 @@ __device__ __forceinline__ void bwd_one_tile(const Params& p, uint8_t* smem, int
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 w[i][e] = Io16<T>::pack(s[i][2 * e], s[i][2 * e + 1]);
-                ds[i][e] = Io16<T>::pack(dp[i][2 * e], dp[i][2 * e + 1]);
+                if constexpr (!kLifted<T>) ds[i][e] = Io16<T>::pack(dp[i][2 * e], dp[i][2 * e + 1]);
             }
+        }
+        if constexpr (kLifted<T>) {
+            lift_rows<NT, DP / 8>(dp, dq, lift, true);
+#pragma unroll
+            for (int i = 0; i < NT; ++i)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) ds[i][e] = Io16<T>::pack(dp[i][2 * e], dp[i][2 * e + 1]);
         }
     } else {
 #pragma unroll
         for (int i = 0; i < NT; ++i) w[i][0] = w[i][1] = ds[i][0] = ds[i][1] = 0;
     }
-#pragma unroll
-    for (int d = 0; d < DP / 8; ++d) dq[d][0] = dq[d][1] = dq[d][2] = dq[d][3] = 0.f;
+    if constexpr (kLifted<T>) {
+        // (rows that do not exist or have ds = 0 keep the largest exponent)
+        int e = work ? min(lift[0], lift[1]) : kLiftMost;
+        e = __reduce_min_sync(0xFFFFFFFFu, e);
+        if (lane == 0) least[warp] = e;
+    }
     if (work) packed_by_rows<T, DP, NT>(dq, ds, sk, steps, la);
     __syncthreads();
+    int lift_dk = 0;
+    if constexpr (kLifted<T>) {
+        lift_dk = kLiftMost;
+#pragma unroll
+        for (int i = 0; i < WU; ++i) lift_dk = min(lift_dk, least[unit * WU + i]);
+        if (work) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                // a second rounding only of what is subnormal then
+                const __half2 f = __float2half2_rn(power_of_two(lift_dk - lift[e]));
+#pragma unroll
+                for (int i = 0; i < NT; ++i) {
+                    const __half2 d = __hmul2(reinterpret_cast<const __half2&>(ds[i][e]), f);
+                    ds[i][e] = reinterpret_cast<const uint32_t&>(d);
+                }
+            }
+        }
+    }
     if (work) {
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
@@ -767,9 +839,17 @@ __device__ __forceinline__ void bwd_one_tile(const Params& p, uint8_t* smem, int
     for (int d = 0; d < DP / 8; ++d) acc[d][0] = acc[d][1] = acc[d][2] = acc[d][3] = 0.f;
     if (key_work) columns_by_rows<T, DP, M>(acc, sv, rw, sdo, n, steps, la);
     __syncthreads();
-    const float mul[2] = {p.scale, p.scale}, one[2] = {1.f, 1.f};
+    float mul_dq[2] = {p.scale, p.scale}, mul[2] = {p.scale, p.scale}, one[2] = {1.f, 1.f};
+    if constexpr (kLifted<T>) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {                       // ds holds the lift of p as well
+            mul_dq[i] *= power_of_two(-lift[i] - 15);
+            mul[i] *= power_of_two(-lift_dk - 15);
+            one[i] = power_of_two(-15);
+        }
+    }
     // over the weights and dO, which all warps are done with; each warp in its own rows
-    if (work) store_rows<T, DP>(dq, mul, sv, rw * 16, n, p.D, static_cast<T*>(p.dq) + first_row * p.dq_stride + col, p.dq_stride, lane);
+    if (work) store_rows<T, DP>(dq, mul_dq, sv, rw * 16, n, p.D, static_cast<T*>(p.dq) + first_row * p.dq_stride + col, p.dq_stride, lane);
     if (key_work) {
         store_rows<T, DP>(acc, one, sdo, rw * 16, kn, p.D, static_cast<T*>(p.dv) + first_key * p.dv_stride + col, p.dv_stride, lane);
 #pragma unroll
@@ -815,6 +895,7 @@ __device__ __forceinline__ void dkv_short_tile(const Params& p, uint8_t* smem, i
     const int key = r0 + rw * 16 + (lane >> 2);
     const long long first_row = static_cast<long long>(t.own.start) + r0;
     float dk[DP / 8][4], dv[DP / 8][4];
+    int lift[2] = {kLiftMost, kLiftMost};
 #pragma unroll
     for (int d = 0; d < DP / 8; ++d)
 #pragma unroll
@@ -835,7 +916,7 @@ __device__ __forceinline__ void dkv_short_tile(const Params& p, uint8_t* smem, i
                 for (int i = tid; i < M; i += WU * 32) {
                     const long long stat = static_cast<long long>(h) * p.q_rows + qr.start + q0 + i;
                     const float l = i < qn ? p.lse[stat] : -INFINITY;
-                    slse[i] = l == -INFINITY ? INFINITY : l * kLog2e;      // weights of zero
+                    slse[i] = l == -INFINITY ? INFINITY : fmaf(l, kLog2e, -kLiftP<T>);      // weights of zero
                     sdelta[i] = i < qn ? p.delta[stat] : 0.f;
                 }
             }
@@ -865,6 +946,7 @@ __device__ __forceinline__ void dkv_short_tile(const Params& p, uint8_t* smem, i
                         dp[i][e] = w == 0.f ? 0.f : w * (dp[i][e] - (e & 1 ? dl.y : dl.x));
                     }
                 }
+                if constexpr (kLifted<T>) lift_rows<NT, DP / 8>(dp, dk, lift, g == 0 && q0 == begin && c0 == 0);
                 weights_by_rows<T, DP, NT>(dv, s, sdo + c0 * RB, steps, la, lane);
                 weights_by_rows<T, DP, NT>(dk, dp, sq + c0 * RB, steps, la, lane);
             }
@@ -874,7 +956,14 @@ __device__ __forceinline__ void dkv_short_tile(const Params& p, uint8_t* smem, i
     cp_async_wait<0>();
     __syncthreads();
     if (!on) return;
-    const float mul[2] = {p.scale, p.scale}, one[2] = {1.f, 1.f};
+    float mul[2] = {p.scale, p.scale}, one[2] = {1.f, 1.f};
+    if constexpr (kLifted<T>) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {                       // ds holds the lift of p as well
+            mul[i] *= power_of_two(-lift[i] - 15);
+            one[i] = power_of_two(-15);
+        }
+    }
     const long long col = static_cast<long long>(hk) * p.D;
     store_rows<T, DP>(dk, mul, sk, rw * 16, n, p.D, static_cast<T*>(p.dk) + first_row * p.dk_stride + col, p.dk_stride, lane);
     store_rows<T, DP>(dv, one, sv, rw * 16, n, p.D, static_cast<T*>(p.dv) + first_row * p.dv_stride + col, p.dv_stride, lane);

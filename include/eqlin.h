@@ -518,7 +518,8 @@ typedef struct {
  *   several query heads are the sums over them.
  *
  * 16-bit I/O multiplies on the tensor cores with fp32 accumulation; the weights exp(s - lse) and
- * ds are rounded to the I/O type before their products (fp16: a ds above 65504 becomes infinite).  fp32
+ * ds are rounded to the I/O type before their products (fp16 gradients: times powers of two that
+ * keep the largest of a row or tile in range, so that neither large nor small ones are lost).  fp32
  * I/O: fp32 arithmetic, or products of three tf32 tensor-core products (within 2^-19.6 of each
  * term; an infinite value counts as NaN there).  Statistics are fp32.  No atomics: repeated calls give the same bits.
  * Rows that no sequence covers (behind the last one) are not read and not written.  A row holding

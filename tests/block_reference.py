@@ -55,12 +55,13 @@ def offsets(lens, device=None) -> torch.Tensor:
     return t.to(torch.int32).to(device) if device else t.to(torch.int32)
 
 
-def attention(q, k, v, do, q_lens, k_lens, heads, kv_heads, causal, scale=None, chained=False):
+def attention(q, k, v, do, q_lens, k_lens, heads, kv_heads, causal, scale=None, chained=False, o_err=0.0):
     """{"o", "lse", "dq", "dk", "dv"} in float64 and {name: bound} for kernels of q's dtype, for
     q [Nq, H Dh, G], k and v [Nk, Hk Dh, G]; the gradients are those for o rounded to q's dtype.
     chained: the gradients were given the kernel's own o and lse.  Then o is off by up to its bound, which
     moves delta_i = do_i . o_i by up to sum_d |do_id| bound(o_id), and lse by up to its bound, which
-    moves every weight by that much relative to itself."""
+    moves every weight by that much relative to itself.  o_err: what each element of the o given to them is off
+    by beside its rounding."""
     T, u, t0 = q.dtype, unit(q.dtype), tiny(q.dtype)
     if T == torch.float32:
         p_round, ds_round = 0.0, 0.0          # fp32 keeps them unrounded
@@ -99,7 +100,7 @@ def attention(q, k, v, do, q_lens, k_lens, heads, kv_heads, causal, scale=None, 
             ot = o.to(T).double()
             dp, delta = w @ z.T, (w * ot).sum(1)
             dp_err = M * (w.abs() @ z.abs().T)
-            delta_err = E * (w.abs() * ot.abs()).sum(1)
+            delta_err = E * (w.abs() * ot.abs()).sum(1) + o_err * w.abs().sum(1)
             ds = p * (dp - delta[:, None])
             p32 = p_err - p * p_round - t0 * (p > 0)             # ds is formed from unrounded weights
             if chained:

@@ -350,6 +350,66 @@ def test_attention_with_one_weight_far_above_the_others(dtype):
     _check_attention(got, want, bound)
 
 
+@pytest.mark.parametrize("lens,k_lens,H,Hk,D,causal", [
+    ([700], None, 2, 2, 64, False), ([700], None, 2, 1, 128, True), ([130, 300], None, 4, 2, 72, True),   # tiles of 128
+    ([5, 200], [900, 640], 3, 3, 64, False),
+    ([49] * 4, None, 3, 3, 128, False), ([30, 17], None, 2, 2, 64, True), ([12] * 5, None, 5, 5, 40, False),   # one tile
+    ([60] * 3, None, 4, 2, 64, True), ([13, 16], None, 6, 2, 128, False), ([8, 8, 8, 150], None, 2, 2, 64, False),
+])
+@pytest.mark.parametrize("do_exp,v_exp,q_exp,k_exp", [
+    (-14, -6, -8, 8), (-14, -6, 8, -8), (-12, 3, -6, 6),          # ds below fp16's smallest number, or among its subnormal ones
+    (12, 8, -4, -4), (11, -2, -4, -4), (0, 9, -2, -2),            # and above its largest
+])
+def test_fp16_gradients_of_small_and_large_values(lens, k_lens, H, Hk, D, causal, do_exp, v_exp, q_exp, k_exp):
+    """The gradients are linear in dO and, with o, in V: those of dO 2^a and V 2^b are 2^(a+b) times (dv: 2^a) those of
+    values near 1, whose bounds hold for them too, but for the rounding of outputs (and of the given o) near zero: ds must
+    not be lost because it is small, nor become infinite because it is large."""
+    k_lens, dtype, G = lens if k_lens is None else k_lens, torch.float16, math.gcd(4, D)
+    Dh, Nq, Nk = D // G, sum(lens), sum(k_lens)
+
+    def pair(n, h, seed, e):         # values near 1, in steps of 2^-10, and the same times 2^e: both are fp16 numbers
+        near = (_randn(n, h * Dh, G, seed=seed, dtype=torch.float16).float() * 1024).round() / 1024
+        t = (near * 2.0 ** e).half()
+        assert torch.isfinite(t).all() and torch.equal(near.double() * 2.0 ** e, t.double())
+        return t.to(DEV), near.half()
+
+    (q, q1), (k, k1), (v, v1), (do, do1) = pair(Nq, H, 1, q_exp), pair(Nk, Hk, 2, k_exp), pair(Nk, Hk, 3, v_exp), pair(Nq, H, 4, do_exp)
+    scale = D ** -0.5
+    want, bound = ref.attention(q1, k1, v1, do1, lens, k_lens, H, Hk, causal, scale=scale * 2.0 ** (q_exp + k_exp),
+                                o_err=ref.tiny(dtype) * 2.0 ** -v_exp)
+    o = (want["o"].half().float() * 2.0 ** v_exp).half()
+    kw = dict(heads=H, kv_heads=Hk, causal=causal, q_offsets=ref.offsets(lens, DEV), k_offsets=ref.offsets(k_lens, DEV))
+    got = eq.eqlin_attention_backward(do, q, k, v, o.to(DEV), want["lse"].float().to(DEV), **kw)
+    # the reference has 2^(q_exp + k_exp) in its scale, and k or q near 1
+    for name, t, e in (("dq", got[0], do_exp + v_exp - q_exp), ("dk", got[1], do_exp + v_exp - k_exp), ("dv", got[2], do_exp)):
+        t = t.double().cpu()
+        # a gradient itself may be above fp16's largest number: it may be infinite where its bound reaches that far
+        most = torch.finfo(dtype).max
+        past = t.isinf() & (t.sign() == want[name].sign()) & ((want[name].abs() + bound[name]) * 2.0 ** e > most)
+        t = torch.where(past, want[name] * 2.0 ** e, t)
+        assert past.double().mean() < 0.05
+        within(t * 2.0 ** -e, want[name], bound[name] + ref.tiny(dtype) * 2.0 ** -e, name)
+
+
+@pytest.mark.parametrize("D,H,Hk,a,b", [(128, 1, 1, 300, 4096), (64, 2, 1, 4096, 200), (64, 2, 2, 50, 3000)])
+@pytest.mark.parametrize("which", ["dq", "dk", "dv"])
+def test_fp16_gradients_keep_their_precision_over_long_sequences(D, H, Hk, a, b, which):
+    """Thousands of keys (or queries) and dO of 2^-10: ds and small weights lie where fp16 has few bits left.  Normwise:
+    ds and p are rounded once, the output once, each by at most u relative, independently and so by u / sqrt(3) in the
+    mean square: u sqrt(2 / 3) together; twice u leaves room for fp32.  k, or q, is large so that the gradient itself
+    is no subnormal number."""
+    G, u, e = 4, ref.unit(torch.float16), {"dq": 7, "dk": -7, "dv": 0}[which]
+    q, do = _randn(a, H * D // G, G, seed=1, dtype=torch.float16, std=2.0 ** -e), _randn(a, H * D // G, G, seed=2, dtype=torch.float16, std=2.0 ** -10)
+    k, v = (_randn(b, Hk * D // G, G, seed=s, dtype=torch.float16, std=d) for s, d in ((3, 2.0 ** e), (4, 1.0)))
+    if which == "dv":
+        do = do * 64
+    want, _ = ref.attention(q, k, v, do, [a], [b], H, Hk, False)
+    got = eq.eqlin_attention_backward(do.to(DEV), q.to(DEV), k.to(DEV), v.to(DEV), want["o"].half().to(DEV),
+                                      want["lse"].float().to(DEV), heads=H, kv_heads=Hk)[["dq", "dk", "dv"].index(which)]
+    err = float((got.double().cpu() - want[which]).norm() / want[which].norm())
+    assert err <= 2 * u, (err, u)
+
+
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("lens", [[49, 3, 20], [130, 5, 260]])
 @pytest.mark.parametrize("causal", [False, True])
