@@ -132,20 +132,22 @@ __device__ __forceinline__ int first_query(int first, int q_len, int k_len, int 
 }
 
 // The gradients round p and ds to the I/O type before their products.  fp16 loses what is below 2^-14 there and has
-// nothing above 65504, so both are lifted by powers of two, which the outputs take back exactly: p <= 1 by 2^15, ds by
-// what its largest value, or a bound of it, allows (row by row, see the kernels).  Without it, 784 tokens with dO of
-// 2^-14 and v of 2^-6 lost dq whole.  What it costs, against no lift: 4096 windows of 49, 3 heads of 128 features 323 to
-// 333 us; 784 tokens, 32 sequences, 8 heads of 64 238 to 255; 8192 tokens 571 to 592; 100 tokens, 300 sequences 165 to
-// 184; 64 queries, 128 keys, 64 sequences, 8 heads on 2 71 to 79.
+// nothing above 65504, so both are lifted by powers of two, which the outputs take back exactly: p <= 1 by 2^12, ds
+// to below 2^13 by what its largest value, or a bound of it for p <= 1, allows (row by row, see the kernels).  That
+// leaves room for p above 1, where scores of 10^7 and more leave exp(s - lse) no correct bit.  Without the lift, 784
+// tokens with dO of 2^-14 and v of 2^-6 lost dq whole.  What it costs, against none: 4096 windows of 49, 3 heads of 128
+// features 323 to 333 us; 784 tokens, 32 sequences, 8 heads of 64 238 to 255; 8192 tokens 571 to 592; 100 tokens, 300
+// sequences 165 to 184; 64 queries, 128 keys, 64 sequences, 8 heads on 2 71 to 79.
 template <class T>
 constexpr bool kLifted = std::is_same<T, __half>::value;
+constexpr int kLiftP = 12;
 template <class T>
-constexpr float kLiftP = kLifted<T> ? 15.f : 0.f;
-constexpr int kLiftMost = 94;
-// The exponent e for values of up to `most`: most * 2^e < 2^15.  Infinite and vanishing ones get a finite e.
+constexpr float kLiftOf = kLifted<T> ? static_cast<float>(kLiftP) : 0.f;
+constexpr int kLiftMost = 92;
+// The exponent e for values of up to `most`: most * 2^e < 2^13.  Infinite and vanishing ones get a finite e.
 __device__ __forceinline__ int lift_of(float most) {
     const int e = static_cast<int>((__float_as_uint(most) >> 23) & 255u) - 127;
-    return 14 - max(14 - kLiftMost, min(e, 80));
+    return 12 - max(12 - kLiftMost, min(e, 80));
 }
 __device__ __forceinline__ float power_of_two(int e) { return __uint_as_float(static_cast<uint32_t>(max(e, -126) + 127) << 23); }
 

@@ -143,7 +143,7 @@ __global__ void __launch_bounds__(256) eqlin_attn_stats_kernel(const Params p) {
         if (LIFT && fabsf(sum) < INFINITY) most = fmaxf(most, fabsf(sum));
         if (lane == 0) {
             const float l = r < n ? p.lse[static_cast<long long>(h) * p.q_rows + first + r] : -INFINITY;
-            out[r] = l == -INFINITY ? INFINITY : fmaf(l, kLog2e, -kLiftP<T>);
+            out[r] = l == -INFINITY ? INFINITY : fmaf(l, kLog2e, -kLiftOf<T>);
             out[kTile + r] = sum;
         }
     }
@@ -377,7 +377,7 @@ __global__ void __launch_bounds__(Bwd<DP>::THREADS, Bwd<DP>::BLOCKS)
         WalkAt cw = {begin, 0, begin, begin + per_head};
         RingAt<ST> at;
         at.next();                                                 // dO_0
-        const float up = power_of_two(lift - 15);                  // p is lifted already
+        const float up = power_of_two(lift - kLiftP);                  // p is lifted already
         for (int j = 0; ok && !idle && j < n; ++j) {
             const float* rj = rows + (j % B::ROW_BUFS) * 2 * BN;
             if (!(ok = wait_warp(full(at.s), at.ph, ctl, p.timeout_ns))) break;
@@ -461,7 +461,7 @@ __global__ void __launch_bounds__(Bwd<DP>::THREADS, Bwd<DP>::BLOCKS)
             if (half) store_accumulator<T>(t_dk + lanes, n > 0, live, static_cast<T*>(p.dk) + at * p.dk_stride + col, p.D,
                                            kLifted<T> ? p.scale * power_of_two(-lift) : p.scale);
             else store_accumulator<T>(t_dv + lanes, n > 0, live, static_cast<T*>(p.dv) + at * p.dv_stride + col, p.D,
-                                      kLifted<T> ? power_of_two(-15) : 1.f);
+                                      kLifted<T> ? power_of_two(-kLiftP) : 1.f);
         }
         ptx::tc_fence_before();
     }
@@ -648,7 +648,7 @@ __global__ void __launch_bounds__(Bwd<DP>::THREADS, Bwd<DP>::BLOCKS)
                 if (ok) lift = lift_of(fmaf(row_norm<DP>(do_tile, threadIdx.x & 127), v, fabsf(delta)));
             }
         }
-        const float up = power_of_two(lift - 15), down = -delta * up;   // p is lifted already
+        const float up = power_of_two(lift - kLiftP), down = -delta * up;   // p is lifted already
         for (int j = 0; ok && idle && j < n; ++j) {
             if (!(ok = wait_warp(s_full(j & 1), (j >> 1) & 1, ctl, p.timeout_ns))) break;
             if (!(ok = wait_warp(dp_full, j & 1, ctl, p.timeout_ns))) break;

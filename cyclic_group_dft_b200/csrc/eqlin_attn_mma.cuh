@@ -512,7 +512,7 @@ constexpr size_t short_bwd_smem() {
 
 // fp16 (kLifted): ds of two rows, lifted so that the rows' largest values use the type's range.  The rows keep the
 // exponents `lift`; where a tile has values of 2^15 and more with them, the sums `acc` (zeros while `fresh`) move to a
-// smaller one, with three bits left so that this is rare.  Every lane of the warp must call it.
+// smaller one, with two bits left so that this is rare.  Every lane of the warp must call it.
 template <int NT, int DT>
 __device__ __forceinline__ void lift_rows(float (&ds)[NT][4], float (&acc)[DT][4], int (&lift)[2], bool fresh) {
     float m[2] = {0.f, 0.f};
@@ -524,7 +524,7 @@ __device__ __forceinline__ void lift_rows(float (&ds)[NT][4], float (&acc)[DT][4
         float fade[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            const int e = min(lift[i], lift_of(quad_max(m[i])) - 3);
+            const int e = min(lift[i], lift_of(quad_max(m[i])));
             fade[i] = power_of_two(e - lift[i]);
             lift[i] = e;
         }
@@ -732,7 +732,7 @@ __device__ __forceinline__ void bwd_one_tile(const Params& p, uint8_t* smem, int
         if (on && row + 8 * i < n) {
             const float l = p.lse[static_cast<long long>(h) * p.q_rows + first_row + row + 8 * i];
             // a row that sees no key: all of it is masked
-            off[i] = l == -INFINITY ? 0.f : fmaf(-l, kLog2e, kLiftP<T>);
+            off[i] = l == -INFINITY ? 0.f : fmaf(-l, kLog2e, kLiftOf<T>);
         }
     float s[NT][4], dp[NT][4];
 #pragma unroll
@@ -843,9 +843,9 @@ __device__ __forceinline__ void bwd_one_tile(const Params& p, uint8_t* smem, int
     if constexpr (kLifted<T>) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {                       // ds holds the lift of p as well
-            mul_dq[i] *= power_of_two(-lift[i] - 15);
-            mul[i] *= power_of_two(-lift_dk - 15);
-            one[i] = power_of_two(-15);
+            mul_dq[i] *= power_of_two(-lift[i] - kLiftP);
+            mul[i] *= power_of_two(-lift_dk - kLiftP);
+            one[i] = power_of_two(-kLiftP);
         }
     }
     // over the weights and dO, which all warps are done with; each warp in its own rows
@@ -916,7 +916,7 @@ __device__ __forceinline__ void dkv_short_tile(const Params& p, uint8_t* smem, i
                 for (int i = tid; i < M; i += WU * 32) {
                     const long long stat = static_cast<long long>(h) * p.q_rows + qr.start + q0 + i;
                     const float l = i < qn ? p.lse[stat] : -INFINITY;
-                    slse[i] = l == -INFINITY ? INFINITY : fmaf(l, kLog2e, -kLiftP<T>);      // weights of zero
+                    slse[i] = l == -INFINITY ? INFINITY : fmaf(l, kLog2e, -kLiftOf<T>);      // weights of zero
                     sdelta[i] = i < qn ? p.delta[stat] : 0.f;
                 }
             }
@@ -960,8 +960,8 @@ __device__ __forceinline__ void dkv_short_tile(const Params& p, uint8_t* smem, i
     if constexpr (kLifted<T>) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {                       // ds holds the lift of p as well
-            mul[i] *= power_of_two(-lift[i] - 15);
-            one[i] = power_of_two(-15);
+            mul[i] *= power_of_two(-lift[i] - kLiftP);
+            one[i] = power_of_two(-kLiftP);
         }
     }
     const long long col = static_cast<long long>(hk) * p.D;
