@@ -64,19 +64,23 @@ def _run(name: str, device: int, *args) -> None:
 
 
 def _in_stream(f):
-    """Gives a function its keyword `stream` (a torch Stream or a cudaStream_t as a number; default: the current
-    stream): the whole call, its allocations among it, is made with that stream current.  What it allocates
-    then belongs to that stream, and a workspace that is given up on return is not reused before the kernels
-    are done with it."""
+    """Gives a function its keyword `stream` (a torch Stream of the tensors' device or a cudaStream_t as a number;
+    default: the current stream): the whole call, its allocations among it, is made with that stream current.
+    What it allocates then belongs to that stream, and a workspace that is given up on return is not reused
+    before the kernels are done with it."""
 
     @functools.wraps(f)
     def call(*args, stream=None, **kwargs):
         if stream is None:
             return f(*args, **kwargs)
+        device = next((t.device for t in (*args, *kwargs.values()) if isinstance(t, torch.Tensor)), None)
+        if device is None or device.type != "cuda":
+            return f(*args, **kwargs)               # which says what is wrong with the tensors
         if not isinstance(stream, torch.cuda.Stream):
-            device = (args[0] if args else next(iter(kwargs.values()))).device
             stream = torch.cuda.ExternalStream(int(stream), device=device) if int(stream) else \
                 torch.cuda.default_stream(device)
+        elif stream.device != device:
+            raise ValueError(f"stream must be a stream of {device}, got one of {stream.device}")
         with torch.cuda.stream(stream):
             return f(*args, **kwargs)
 

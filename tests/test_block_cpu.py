@@ -2,6 +2,7 @@
 points validate sizes, dtypes, pointers, alignment and workspaces before any CUDA work."""
 from __future__ import annotations
 
+import contextlib
 import ctypes
 
 import pytest
@@ -163,6 +164,37 @@ def test_binding_refuses_cpu_tensors_and_wrong_shapes():
                  lambda: eq.eqlin_add_rmsnorm(torch.zeros(4, 8))):
         with pytest.raises(ValueError):
             call()
+
+
+def test_binding_refuses_a_stream_of_another_device(monkeypatch):
+    """With stand-ins for the stream and the tensor, so that one device or none is enough."""
+
+    class Stream:
+        device = torch.device("cuda:1")
+
+    class Tensor:
+        device = torch.device("cuda:0")
+
+    called = []
+    with monkeypatch.context() as m:
+        m.setattr(_block.torch.cuda, "Stream", Stream)
+        m.setattr(_block.torch, "Tensor", Tensor)
+        m.setattr(_block.torch.cuda, "stream", lambda s: contextlib.nullcontext(called.append(s)))
+        call = _block._in_stream(lambda *a, **k: "done")
+        for args, kwargs in (((Tensor(),), {}), ((), {"heads": 2, "x": Tensor()})):
+            with pytest.raises(ValueError, match="stream of cuda:0"):
+                call(*args, stream=Stream(), **kwargs)
+            right = Stream()
+            right.device = Tensor.device
+            assert call(*args, stream=right, **kwargs) == "done" and called == [right]
+            called.clear()
+
+
+def test_binding_with_a_stream_refuses_cpu_tensors():
+    x = torch.zeros(4, 8, 4, dtype=torch.bfloat16)
+    for stream in (0, 256):
+        with pytest.raises(ValueError):
+            eq.eqlin_attention_forward(heads=1, q=x, k=x, v=x, stream=stream)
 
 
 @pytest.mark.skipif(torch.cuda.is_available(), reason="checks behaviour without a GPU")

@@ -599,6 +599,19 @@ def test_calls_on_a_given_stream():
         assert all(torch.equal(a, b) for a, b in zip(got, want))
 
 
+def test_stream_numbers_with_keyword_arguments_in_any_order():
+    x = _randn(30, 16, 4, seed=1, dtype=torch.bfloat16).to(DEV)
+    pos = torch.arange(30, dtype=torch.int32, device=DEV)[:, None].contiguous()
+    want = eq.eqlin_rope(x, pos, 2, (4,)), eq.eqlin_attention_forward(x, x, x, 2)[0]
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for stream in (side.cuda_stream, side, 0):
+        y = eq.eqlin_rope(heads=2, sections=(4,), positions=pos, x=x, stream=stream)
+        o, _ = eq.eqlin_attention_forward(heads=2, causal=False, v=x, k=x, q=x, stream=stream)
+        torch.cuda.synchronize()
+        assert torch.equal(y, want[0]) and torch.equal(o, want[1])
+
+
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 def test_transformer_block(dtype):
     """norm -> joint projection -> rotary positions -> attention -> projection -> add and norm, forward
