@@ -19,7 +19,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libeqlin.so")
-OBJ = os.path.join(PKG, "_build")   # one object file and one dependency list per source
+OBJ = os.path.join(PKG, "_build")   # one object file, dependency list and command line per source
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
@@ -50,10 +50,14 @@ def nvcc() -> str:
     return cand if os.path.exists(cand) else "nvcc"
 
 
-def _object_stale(obj: str, dep: str) -> bool:
-    """Is the object older than its source, one of the headers it included, or this file?"""
-    if not (os.path.exists(obj) and os.path.exists(dep)):
+def _object_stale(obj: str, dep: str, made_by: str, command: str) -> bool:
+    """Is the object older than its source, one of the headers it included, or this file, or was it made by another
+    command (other flags, or another tree of which this one is a copy)?"""
+    if not (os.path.exists(obj) and os.path.exists(dep) and os.path.exists(made_by)):
         return True
+    with open(made_by) as f:
+        if f.read() != command:
+            return True
     t = os.path.getmtime(obj)
     with open(dep) as f:
         names = f.read().split(":", 1)[-1].replace("\\\n", " ").split()
@@ -63,22 +67,27 @@ def _object_stale(obj: str, dep: str) -> bool:
 
 def _compile(src: str, force: bool, verbose: bool, extra: list[str]) -> str:
     stem = os.path.join(OBJ, os.path.splitext(os.path.basename(src))[0])
-    obj, dep = stem + ".o", stem + ".d"
-    if force or extra or _object_stale(obj, dep):
+    obj, dep, made_by = stem + ".o", stem + ".d", stem + ".cmd"
+    cmd = [nvcc(), *NVCC_FLAGS, *extra, "-I", INCLUDE, "-I", CSRC, "-c", src]
+    if force or _object_stale(obj, dep, made_by, "\n".join(cmd)):
         tmp = f"{stem}.tmp{os.getpid()}"
-        cmd = [nvcc(), *NVCC_FLAGS, *extra, "-I", INCLUDE, "-I", CSRC, "-MD", "-MF", tmp + ".d",
-               "-c", "-o", tmp + ".o", src]
+        run = [*cmd, "-MD", "-MF", tmp + ".d", "-o", tmp + ".o"]
         if verbose:
-            print(" ".join(cmd), file=sys.stderr)
-        subprocess.run(cmd, check=True)
+            print(" ".join(run), file=sys.stderr)
+        subprocess.run(run, check=True)
+        if os.path.exists(made_by):
+            os.remove(made_by)          # none while the object and its list are replaced
         os.replace(tmp + ".d", dep)
         os.replace(tmp + ".o", obj)
+        with open(tmp + ".cmd", "w") as f:
+            f.write("\n".join(cmd))
+        os.replace(tmp + ".cmd", made_by)
     return obj
 
 
 def build(force: bool = False, verbose: bool = False, extra: list[str] | None = None) -> str:
     """Compile libeqlin.so unless it is newer than every source (sources in parallel, each
-    only when it or a header that it includes changed)."""
+    only when it, a header that it includes or its command line changed)."""
     if not force and up_to_date():
         return LIB
     os.makedirs(OBJ, exist_ok=True)
