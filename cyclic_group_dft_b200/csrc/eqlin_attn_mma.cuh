@@ -725,7 +725,7 @@ __device__ __forceinline__ void bwd_one_tile(const Params& p, uint8_t* smem, int
 #pragma unroll
     for (int c = 0; c < RB / 32; ++c) {
         const int first = (2 * c + (lane & 1)) * 8;
-        o[c] = on && dr < n && first < p.D ? __ldg(reinterpret_cast<const uint4*>(po + first)) : make_uint4(0, 0, 0, 0);
+        o[c] = on && dr < n && first < p.D ? *reinterpret_cast<const uint4*>(po + first) : make_uint4(0, 0, 0, 0);
     }
 #pragma unroll
     for (int i = 0; i < 2; ++i)

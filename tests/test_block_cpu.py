@@ -4,12 +4,14 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import glob
+import os
 
 import pytest
 import torch
 
 import cyclic_group_dft_b200 as eq
-from cyclic_group_dft_b200 import _block
+from cyclic_group_dft_b200 import _block, build
 
 LIB = eq.library()
 BF, F16, F32 = eq.EQLIN_BF16, eq.EQLIN_F16, eq.EQLIN_F32
@@ -195,6 +197,18 @@ def test_binding_with_a_stream_refuses_cpu_tensors():
     for stream in (0, 256):
         with pytest.raises(ValueError):
             eq.eqlin_attention_forward(heads=1, q=x, k=x, v=x, stream=stream)
+
+
+def test_kernels_read_by_coherent_loads():
+    """The block operators' kernels start while the kernel before them still runs, and read what it writes.  The
+    non-coherent path is for memory that nothing writes while a kernel runs, and its loads may be moved
+    before the wait for that kernel."""
+    for path in glob.glob(os.path.join(build.CSRC, "eqlin_attn*")) + [os.path.join(build.CSRC, f"eqlin_{n}.cuh")
+                                                                    for n in ("norm", "rope", "vec")]:
+        with open(path) as f:
+            text = f.read()
+        for word in ("__ldg", "ld.global.nc", "__ldcs", "__restrict__"):
+            assert word not in text, (path, word)
 
 
 @pytest.mark.skipif(torch.cuda.is_available(), reason="checks behaviour without a GPU")
