@@ -20,7 +20,7 @@ using namespace eqlin::host;
 using eqlin::report;
 namespace attn = eqlin::attn;
 
-constexpr int64_t kMaxRows = int64_t(1) << 31;
+constexpr int64_t kMaxRows = (int64_t(1) << 31) - 1024;   // rows past the end of the last tile are counted in 32 bits too
 constexpr int64_t kMaxStride = int64_t(1) << 38;   // (a TMA stride is below 2^40 bytes)
 
 int check_shape(const eqlin_attention_shape* a) {
@@ -39,7 +39,7 @@ int check_shape(const eqlin_attention_shape* a) {
     if (a->head_dim % 8 || a->head_dim > 128)
         return report(EQLIN_ERR_UNSUPPORTED, "head_dim must be a multiple of 8 and at most 128");
     if (a->heads > 65535 || a->q_rows >= kMaxRows || a->k_rows >= kMaxRows || a->sequences >= (int64_t(1) << 24))
-        return report(EQLIN_ERR_UNSUPPORTED, "fewer than 65536 heads, 2^31 rows and 2^24 sequences are supported");
+        return report(EQLIN_ERR_UNSUPPORTED, "fewer than 65536 heads, 2^31 - 1024 rows and 2^24 sequences are supported");
     if (!aligned(a->q_offsets, 4) || !aligned(a->k_offsets, 4))
         return report(EQLIN_ERR_MISALIGNED, "the offsets must be 4-byte aligned");
     return EQLIN_OK;
@@ -178,7 +178,7 @@ Fwd forward_kind(const eqlin_attention_shape& a) {
     const int64_t n = a.sequences, packed = a.q_rows * (a.heads / a.kv_heads);
     const int64_t few_tiles = std::max(n, (packed + 15) / 16) * a.kv_heads;     // blocks without splits
     const int64_t short_tiles = std::max(n, (a.q_rows + 63) / 64) * a.heads;
-    if (a.k_rows >= 128 * n && packed < (int64_t(1) << 31)) {   // (packed rows are counted in 32 bits)
+    if (a.k_rows >= 128 * n && packed < kMaxRows) {   // (packed rows are counted in 32 bits)
         const bool longer = a.k_rows >= 512 * n;
         if (few_tiles <= kB200Sms && (packed <= 16 * n || (packed <= 128 * n && longer))) return Fwd::kFew;
         if (few_tiles * (longer ? 2 : 4) <= short_tiles) return Fwd::kFew;

@@ -163,7 +163,7 @@ __global__ void __launch_bounds__(kThreads) eqlin_attn_fwd_f32_kernel(const Para
         const float *sk = skv + (k & 1) * 2 * S::WALK, *sv = sk + S::WALK;
         float s[4] = {};
         dot_tile<DP>(sq, sk, ty, tx, s);
-        const int last = p.causal ? r0 + ty + kr.len - t.own.len : kr.len - 1;
+        const int last = p.causal ? r0 + ty - t.own.len + kr.len : kr.len - 1;
         float m = -INFINITY;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -250,7 +250,7 @@ __device__ __forceinline__ void dkv_tile(const Params& p, float* smem, int slot,
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const int key = r0 + ty, query = q0 + tx + 16 * j;
-            const bool vis = !p.causal || key <= query + t.own.len - qr.len;
+            const bool vis = !p.causal || key <= query - qr.len + t.own.len;
             const float w = vis ? exp2f(s[j] * c2 - slse[tx + 16 * j]) : 0.f;
             sp[ty * kPS + tx + 16 * j] = w;
             sds[ty * kPS + tx + 16 * j] = vis ? w * (dp[j] - sdelta[tx + 16 * j]) : 0.f;
@@ -299,7 +299,7 @@ __device__ __forceinline__ void dq_tile(const Params& p, float* smem, int slot, 
         float s[4] = {}, dp[4] = {};
         dot_tile<DP>(sq, sk, ty, tx, s);
         dot_tile<DP>(sdo, sv, ty, tx, dp);
-        const int last = p.causal ? r0 + ty + kr.len - t.own.len : kr.len - 1;
+        const int last = p.causal ? r0 + ty - t.own.len + kr.len : kr.len - 1;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const int col = k * kN + tx + 16 * j;

@@ -468,7 +468,7 @@ __device__ __forceinline__ void fwd_short_tile(const Params& p, uint8_t* smem, i
             int last[2];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                const int lim = p.causal ? r0 + row + 8 * i + 1 + kr.len - t.own.len - k0 : kn;
+                const int lim = p.causal ? r0 + row + 8 * i + 1 - t.own.len + kr.len - k0 : kn;
                 last[i] = min(lim, kn);
             }
             softmax_step<NT, DP / 8>(s, o, top, sum, last, p.causal ? 0 : kn, k0 == 0, c2, lane);
@@ -629,7 +629,7 @@ __device__ __forceinline__ void dq_short_tile(const Params& p, uint8_t* smem, in
         rows_by_rows<T, DP, NT>(dp, sdo + rw * 16 * RB, sv, steps, la);
         int last[2];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) last[i] = min(kn, p.causal ? r0 + row + 8 * i + 1 + kr.len - t.own.len - k0 : kn);
+        for (int i = 0; i < 2; ++i) last[i] = min(kn, p.causal ? r0 + row + 8 * i + 1 - t.own.len + kr.len - k0 : kn);
 #pragma unroll
         for (int i = 0; i < NT; ++i)
 #pragma unroll

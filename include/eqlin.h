@@ -490,7 +490,7 @@ EQLIN_API int eqlin_rope(const void* x, const int32_t* positions, void* y, int64
  * adds nothing to any gradient.
  */
 typedef struct {
-    int64_t q_rows, k_rows;     /* rows of q and o; rows of k and v (< 2^31) */
+    int64_t q_rows, k_rows;     /* rows of q and o; rows of k and v (< 2^31 - 1024) */
     int64_t sequences;          /* >= 1 */
     int64_t heads, kv_heads;    /* heads a multiple of kv_heads */
     int64_t head_dim;           /* features of a head: a multiple of 8, at most 128 */

@@ -124,6 +124,16 @@ def test_attention_refusals(change, status):
     assert eq.eqlin_last_error()
 
 
+@pytest.mark.parametrize("side", ["q_rows", "k_rows"])
+def test_attention_row_limit_leaves_room_for_the_last_tile(side):
+    """Kernels count rows in 32 bits, up to the end of a tile that begins before the last row."""
+    n = ctypes.c_size_t()
+    for rows, status in (((1 << 31) - 1, UNSUP), ((1 << 31) - 1024, UNSUP), ((1 << 31) - 1025, OK)):
+        s = _shape(heads=1, kv_heads=1, head_dim=8, q_stride=8, k_stride=8, v_stride=8, o_stride=8, **{side: rows})
+        for backward in (0, 1):
+            assert LIB.eqlin_attention_workspace_size(ctypes.byref(s), backward, ctypes.byref(n)) == status
+
+
 def test_attention_pointer_refusals():
     s, big = _shape(), 1 << 30
     ref = ctypes.byref(s)
