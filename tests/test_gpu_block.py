@@ -312,6 +312,17 @@ def test_attention_of_many_tiles(n, q_most, k_most, H, Hk, D, causal, dtype):
     _check_attention(*_attention(q_lens, k_lens, H, Hk, D, causal, dtype, seed=n))
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("lens,k_lens,H,Hk,D,causal", [
+    ([3] * 300 + [1500] + [7] * 200, None, 2, 1, 64, True),     # one long sequence among many short ones
+    ([20] * 60 + [900], [20] * 60 + [1100], 2, 2, 128, False),
+    ([1200], None, 6, 2, 128, True), ([900, 1, 700], None, 4, 1, 64, False),   # long ones with shared key heads
+    ([700], [1900], 4, 2, 96, True),
+])
+def test_attention_of_outliers_and_long_sequences(lens, k_lens, H, Hk, D, causal, dtype):
+    _check_attention(*_attention(lens, lens if k_lens is None else k_lens, H, Hk, D, causal, dtype, seed=D))
+
+
 @pytest.mark.parametrize("q_len,k_len", [(30, 8192), (8192, 30)])
 def test_fp32_attention_sums_do_not_drift(q_len, k_len):
     """Thousands of terms of one sign: roundings that all go one way would add up in o, or in dv."""
