@@ -119,6 +119,9 @@ int norm_forward(const void* x, const void* residual, const void* weight, void* 
     if ((s = plan_norm(N, C, G, io, 1, false, &pl)) != EQLIN_OK) return s;   // sizes first, without a device
     if (N == 0) return EQLIN_OK;
     if (!x || !y || (out8 && !scale)) return report(EQLIN_ERR_INVALID_ARG, "x, y or scale is NULL");
+    if (y == sum_out) return report(EQLIN_ERR_INVALID_ARG, "y and sum_out are the same tensor");
+    if (out8 && (y == x || y == residual))   // rows of other sizes: one row's output lies over another's input
+        return report(EQLIN_ERR_INVALID_ARG, "the 8-bit output cannot be written over its input");
     if (!aligned(x, 16) || !aligned(y, 16) || !aligned(residual, 16) || !aligned(sum_out, 16) || !aligned(scale, 4) ||
         !aligned(weight, elem_bytes(w_dtype)))
         return report(EQLIN_ERR_MISALIGNED, "x, residual, y and sum_out must be 16-byte aligned");

@@ -54,6 +54,14 @@ def test_norm_fp8_needs_scales():
     assert LIB.eqlin_add_rmsnorm_fp8(256, None, None, 512, 1026, None, 4, 96, 4, 1e-6, BF, BF, None) == MISAL
 
 
+def test_norm_refuses_outputs_over_one_another():
+    sizes = (4, 96, 4, 1e-6, BF, BF, None)
+    assert LIB.eqlin_add_rmsnorm(256, 512, None, 1024, 1024, *sizes) == BAD
+    assert LIB.eqlin_add_rmsnorm_fp8(256, 512, None, 1024, 2048, 1024, *sizes) == BAD
+    for y in (256, 512):
+        assert LIB.eqlin_add_rmsnorm_fp8(256, 512, None, y, 2048, None, *sizes) == BAD
+
+
 def test_norm_backward_workspace():
     n = eq.eqlin_rmsnorm_backward_workspace_size(1000, 96, 4)
     assert n > 0 and n % (96 * 4) == 0
