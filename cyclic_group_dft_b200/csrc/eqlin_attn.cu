@@ -207,8 +207,11 @@ bool f32_small_forward(int64_t rows, int64_t sequences, int64_t heads) {
     return f32_tiles(rows, sequences, heads) < (rows <= 16 * sequences ? kB200Sms : kB200Sms / 4);
 }
 
-// Slices of the keys, where the tiles alone would leave SMs idle: as many as fill them once (fp32: two blocks
-// fit an SM; tiles of 16 rows), but no slice below 256 keys.
+// Slices of the keys, where the tiles alone would leave SMs idle: as many as fill them once, but no slice below 256
+// keys.  fp32: tiles of 16 rows, two blocks to an SM for heads of up to 64 features.  Above, one fits, and twice as many
+// slices run in two waves, which costs as often as it gains, for 148 blocks / 296: 128 features, 48 queries, 2048 keys, 8
+// heads 42 / 53 us; 1 query, 4096 keys, 4 sequences, 8 heads 99 / 96; 64 queries, 8192 keys, 8 heads 190 / 182; 100
+// queries, 1500 keys, 2 sequences, 4 heads 74 / 65.
 int forward_splits(const eqlin_attention_shape& a) {
     const Fwd kind = forward_kind(a);
     const int64_t keys = a.k_rows / a.sequences;

@@ -10,7 +10,8 @@
 //
 // The angle is reduced exactly: a frequency is held in turns as a 64-bit binary fraction F
 // (error below 2^-64 turns), position * F wraps modulo one turn in integer arithmetic, and its
-// top 32 bits give the angle to 2^-32 turns for every 32-bit position.  An fp32 product would
+// top 32 bits, rounded to the 24 of an fp32 number, give the angle within 2^-26 turns for every 32-bit position (half a
+// unit of fp32 just below half a turn).  An fp32 product would
 // lose 2^-24 of the whole angle, which is several percent of a turn at position 10^6.
 //
 // Bound by memory: one read and one write of the features.  A block takes a few tokens,

@@ -470,7 +470,7 @@ EQLIN_API int eqlin_rmsnorm_backward(const void* dy, const void* sum, const void
  *   sections     host, `axes` counts >= 0 that add up to head_channels / 2.
  *   base         finite, >= 1.
  *   inverse      non-zero: turn back (this is also the gradient: dx = inverse rotation of dy).
- * Angles are exact to 2^-32 turns for every position.  N == 0 is a no-op.
+ * Angles are within 2^-26 turns for every position.  N == 0 is a no-op.
  * Errors: INVALID_ARG, UNSUPPORTED (G not in {1, 2, 4, 8, 16}; head_channels odd or above 256),
  * MISALIGNED, CUDA.
  */
@@ -521,7 +521,7 @@ typedef struct {
  * ds are rounded to the I/O type before their products (fp16 gradients: times powers of two that
  * keep the largest of a row or tile in range, so that neither large nor small ones are lost).  fp32
  * I/O: fp32 arithmetic, or products of three tf32 tensor-core products (within 2^-19.6 of each
- * term; an infinite value counts as NaN there).  Statistics are fp32.  No atomics: repeated calls give the same bits.
+ * term; an infinite value, or one of 3.4019e38 and more, counts as NaN there).  Statistics are fp32.  No atomics: repeated calls give the same bits.
  * Rows that no sequence covers (behind the last one) are not read and not written.  A row holding
  * infinities or NaN affects its own sequence only.  Offsets are device data the host cannot
  * check: decreasing or out-of-range ones are clamped (wrong sequences, no access out of bounds).
