@@ -189,6 +189,7 @@ __global__ void __launch_bounds__(kThreads) eqlin_attn_fwd_f32_kernel(const Para
         apply_tile<DP>(sp, sv, ty, tx, acc);
         __syncthreads();
     }
+    cp_async_wait<0>();   // without keys the copy of Q is still on its way
     sum = row_sum(sum);
     const float mul = sum == 0.f ? 0.f : 1.f / sum;   // a row that sees no key
     const float lse = sum == 0.f ? -INFINITY : fmaf(top, kLn2, logf(sum));
@@ -260,6 +261,7 @@ __device__ __forceinline__ void dkv_tile(const Params& p, float* smem, int slot,
         apply_tile<DP>(sds, sq, ty, tx, dk);
         __syncthreads();
     }
+    cp_async_wait<0>();   // without queries those of K and V
     store_rows<DP>(p.dv, p.dv_stride, static_cast<long long>(t.own.start) + r0, n, p.D, hk, ty, tx, dv, 1.f);
     store_rows<DP>(p.dk, p.dk_stride, static_cast<long long>(t.own.start) + r0, n, p.D, hk, ty, tx, dk, p.scale);
 }
@@ -310,6 +312,7 @@ __device__ __forceinline__ void dq_tile(const Params& p, float* smem, int slot, 
         apply_tile<DP>(sds, sk, ty, tx, dq);
         __syncthreads();
     }
+    cp_async_wait<0>();
     store_rows<DP>(p.dq, p.dq_stride, static_cast<long long>(t.own.start) + r0, n, p.D, h, ty, tx, dq, p.scale);
 }
 
